@@ -359,6 +359,210 @@ TSA_API int attend_set(const void* q, const tsa_kv* kv, int B, int Hq, int Hkv, 
                        void* stream);
 
 /* ------------------------------------------------------------------ */
+/* Rotary positions.
+ *
+ * For a head row x and a position t, every pair i < rot_dim/2 of elements is
+ * turned by the angle t * w_i and multiplied by the amplitude:
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin),
+ * (a, b) = (x_i, x_{i + rot_dim/2}) in the half layout and (x_2i, x_{2i+1}) in
+ * the interleaved one; elements from rot_dim on are copied.  The rates are
+ * w_i = theta^(-2i/rot_dim), changed for contexts longer than those a model
+ * was trained on (factor >= 1, orig_len the original context):
+ *   TSA_ROPE_PLAIN     as they are
+ *   TSA_ROPE_LINEAR    w_i / factor
+ *   TSA_ROPE_NTK       theta * factor^(rot_dim / (rot_dim - 2)) for theta
+ *   TSA_ROPE_BY_PARTS  by the turns n_i = orig_len w_i / 2pi over the original
+ *                      context: t = clamp((n_i - low) / (high - low), 0, 1),
+ *                      w_i -> (1 - t) w_i / factor + t w_i (default low 1, high 4)
+ *   TSA_ROPE_YARN      by the pair: lo, hi = floor, ceil of
+ *                      rot_dim ln(orig_len / (2pi beta)) / (2 ln theta) at
+ *                      beta = high and low (default low 1, high 32), clipped to
+ *                      [0, rot_dim - 1]; r = clamp((i - lo) / (hi - lo), 0, 1)
+ *                      (0.001 for hi - lo where they meet),
+ *                      w_i -> r w_i / factor + (1 - r) w_i;
+ *                      amplitude 0.1 ln(factor) + 1 unless given
+ * Angles are taken in 64 bits, so far positions lose nothing. */
+enum { TSA_ROPE_HALF = 0, TSA_ROPE_INTERLEAVED = 1 };
+enum {
+  TSA_ROPE_PLAIN = 0, TSA_ROPE_LINEAR = 1, TSA_ROPE_NTK = 2, TSA_ROPE_BY_PARTS = 3,
+  TSA_ROPE_YARN = 4
+};
+typedef struct tsa_rope_spec {
+  double theta;      /* base, > 1 */
+  double factor;     /* >= 1; only read by the scaled kinds */
+  double low, high;  /* both 0: the kind's defaults */
+  double amplitude;  /* 0: the kind's default (1 but for yarn) */
+  int64_t orig_len;  /* > 0 for TSA_ROPE_BY_PARTS and TSA_ROPE_YARN */
+  int64_t max_pos;   /* positions [0, max_pos) are covered; <= 2^26 */
+  int32_t rot_dim;   /* a multiple of 16, at most 128 */
+  int32_t layout;    /* TSA_ROPE_HALF or TSA_ROPE_INTERLEAVED */
+  int32_t scaling;   /* TSA_ROPE_PLAIN .. TSA_ROPE_YARN */
+} tsa_rope_spec;
+
+/* A table of the spec's angles, caller device memory (16-byte aligned) of
+ * tsa_rope_table_size() bytes.  It holds cos and sin of l w_i for l < 2048 and
+ * of 2048 h w_i, and the kernels add the two angles: 1 MiB for rot_dim 128 and a
+ * million positions, which stays in L2, where a row per position would be
+ * 512 MiB. */
+typedef struct tsa_rope {
+  const void* table;
+  int64_t max_pos;
+  int32_t rot_dim;
+  int32_t layout;
+} tsa_rope;
+
+/* Bytes of the table (0 for sizes that tsa_rope_table refuses). */
+TSA_API size_t tsa_rope_table_size(int rot_dim, int64_t max_pos);
+/* Fills `table` (one kernel on `stream`) and *rope, which names it. */
+TSA_API int tsa_rope_table(const tsa_rope_spec* spec, void* table, size_t bytes,
+                           tsa_rope* rope, void* stream);
+
+/* Rows of T tokens and H heads: element (t, h, j) at data + t*stride_t +
+ * h*stride_h + j (bf16; strides in elements, multiples of 8; data 16-byte
+ * aligned), so that a slice of a fused projection is taken as it is.  Rows that
+ * are written must not overlap one another. */
+typedef struct tsa_rows {
+  void* data;
+  int64_t stride_t;
+  int64_t stride_h;
+} tsa_rows;
+
+/* rope_apply -- rotates the q rows [T][Hq] and the k rows [T][Hkv] of T tokens.
+ *
+ * positions: int32 [T] (device).  inverse != 0 turns by the opposite angle (the
+ * amplitude stays), which is the gradient of the forward rotation and, with
+ * amplitude 1, its inverse.  k and k_out may be NULL with Hkv = 0.  An output may
+ * be its input (same data and strides); other overlaps are not allowed.  A
+ * position outside [0, max_pos) gives NaN in the row's first rot_dim elements.
+ * Each output is rounded once, from 32 bits. */
+TSA_API int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
+                       const tsa_rows* k_out, int Hkv, int64_t T, int d,
+                       const int32_t* positions, const tsa_rope* rope, int inverse,
+                       void* stream);
+
+/* ------------------------------------------------------------------ */
+/* 8-bit KV cache: keys and values in one byte an element, with one scale for
+ * each block of `block` consecutive positions and KV head (K and V apart).
+ *
+ * Geometry as tsa_kv, one byte an element:
+ *   contiguous  k, v: [B][Hkv][l_cap][128]; scales fp32 [B][Hkv][l_cap/block]
+ *   paged       k, v: [n_pages][Hkv][page_size][128] through page_table int32
+ *               [B][max_pages]; scales fp32 [n_pages][Hkv][page_size/block]
+ * block: 16, 32, 64 or 128, dividing l_cap (contiguous) or page_size (paged).
+ * A value is scale * code:
+ *   TSA_KV8_INT8  whole numbers in [-127, 127], stored as the byte code + 128
+ *   TSA_KV8_E4M3  8-bit floats (4 exponent and 3 mantissa bits, no infinities)
+ * A scale is a power of two, the smallest 2^e with 127 * 2^e (int8) or 448 *
+ * 2^e (e4m3) at or above the block's largest finite magnitude, e >= -60.  Powers
+ * of two make every division here exact: a code is the value rounded once (to
+ * nearest, ties to even), and every stored value is exact in bf16.
+ * Codes are 16-byte aligned.  status: NULL, or one 256-byte aligned device int
+ * that kernels flag bad lengths, pages and positions in (sticky; read and clear
+ * it with tsa_workspace_status). */
+enum { TSA_KV8_INT8 = 0, TSA_KV8_E4M3 = 1 };
+typedef struct tsa_kv8 {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int32_t* status;
+  int64_t l_cap;
+  int32_t page_size;
+  int32_t max_pages;
+  int32_t n_pages;   /* pages of the pool (paged only) */
+  int32_t block;
+  int32_t format;
+} tsa_kv8;
+
+/* kv8_append -- writes new tokens' K and V into the cache.
+ *
+ * k_new, v_new: bf16 rows [T][Hkv]; sequence b's are tokens [cu_new[b],
+ * cu_new[b+1]) (int32 [B+1], device), or, with cu_new NULL, [b*max_new,
+ * (b+1)*max_new).  max_new: the most new tokens of a sequence (a sequence with
+ * more is flagged and nothing of it is written).  lens: int32 [B] (device), the
+ * lengths after the call: the n_b tokens go to positions [lens[b] - n_b, lens[b]).
+ * rope: NULL, or the rotation of the keys, applied in 32 bits on the way (one
+ * rounding in all); positions: int32 [T] (device) or NULL for the cache's own.
+ * Blocks that begin with a new token take their scale from the new rows.  The
+ * block that older rows share takes the larger of its scale and the new rows',
+ * and where it grows the older rows' codes are rounded again to it.  Rows from
+ * lens[b] on are left as they were.  Infinities are stored as the largest code,
+ * NaN as 0 (int8) or NaN (e4m3).  A sequence with lens[b] outside [n_b, l_cap], or rows
+ * on a page outside [0, n_pages), are not written, and flagged.  Sequences of one
+ * call must not share the pages that they write. */
+TSA_API int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
+                       const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens, int B,
+                       int Hkv, int d, const tsa_rope* rope, const int32_t* positions,
+                       void* stream);
+
+/* kv8_read -- the last n_b positions of every sequence, back in bf16 (exact).
+ *
+ * Row counts and places as in kv8_append: token cu[b] + j of k_out and v_out
+ * (bf16 rows [T][Hkv]) is position lens[b] - n_b + j.  Positions below 0 give
+ * rows of zeros; lens[b] outside [0, l_cap] or a page outside [0, n_pages) gives
+ * NaN, and is flagged.  Rows of a sequence past max_new are left as they were. */
+TSA_API int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows* v_out,
+                     const int32_t* cu, int64_t T, int max_new, const int32_t* lens, int B,
+                     int Hkv, int d, void* stream);
+
+/* ------------------------------------------------------------------ */
+/* Attention with a sliding window and sinks, and attention over the 8-bit
+ * cache.  A query at position p sees the positions j <= p with j < n_init (the
+ * sinks) or j > p - n_recent (the window): the static W of sparse_attn_decode.
+ * n_recent >= p + 1 sees everything before it.  Rows that no query of the call
+ * sees are not used, whatever they hold, and pages that hold no visible row are
+ * not looked up.  Rows that some query of a sequence sees must be finite.
+ *
+ * kv8_attn_decode / window_attn_decode: one step, the query of sequence b at
+ * position lens[b] - 1.
+ *   q: bf16 [B][Hq][128]; lens: int32 [B] (device);
+ *   out: fp32 [B][Hq][128] = softmax(scale q.k) . v over the visible rows;
+ *   lse_out: fp32 [B][Hq] or NULL (log sum e^z): (out, lse) is a partial that
+ *     lse_merge takes.  No visible row: out 0, lse -inf.
+ *   Products and sums are as those of 32-bit arithmetic: codes, keys and
+ *   queries enter the tensor cores exactly, the softmax weights in two parts.
+ *   Limits: Hq / Hkv <= 8, B <= 4096, Hkv <= 1024, B * Hq <= 65535.
+ *   workspace: tsa_attn_decode_workspace_size() bytes, 256-byte aligned,
+ *   zero-filled before its first use; calls leave it ready for any call that it
+ *   is large enough for (of either entry point).
+ * Device-detected errors (tsa_workspace_status on the workspace): a lens[b]
+ * outside [0, l_cap] is clamped and flagged; a visible row on a page outside
+ * [0, n_pages) (kv8), or on a negative page (tsa_kv), makes the sequence's out and
+ * lse NaN and is flagged. */
+TSA_API size_t tsa_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
+TSA_API int kv8_attn_decode(const void* q, const tsa_kv8* cache, const int32_t* lens, int B,
+                            int Hq, int Hkv, int d, int64_t n_init, int64_t n_recent,
+                            float scale, float* out, float* lse_out, void* workspace,
+                            size_t ws_bytes, void* stream);
+TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int B,
+                               int Hq, int Hkv, int d, int64_t n_init, int64_t n_recent,
+                               float scale, float* out, float* lse_out, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/* window_attn_prefill -- the same for many new tokens per sequence, over a
+ * bf16 cache that holds them already (prompts, chunks of prompts).
+ *
+ * q: bf16 rows [T][Hq]; sequence b's are tokens [cu_q[b], cu_q[b+1]) (int32
+ * [B+1], device), or [b*max_q, (b+1)*max_q) with cu_q NULL; token j of n_b has
+ * position lens[b] - n_b + j (below 0: it sees nothing).  max_q: the most tokens
+ * of a sequence (a sequence with more is flagged, its outputs NaN up to max_q).
+ * out: bf16 [T][Hq][128], rounded once from 32-bit sums (the softmax weights
+ * enter the products in bf16); lse_out: fp32 [T][Hq] or NULL.  Rows from cu_q[B]
+ * on are left as they were.
+ * workspace: window_attn_prefill_workspace_size() bytes (from the same max_q,
+ * l_cap and window), 256-byte aligned, zero-filled before its first use.
+ * Limits: Hq / Hkv <= 8, B <= 4096, B * Hkv <= 65535. */
+TSA_API size_t window_attn_prefill_workspace_size(int B, int Hq, int Hkv, int d, int max_q,
+                                                  int64_t l_cap, int64_t n_init,
+                                                  int64_t n_recent);
+TSA_API int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q,
+                                int64_t T, int max_q, const int32_t* lens, int B, int Hq,
+                                int Hkv, int d, int64_t n_init, int64_t n_recent, float scale,
+                                void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/* ------------------------------------------------------------------ */
 /* lse_merge -- [RA] Eq. 4-5 on precomputed partials.
  *
  * For each row r < rows, merges two attention partials over disjoint key

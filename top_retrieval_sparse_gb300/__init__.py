@@ -24,7 +24,9 @@ __all__ = [
     "TsaError", "lib", "KV", "kv_contiguous", "kv_paged", "decode_workspace_size",
     "sparse_attn_decode", "lse_merge", "ReTopK", "library_path", "set_stage_events",
     "set_trace", "read_trace", "kernel_launches", "sparse_attn_decode_noalloc",
-    "noalloc_scratch_bytes",
+    "noalloc_scratch_bytes", "RopeTable", "rope", "KV8", "kv8_append", "kv8_read",
+    "attn_decode_workspace", "kv8_attn_decode", "window_attn_decode",
+    "window_attn_prefill_workspace", "window_attn_prefill",
 ]
 
 TSA_OK = 0
@@ -41,6 +43,29 @@ class TsaError(RuntimeError):
 class _KvStruct(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_table", C.c_void_p),
                 ("page_size", C.c_int32), ("max_pages", C.c_int32), ("l_cap", C.c_int64)]
+
+
+class _RopeSpec(C.Structure):
+    _fields_ = [("theta", C.c_double), ("factor", C.c_double), ("low", C.c_double),
+                ("high", C.c_double), ("amplitude", C.c_double), ("orig_len", C.c_int64),
+                ("max_pos", C.c_int64), ("rot_dim", C.c_int32), ("layout", C.c_int32),
+                ("scaling", C.c_int32)]
+
+
+class _RopeStruct(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("max_pos", C.c_int64), ("rot_dim", C.c_int32),
+                ("layout", C.c_int32)]
+
+
+class _RowsStruct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
+
+
+class _Kv8Struct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("page_table", C.c_void_p), ("status", C.c_void_p),
+                ("l_cap", C.c_int64), ("page_size", C.c_int32), ("max_pages", C.c_int32),
+                ("n_pages", C.c_int32), ("block", C.c_int32), ("format", C.c_int32)]
 
 
 _lock = threading.Lock()
@@ -102,6 +127,21 @@ def lib():
             L.tsa_decode_q8_workspace_size.restype = sz
             L.sparse_attn_decode_q8.argtypes = [P, P, P, i32, P, i32, i32, i32, i32, i32, i32,
                                                 i32, f32, P, P, P, P, P, sz, P]
+            L.tsa_rope_table_size.argtypes = [i32, i64]
+            L.tsa_rope_table_size.restype = sz
+            L.tsa_rope_table.argtypes = [P, P, sz, P, P]
+            L.rope_apply.argtypes = [P, P, i32, P, P, i32, i64, i32, P, P, i32, P]
+            L.kv8_append.argtypes = [P, P, P, P, i64, i32, P, i32, i32, i32, P, P, P]
+            L.kv8_read.argtypes = [P, P, P, P, i64, i32, P, i32, i32, i32, P]
+            L.tsa_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32]
+            L.tsa_attn_decode_workspace_size.restype = sz
+            for fn in (L.kv8_attn_decode, L.window_attn_decode):
+                fn.argtypes = [P, P, P, i32, i32, i32, i32, i64, i64, f32, P, P, P, sz, P]
+            L.window_attn_prefill_workspace_size.argtypes = [i32, i32, i32, i32, i32, i64, i64,
+                                                             i64]
+            L.window_attn_prefill_workspace_size.restype = sz
+            L.window_attn_prefill.argtypes = [P, P, P, i64, i32, P, i32, i32, i32, i32, i64, i64,
+                                              f32, P, P, P, sz, P]
             _lib = L
     return _lib
 
@@ -502,3 +542,360 @@ class ReTopK:
 
     def set_counters(self, t: int, fifo_head: int) -> None:
         _check(lib().retopk_set_counters(self.handle, t, fifo_head))
+
+
+# --------------------------------------------- cache-side operators
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_KV8_FORMAT = {"int8": 0, "e4m3": 1}
+
+
+def _gpu(*named) -> torch.device:
+    """The one CUDA device that the given (tensor, name) pairs live on."""
+    dev = None
+    for t, name in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return dev
+
+
+def _run_on(dev: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream) with dev current; stream None: dev's current one."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(stream)))
+
+
+def _new(stream, dev: torch.device, shape, dtype, zero: bool = False) -> torch.Tensor:
+    """A tensor made on the stream that the call runs on."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
+def _rows(t: torch.Tensor, name: str) -> _RowsStruct:
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens][heads][128] with contiguous rows")
+    return _RowsStruct(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _offsets(cu, T: int, max_n, B: int, what: str) -> int:
+    """The most tokens of a sequence (max_n, or T / B without offsets)."""
+    if cu is None:
+        if B and T % B:
+            raise ValueError(f"{T} tokens do not divide over {B} sequences: pass offsets")
+        if max_n is not None and max_n * B != T:
+            raise ValueError(f"{what} = {max_n}: {T} tokens of {B} sequences without offsets")
+        return T // B if B else 0
+    _want(cu, torch.int32, "offsets")
+    if cu.shape != (B + 1,):
+        raise ValueError(f"offsets must be int32 [{B + 1}], got {tuple(cu.shape)}")
+    if max_n is None:
+        raise ValueError(f"{what} is needed with offsets")
+    return int(max_n)
+
+
+class RopeTable:
+    """The angles of a rotary embedding on the device (tsa_rope_table).
+
+    layout: "half" (pairs i, i + rot_dim/2) or "interleaved" (2i, 2i + 1);
+    scaling: "none", "linear", "ntk", "by_parts" or "yarn" (see include/tsa.h)
+    with `factor` and `orig_len`; low, high and amplitude default to the kind's.
+    """
+
+    def __init__(self, rot_dim: int, max_pos: int, theta: float = 10000.0, layout: str = "half",
+                 scaling: Optional[str] = None, factor: float = 1.0, orig_len: int = 0,
+                 low: float = 0.0, high: float = 0.0, amplitude: float = 0.0, device="cuda",
+                 stream=None):
+        if layout not in _ROPE_LAYOUT:
+            raise ValueError(f"layout {layout!r}: one of {sorted(_ROPE_LAYOUT)}")
+        if (scaling or "none") not in _ROPE_SCALING:
+            raise ValueError(f"scaling {scaling!r}: one of {sorted(_ROPE_SCALING)}")
+        n = int(lib().tsa_rope_table_size(int(rot_dim), int(max_pos)))
+        if n == 0:
+            raise TsaError(-1, f"invalid rotation sizes (rot_dim {rot_dim}, max_pos {max_pos})")
+        spec = _RopeSpec(theta, factor, low, high, amplitude, int(orig_len), int(max_pos),
+                         int(rot_dim), _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling or "none"])
+        self.rot_dim, self.max_pos, self.layout = int(rot_dim), int(max_pos), layout
+        self.struct = _RopeStruct()
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.table = _new(stream, dev, (n,), torch.uint8)
+        _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table, C.byref(spec),
+                _p(self.table), n, C.byref(self.struct))
+
+
+def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
+         k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, inverse: bool = False, stream=None):
+    """Rotates q bf16 [T][Hq][128] (and k [T][Hkv][128]) by positions int32 [T].
+
+    Rows may be strided (a slice of a fused projection); q_out=q rotates in
+    place.  Returns (q_out, k_out)."""
+    dev = _gpu((q, "q"), (positions, "positions"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"),
+               (table.table, "table"))
+    _want(positions, torch.int32, "positions")
+    T, Hq, d = q.shape
+    if positions.shape != (T,):
+        raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
+    if q_out is None:
+        q_out = _new(stream, dev, q.shape, torch.bfloat16)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    Hkv, ks, kos = 0, None, None
+    if k is not None:
+        if k_out is None:
+            k_out = _new(stream, dev, k.shape, torch.bfloat16)
+        if k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("k and k_out must be [tokens][heads][128] with q's tokens")
+        Hkv, ks, kos = k.shape[1], C.byref(_rows(k, "k")), C.byref(_rows(k_out, "k_out"))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _run_on(dev, stream, lib().rope_apply, C.byref(_rows(q, "q")), C.byref(_rows(q_out, "q_out")),
+            Hq, ks, kos, Hkv, T, d, _p(positions), C.byref(table.struct), 1 if inverse else 0)
+    return q_out, k_out
+
+
+class KV8:
+    """An 8-bit KV cache as the library sees it (tsa_kv8 in include/tsa.h).
+
+    k, v: uint8 codes [B][Hkv][l_cap][128], or [pages][Hkv][page_size][128]
+    with page_table int32 [B][max_pages]; k_scale, v_scale: fp32 with one
+    entry per block of rows, [...][Hkv][rows / block].  status: optional int32
+    word (256-byte aligned) for workspace_status."""
+
+    def __init__(self, k, v, k_scale, v_scale, fmt: str = "int8", page_table=None, status=None):
+        if fmt not in _KV8_FORMAT:
+            raise ValueError(f"fmt {fmt!r}: one of {sorted(_KV8_FORMAT)}")
+        for t, name in ((k, "k"), (v, "v")):
+            _want(t, torch.uint8, name)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _want(t, torch.float32, name)
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must have one shape [B or pages][Hkv][rows][128]")
+        n, self.Hkv, rows, self.d = k.shape
+        if k_scale.shape != v_scale.shape or k_scale.dim() != 3 or \
+                k_scale.shape[:2] != k.shape[:2] or not k_scale.shape[2] or \
+                rows % k_scale.shape[2]:
+            raise ValueError("scales must be [B or pages][Hkv][rows / block]")
+        self.device = _gpu((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                           (page_table, "page_table"), (status, "status"))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.status, self.fmt = page_table, status, fmt
+        self.block = rows // k_scale.shape[2]
+        if page_table is None:
+            self.B, self.l_cap, ps, mp, n_pages = n, rows, 0, 0, 0
+        else:
+            _want(page_table, torch.int32, "page_table")
+            self.B, mp = page_table.shape
+            self.l_cap, ps, n_pages = mp * rows, rows, n
+        if status is not None:
+            _want(status, torch.int32, "status")
+        self.struct = _Kv8Struct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            None if page_table is None else page_table.data_ptr(),
+            None if status is None else status.data_ptr(), self.l_cap, ps, mp, n_pages,
+            self.block, _KV8_FORMAT[fmt])
+        self._ref = C.byref(self.struct)
+
+    @classmethod
+    def contiguous(cls, B: int, Hkv: int, l_cap: int, block: int = 64, fmt: str = "int8",
+                   device="cuda") -> "KV8":
+        """A zeroed contiguous cache with a status word."""
+        return cls._made(B, Hkv, l_cap, block, fmt, None, device)
+
+    @classmethod
+    def paged(cls, pages: int, Hkv: int, page_size: int, page_table: torch.Tensor,
+              block: int = 16, fmt: str = "int8") -> "KV8":
+        """A zeroed pool of pages with a status word."""
+        return cls._made(pages, Hkv, page_size, block, fmt, page_table, page_table.device)
+
+    @classmethod
+    def _made(cls, n, Hkv, rows, block, fmt, page_table, device):
+        if rows % block:
+            raise ValueError(f"block {block} does not divide {rows} rows")
+        code = [torch.zeros((n, Hkv, rows, 128), dtype=torch.uint8, device=device)
+                for _ in range(2)]
+        scale = [torch.zeros((n, Hkv, rows // block), dtype=torch.float32, device=device)
+                 for _ in range(2)]
+        status = torch.zeros(64, dtype=torch.int32, device=device)
+        return cls(*code, *scale, fmt=fmt, page_table=page_table, status=status)
+
+
+def _cache_batch(cache, lens: torch.Tensor) -> int:
+    _want(lens, torch.int32, "lens")
+    B = lens.shape[0]
+    if lens.dim() != 1 or B > cache.B:
+        raise ValueError(f"lens must be int32 [B] with B <= {cache.B}, the cache's sequences")
+    return B
+
+
+def kv8_append(cache: KV8, k_new: torch.Tensor, v_new: torch.Tensor, lens: torch.Tensor,
+               cu_new: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+               rope: Optional[RopeTable] = None, positions: Optional[torch.Tensor] = None,
+               stream=None) -> KV8:
+    """Writes new tokens' rows (bf16 [T][Hkv][128], strided allowed) at the
+    last positions before lens[b], quantised, the keys rotated if `rope` is
+    given (at positions int32 [T], or their own).  Ragged with cu_new int32
+    [B+1] and max_new, else T / B tokens a sequence."""
+    B = _cache_batch(cache, lens)
+    dev = _gpu((cache.k, "cache"), (k_new, "k_new"), (v_new, "v_new"), (lens, "lens"),
+               (cu_new, "cu_new"), (positions, "positions"), (rope.table if rope else None, "rope"))
+    T = k_new.shape[0]
+    if k_new.shape != (T, cache.Hkv, cache.d) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must be [T][{cache.Hkv}][{cache.d}]")
+    if positions is not None:
+        _want(positions, torch.int32, "positions")
+        if positions.shape != (T,):
+            raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
+    n = _offsets(cu_new, T, max_new, B, "max_new")
+    _run_on(dev, stream, lib().kv8_append, cache._ref, C.byref(_rows(k_new, "k_new")),
+            C.byref(_rows(v_new, "v_new")), _p(cu_new), T, n, _p(lens), B, cache.Hkv, cache.d,
+            C.byref(rope.struct) if rope else None, _p(positions))
+    return cache
+
+
+def kv8_read(cache: KV8, lens: torch.Tensor, n: Optional[int] = None,
+             cu: Optional[torch.Tensor] = None, T: Optional[int] = None,
+             k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+             stream=None):
+    """The last rows before lens[b] back in bf16: n of every sequence, or
+    cu[b+1] - cu[b] <= n of sequence b (T tokens in all, known to the host).
+    Returns (k_out, v_out), [T][Hkv][128]."""
+    B = _cache_batch(cache, lens)
+    if n is None or (cu is not None and T is None and k_out is None):
+        raise ValueError("pass n, and T (or k_out and v_out) with offsets")
+    if T is None:
+        T = B * n if cu is None else k_out.shape[0]
+    dev = _gpu((cache.k, "cache"), (lens, "lens"), (cu, "cu"), (k_out, "k_out"), (v_out, "v_out"))
+    shape = (T, cache.Hkv, cache.d)
+    if k_out is None:
+        k_out = _new(stream, dev, shape, torch.bfloat16)
+    if v_out is None:
+        v_out = _new(stream, dev, shape, torch.bfloat16)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"k_out and v_out must be {list(shape)}")
+    n = _offsets(cu, T, n, B, "n")
+    _run_on(dev, stream, lib().kv8_read, cache._ref, C.byref(_rows(k_out, "k_out")),
+            C.byref(_rows(v_out, "v_out")), _p(cu), T, n, _p(lens), B, cache.Hkv, cache.d)
+    return k_out, v_out
+
+
+def attn_decode_workspace(B: int, Hq: int, Hkv: int, d: int = 128, device="cuda") -> torch.Tensor:
+    """A zeroed workspace of kv8_attn_decode and window_attn_decode."""
+    n = int(lib().tsa_attn_decode_workspace_size(B, Hq, Hkv, d))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _attn_decode(fn, ref, q, cache, lens, n_init, n_recent, scale, out, lse_out, workspace,
+                 stream):
+    B = _cache_batch(cache, lens)
+    _want(q, torch.bfloat16, "q")
+    Bq, Hq, d = q.shape
+    if Bq != B:
+        raise ValueError(f"q has {Bq} sequences, lens {B}")
+    dev = _gpu((q, "q"), (cache.k, "cache"), (lens, "lens"), (out, "out"), (lse_out, "lse_out"),
+               (workspace, "workspace"))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _new(stream, dev, (B, Hq, d), torch.float32)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    else:
+        _want(out, torch.float32, "out")
+    if lse_out is not None:
+        _want(lse_out, torch.float32, "lse_out")
+        if lse_out.shape != (B, Hq):
+            raise ValueError(f"lse_out must be fp32 [{B}][{Hq}]")
+    if workspace is None:
+        n = int(lib().tsa_attn_decode_workspace_size(B, Hq, cache.Hkv, d))
+        workspace = _new(stream, dev, (max(n, 256),), torch.uint8, zero=True)
+    _run_on(dev, stream, fn, _p(q), ref, _p(lens), B, Hq, cache.Hkv, d, int(n_init),
+            cache.l_cap if n_recent is None else int(n_recent), float(scale), _p(out),
+            _p(lse_out), _p(workspace), workspace.numel() * workspace.element_size())
+    return out, lse_out
+
+
+def kv8_attn_decode(q: torch.Tensor, cache: KV8, lens: torch.Tensor, n_init: int = 0,
+                    n_recent: Optional[int] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """One decode step of attention over the 8-bit cache: q bf16 [B][Hq][128],
+    all rows (n_recent None) or the sinks and the window.  Returns (out fp32
+    [B][Hq][128], lse_out)."""
+    return _attn_decode(lib().kv8_attn_decode, cache._ref, q, cache, lens, n_init, n_recent,
+                        scale, out, lse_out, workspace, stream)
+
+
+def window_attn_decode(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int,
+                       n_recent: Optional[int], scale: Optional[float] = None,
+                       out: Optional[torch.Tensor] = None,
+                       lse_out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """One decode step over a bf16 cache, the first n_init and the last
+    n_recent rows visible (None: all).  Returns (out fp32, lse_out), a partial
+    that lse_merge takes."""
+    return _attn_decode(lib().window_attn_decode, C.byref(kv.struct), q, kv, lens, n_init,
+                        n_recent, scale, out, lse_out, workspace, stream)
+
+
+def window_attn_prefill_workspace(B: int, Hq: int, Hkv: int, max_q: int, l_cap: int, n_init: int,
+                                  n_recent: Optional[int], d: int = 128,
+                                  device="cuda") -> torch.Tensor:
+    """A zeroed workspace of window_attn_prefill for these sizes."""
+    n = int(lib().window_attn_prefill_workspace_size(
+        B, Hq, Hkv, d, max_q, l_cap, n_init, l_cap if n_recent is None else n_recent))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def window_attn_prefill(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int,
+                        n_recent: Optional[int], cu_q: Optional[torch.Tensor] = None,
+                        max_q: Optional[int] = None, scale: Optional[float] = None,
+                        out: Optional[torch.Tensor] = None,
+                        lse_out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Many new tokens per sequence over a bf16 cache that holds them: q bf16
+    [T][Hq][128] (strided allowed), ragged with cu_q int32 [B+1] and max_q, else
+    T / B tokens a sequence.  Returns (out bf16 [T][Hq][128], lse_out)."""
+    B = _cache_batch(kv, lens)
+    T, Hq, d = q.shape
+    dev = _gpu((q, "q"), (kv.k, "kv"), (lens, "lens"), (cu_q, "cu_q"), (out, "out"),
+               (lse_out, "lse_out"), (workspace, "workspace"))
+    n = _offsets(cu_q, T, max_q, B, "max_q")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _new(stream, dev, (T, Hq, d), torch.bfloat16)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    else:
+        _want(out, torch.bfloat16, "out")
+    if lse_out is not None:
+        _want(lse_out, torch.float32, "lse_out")
+        if lse_out.shape != (T, Hq):
+            raise ValueError(f"lse_out must be fp32 [{T}][{Hq}]")
+    nr = kv.l_cap if n_recent is None else int(n_recent)
+    if workspace is None:
+        nb = int(lib().window_attn_prefill_workspace_size(B, Hq, kv.Hkv, d, n, kv.l_cap,
+                                                          int(n_init), nr))
+        workspace = _new(stream, dev, (max(nb, 256),), torch.uint8, zero=True)
+    _run_on(dev, stream, lib().window_attn_prefill, C.byref(_rows(q, "q")), C.byref(kv.struct),
+            _p(cu_q), T, n, _p(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale), _p(out),
+            _p(lse_out), _p(workspace), workspace.numel() * workspace.element_size())
+    return out, lse_out

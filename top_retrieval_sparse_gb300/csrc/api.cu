@@ -277,6 +277,11 @@ int validate_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int B,
                     const float* out) {
   return check_decode(q, kv, lens, B, Hq, Hkv, d, K, n_init, n_recent, scale, out);
 }
+// The same for an entry point elsewhere that succeeded, the host checks of a
+// bf16 cache, and the count of launches.
+int report_ok() { return ok(); }
+int validate_kv(const tsa_kv* kv) { return check_kv(kv, 0, 0); }
+cudaError_t count_launch(cudaError_t e) { return counted(e); }
 // Bytes at the start of a decode workspace that must be zero before a call.
 size_t decode_zero_bytes(int B, int Hq, int Hkv, int64_t l_cap, int K, int n_init, int n_recent) {
   (void)K;
