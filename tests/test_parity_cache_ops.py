@@ -402,7 +402,18 @@ def seen_of(p, W, ni, nr):
     return (j <= p) & ((j < ni) | (j > p - nr))
 
 
-def decode_close(out, lse, ref, rlse, pv, zabs, n):
+def small_weights(q, k, v, seen, scale, steps):
+    """What weights too small for fp16 can change: the 8-bit path's weights
+    carry their row's value scale s_i, and are rounded to at least 2^-25 where
+    the largest of them is at least 2^7 (each warp's own largest, at most the
+    row's).  So out is off by at most 2^-32 max_j(p_j s_j) sum_i |v_i| / s_i."""
+    z = torch.where(seen, q.double() @ k.double().T * scale, -math.inf)
+    p = torch.softmax(z, dim=1).nan_to_num(0.0)
+    return 2.0 ** -32 * (p * steps).amax(dim=1, keepdim=True) * \
+        (seen.double() @ (v.double().abs() / steps[:, None]))
+
+
+def decode_close(out, lse, ref, rlse, pv, zabs, n, extra=0.0):
     # Logit: 128 exact products added in 32 bits with truncating adds: within
     # 2^-20 of their magnitudes' sum (16 steps of 2^-23, and a factor 2 on top).
     # exp: 2^-21 with its argument's rounding (2^-24 of |z| log2 e, covered by
@@ -410,7 +421,7 @@ def decode_close(out, lse, ref, rlse, pv, zabs, n):
     # bits, 16 a step, truncating: n/16 * 2^-23 at most.  Twice, for the
     # numerator and the denominator.
     eps = 2 * (zabs * 2.0 ** -19 + 2.0 ** -17 + 2.0 ** -20 + n * 2.0 ** -27)
-    bad = (out.double() - ref).abs() > pv * eps[:, None] + 1e-30
+    bad = (out.double() - ref).abs() > pv * eps[:, None] + extra + 1e-30
     assert not bad.any(), float(((out.double() - ref).abs() / pv.clamp(min=1e-30)).max())
     empty = rlse.isinf()
     assert torch.equal(lse.isinf(), empty) and (out[empty] == 0).all()
@@ -470,7 +481,16 @@ def test_window_attn_decode(tsa, case):
     assert torch.equal(out, tsa.window_attn_decode(q, kv, i32(lens), ni, nr)[0])
 
 
-def check_decode(q, rows, lens, Hkv, ni, nr, out, lse, scale=1 / math.sqrt(D)):
+def value_steps(cache, b, h):
+    """The value scale of every row of a sequence and KV head."""
+    if cache.page_table is None:
+        s = cache.v_scale[b, h]
+    else:
+        s = cache.v_scale[cache.page_table[b].long(), h].reshape(-1)
+    return s.double().repeat_interleave(cache.block)
+
+
+def check_decode(q, rows, lens, Hkv, ni, nr, out, lse, scale=1 / math.sqrt(D), steps=None):
     G = q.shape[1] // Hkv
     for b, L in enumerate(lens):
         seen = seen_of([L - 1], L, ni, nr)
@@ -478,7 +498,9 @@ def check_decode(q, rows, lens, Hkv, ni, nr, out, lse, scale=1 / math.sqrt(D)):
             k, v = rows(b, h)
             at = slice(h * G, h * G + G)
             r = attend64(q[b, at], k[:L], v[:L], seen.expand(G, L), scale)
-            decode_close(out[b, at], lse[b, at], *r, n=L)
+            extra = 0.0 if steps is None or L == 0 else small_weights(
+                q[b, at], k[:L], v[:L], seen.expand(G, L), scale, steps(b, h)[:L])
+            decode_close(out[b, at], lse[b, at], *r, n=L, extra=extra)
 
 
 @pytest.mark.parametrize("fmt,block", [("int8", 16), ("int8", 128), ("e4m3", 64), ("e4m3", 32)])
@@ -495,7 +517,8 @@ def test_kv8_attn_decode(tsa, case, fmt, block):
     ws = tsa.attn_decode_workspace(B, Hq, Hkv)
     out, _ = tsa.kv8_attn_decode(q, cache, i32(lens), ni, nr, lse_out=lse, workspace=ws)
     check_decode(q, lambda b, h: (rows(0, b, h), rows(1, b, h)), lens, Hkv, ni,
-                 cap if nr is None else nr, out, lse)
+                 cap if nr is None else nr, out, lse,
+                 steps=lambda b, h: value_steps(cache, b, h))
     assert tsa.workspace_status(ws) == 0
     again, _ = tsa.kv8_attn_decode(q, cache, i32(lens), ni, nr, workspace=ws)
     assert torch.equal(out, again)
@@ -525,11 +548,13 @@ def test_decode_logits_and_scales_over_a_wide_range(tsa):
     q = (q / 30).bfloat16()
     for lens in ([512, 511], [64, 65], [128, 128]):
         out, _ = tsa.kv8_attn_decode(q, cache, i32(lens), lse_out=lse)
-        check_decode(q, lambda b, h: (val[0][b, h], val[1][b, h]), lens, Hkv, 0, cap, out, lse)
+        check_decode(q, lambda b, h: (val[0][b, h], val[1][b, h]), lens, Hkv, 0, cap, out, lse,
+                     steps=lambda b, h: value_steps(cache, b, h))
     # a window over the block of zeros alone
     out, _ = tsa.kv8_attn_decode(q, cache, i32([128, 128]), 0, 64, lse_out=lse)
     assert (out[0] == 0).all()
-    check_decode(q, lambda b, h: (val[0][b, h], val[1][b, h]), [128, 128], Hkv, 0, 64, out, lse)
+    check_decode(q, lambda b, h: (val[0][b, h], val[1][b, h]), [128, 128], Hkv, 0, 64, out, lse,
+                 steps=lambda b, h: value_steps(cache, b, h))
 
 
 def test_invisible_rows_and_pages_do_not_matter(tsa):

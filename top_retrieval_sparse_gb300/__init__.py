@@ -556,22 +556,35 @@ def _gpu(*named) -> torch.device:
     for t, name in named:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+        d = t.device
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+            if d.type != "cuda":
+                raise ValueError(f"{name} must be a CUDA tensor")
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on {d}, not on {dev}: it must be a CUDA tensor there")
     return dev
 
 
 def _run_on(dev: torch.device, stream, fn, *args) -> None:
-    """fn(*args, stream) with dev current; stream None: dev's current one."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream(stream)))
+    """fn(*args, stream) with dev current; stream None: dev's current one
+    (its raw handle: torch.cuda.current_stream() costs several microseconds)."""
+    i = dev.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(i)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if i == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != TSA_OK:
+        _check(rc)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _new(stream, dev: torch.device, shape, dtype, zero: bool = False) -> torch.Tensor:
@@ -588,9 +601,10 @@ def _new(stream, dev: torch.device, shape, dtype, zero: bool = False) -> torch.T
 def _rows(t: torch.Tensor, name: str) -> _RowsStruct:
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.stride(2) != 1:
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1:
         raise ValueError(f"{name} must be [tokens][heads][128] with contiguous rows")
-    return _RowsStruct(t.data_ptr(), t.stride(0), t.stride(1))
+    return _RowsStruct(t.data_ptr(), st[0], st[1])
 
 
 def _offsets(cu, T: int, max_n, B: int, what: str) -> int:
@@ -632,12 +646,13 @@ class RopeTable:
                          int(rot_dim), _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling or "none"])
         self.rot_dim, self.max_pos, self.layout = int(rot_dim), int(max_pos), layout
         self.struct = _RopeStruct()
+        self._ref = C.byref(self.struct)
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.table = _new(stream, dev, (n,), torch.uint8)
         _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table, C.byref(spec),
-                _p(self.table), n, C.byref(self.struct))
+                _ptr(self.table), n, self._ref)
 
 
 def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
@@ -667,7 +682,7 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
     elif k_out is not None:
         raise ValueError("k_out without k")
     _run_on(dev, stream, lib().rope_apply, C.byref(_rows(q, "q")), C.byref(_rows(q_out, "q_out")),
-            Hq, ks, kos, Hkv, T, d, _p(positions), C.byref(table.struct), 1 if inverse else 0)
+            Hq, ks, kos, Hkv, T, d, _ptr(positions), table._ref, 1 if inverse else 0)
     return q_out, k_out
 
 
@@ -765,8 +780,8 @@ def kv8_append(cache: KV8, k_new: torch.Tensor, v_new: torch.Tensor, lens: torch
             raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
     n = _offsets(cu_new, T, max_new, B, "max_new")
     _run_on(dev, stream, lib().kv8_append, cache._ref, C.byref(_rows(k_new, "k_new")),
-            C.byref(_rows(v_new, "v_new")), _p(cu_new), T, n, _p(lens), B, cache.Hkv, cache.d,
-            C.byref(rope.struct) if rope else None, _p(positions))
+            C.byref(_rows(v_new, "v_new")), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
+            rope._ref if rope else None, _ptr(positions))
     return cache
 
 
@@ -792,7 +807,7 @@ def kv8_read(cache: KV8, lens: torch.Tensor, n: Optional[int] = None,
         raise ValueError(f"k_out and v_out must be {list(shape)}")
     n = _offsets(cu, T, n, B, "n")
     _run_on(dev, stream, lib().kv8_read, cache._ref, C.byref(_rows(k_out, "k_out")),
-            C.byref(_rows(v_out, "v_out")), _p(cu), T, n, _p(lens), B, cache.Hkv, cache.d)
+            C.byref(_rows(v_out, "v_out")), _ptr(cu), T, n, _ptr(lens), B, cache.Hkv, cache.d)
     return k_out, v_out
 
 
@@ -826,9 +841,9 @@ def _attn_decode(fn, ref, q, cache, lens, n_init, n_recent, scale, out, lse_out,
     if workspace is None:
         n = int(lib().tsa_attn_decode_workspace_size(B, Hq, cache.Hkv, d))
         workspace = _new(stream, dev, (max(n, 256),), torch.uint8, zero=True)
-    _run_on(dev, stream, fn, _p(q), ref, _p(lens), B, Hq, cache.Hkv, d, int(n_init),
-            cache.l_cap if n_recent is None else int(n_recent), float(scale), _p(out),
-            _p(lse_out), _p(workspace), workspace.numel() * workspace.element_size())
+    _run_on(dev, stream, fn, _ptr(q), ref, _ptr(lens), B, Hq, cache.Hkv, d, int(n_init),
+            cache.l_cap if n_recent is None else int(n_recent), float(scale), _ptr(out),
+            _ptr(lse_out), _ptr(workspace), workspace.nbytes)
     return out, lse_out
 
 
@@ -896,6 +911,6 @@ def window_attn_prefill(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int
                                                           int(n_init), nr))
         workspace = _new(stream, dev, (max(nb, 256),), torch.uint8, zero=True)
     _run_on(dev, stream, lib().window_attn_prefill, C.byref(_rows(q, "q")), C.byref(kv.struct),
-            _p(cu_q), T, n, _p(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale), _p(out),
-            _p(lse_out), _p(workspace), workspace.numel() * workspace.element_size())
+            _ptr(cu_q), T, n, _ptr(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale), _ptr(out),
+            _ptr(lse_out), _ptr(workspace), workspace.nbytes)
     return out, lse_out

@@ -21,6 +21,21 @@ int scan_grid_rows(bool q8);
 
 using namespace tsa;
 
+namespace tsa {
+// Multiprocessors of the current device.
+int num_sms() {
+  static int sms[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (!sms[dev]) {
+    int v = 0;
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    sms[dev] = v > 0 ? v : 148;
+  }
+  return sms[dev];
+}
+}  // namespace tsa
+
 namespace {
 
 thread_local std::string g_err;
@@ -67,18 +82,6 @@ size_t up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 // padding of at most 7 slots per (CTA, warp, unit visit) run.
 int64_t dense_stride_for(int64_t l_cap) {
   return (int64_t)up((size_t)(l_cap > 0 ? l_cap : 1) + 65536, 64);
-}
-
-int num_sms() {
-  static int sms[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!sms[dev]) {
-    int v = 0;
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    sms[dev] = v > 0 ? v : 148;
-  }
-  return sms[dev];
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

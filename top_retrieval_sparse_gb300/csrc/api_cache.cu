@@ -15,6 +15,7 @@ int report_error(int code, const char* msg);
 int report_ok();
 int validate_kv(const tsa_kv* kv);
 cudaError_t count_launch(cudaError_t e);
+int num_sms();
 }  // namespace tsa
 
 using namespace tsa;
@@ -192,6 +193,13 @@ int check_window(int64_t n_init, int64_t n_recent, float scale) {
   return TSA_OK;
 }
 
+// Workspace of a decode step: the status word, the shares' partials, then the
+// units' arrival counters.  The counters come after a region of fixed size, so
+// that whatever sizes share a workspace, they only ever hold counters.
+constexpr size_t kDecodePartial = kAlign;
+constexpr size_t kDecodeArrived =
+    kDecodePartial + (size_t)2 * kDecodeShares * kDecodeSlot * sizeof(float);
+
 // Both decode entry points after their cache's checks.
 int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, int B, int Hq,
                int Hkv, int64_t n_init, int64_t n_recent, float scale, float* out,
@@ -204,21 +212,31 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
     return fail(TSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((rc = check_workspace(workspace, ws_bytes, tsa_attn_decode_workspace_size(B, Hq, Hkv, kD))))
     return rc;
-  AttnArgs a{};
-  a.q = RowsView{static_cast<uint16_t*>(const_cast<void*>(q)), (int64_t)Hq * kD, kD};
+  DecodeArgs a{};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = static_cast<const uint16_t*>(q);
   a.c = c;
-  a.fmt = fmt;
-  a.T = B;
   a.lens = lens;
   a.B = B;
   a.Hq = Hq;
   a.n_init = n_init;
   a.n_recent = n_recent;
   a.scale_log2 = (float)((double)scale * kLog2e);
-  a.out32 = out;
+  a.out = out;
   a.lse = lse_out;
-  a.status = static_cast<int*>(workspace);
-  return launched(launch_attn_plain(a, static_cast<cudaStream_t>(stream)), "attention launch");
+  a.status = reinterpret_cast<int*>(ws);
+  a.partial = reinterpret_cast<float*>(ws + kDecodePartial);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + kDecodeArrived);
+  // CTAs: as many as fit at once, fewer where even the longest sequences
+  // would not fill the smallest shares (8 slabs of 16 rows).
+  const int64_t cap = c.l_cap;
+  const int64_t seen = (n_init < cap ? n_init : cap) + (n_recent < cap ? n_recent : cap) + 32;
+  const int64_t slabs = (int64_t)B * Hkv * (((seen < cap ? seen : cap) + 15) / 16 + 1);
+  int64_t grid = num_sms() * 3;
+  if (grid > kDecodeShares) grid = kDecodeShares;
+  if (grid > (slabs + 7) / 8) grid = (slabs + 7) / 8;
+  return launched(launch_attn_decode(a, fmt, (int)grid, static_cast<cudaStream_t>(stream)),
+                  "attention launch");
 }
 
 }  // namespace
@@ -384,7 +402,7 @@ int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows* v_out,
 
 size_t tsa_attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || d != kD) return 0;
-  return kAlign;
+  return kDecodeArrived + ((size_t)B * Hkv * sizeof(uint32_t) + kAlign - 1) / kAlign * kAlign;
 }
 
 int kv8_attn_decode(const void* q, const tsa_kv8* cache, const int32_t* lens, int B, int Hq,

@@ -137,6 +137,25 @@ struct AttnArgs {
 };
 cudaError_t launch_attn_plain(const AttnArgs& a, cudaStream_t st);
 
+// One decode step (attn_decode.cu).
+constexpr int kDecodeThreads = 128;
+constexpr int kDecodeShares = 3 * 152;                      // most CTAs of a call
+constexpr int kDecodeSlot = 2 * kMaxGroup + kMaxGroup * kD; // floats of a partial
+struct DecodeArgs {
+  const uint16_t* q;       // bf16 [B][Hq][128]
+  CacheView c;
+  const int32_t* lens;
+  int B, Hq;
+  int64_t n_init, n_recent;
+  float scale_log2;        // scale * log2(e)
+  float* out;              // fp32 [B][Hq][128]
+  float* lse;              // [B][Hq] or nullptr
+  int* status;
+  float* partial;          // [2 * kDecodeShares][kDecodeSlot]
+  uint32_t* arrived;       // [B * Hkv], zero between calls
+};
+cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st);
+
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // every such kernel calls pdl_wait() before it touches memory.
 template <typename... P, typename... A>
