@@ -3,6 +3,7 @@
 //
 // Host-side validation, workspace layout and launches.  Nothing here allocates
 // device memory, synchronises or prints.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -193,6 +194,31 @@ int check_window(int64_t n_init, int64_t n_recent, float scale) {
   return TSA_OK;
 }
 
+// The tensor map of a bf16 pool's rows: boxes of 64 elements by `box` rows with
+// the 128-byte swizzle (encoded on the host; nothing is launched).
+int row_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || !f)
+      return fail(TSA_ERR_CUDA, "cuTensorMapEncodeTiled not found: %s", cudaGetErrorString(e));
+    fn.store(f, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {kRowBytes};
+  const cuuint32_t extent[2] = {64, (cuuint32_t)box}, step[2] = {1, 1};
+  const CUresult r = reinterpret_cast<Encode>(f)(
+      map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, extent,
+      step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TSA_ERR_CUDA, "tensor map: driver error %d", (int)r);
+  return TSA_OK;
+}
+
 // Workspace of a decode step: the status word, the shares' partials, then the
 // units' arrival counters.  The counters come after a region of fixed size, so
 // that whatever sizes share a workspace, they only ever hold counters.
@@ -212,6 +238,11 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
     return fail(TSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((rc = check_workspace(workspace, ws_bytes, tsa_attn_decode_workspace_size(B, Hq, Hkv, kD))))
     return rc;
+  // The kernels count rows in 32 bits (more keys than that exceed the memory).
+  const int64_t pool = c.page_table ? (fmt == kFmtBf16 ? 0 : (int64_t)c.n_pages << c.page_shift)
+                                    : (int64_t)B * c.l_cap;
+  if (pool > (int64_t)0xffffffff / Hkv)
+    return fail(TSA_ERR_INVALID_ARG, "the cache has 2^32 rows or more");
   DecodeArgs a{};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.q = static_cast<const uint16_t*>(q);
@@ -232,7 +263,7 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   const int64_t cap = c.l_cap;
   const int64_t seen = (n_init < cap ? n_init : cap) + (n_recent < cap ? n_recent : cap) + 32;
   const int64_t slabs = (int64_t)B * Hkv * (((seen < cap ? seen : cap) + 15) / 16 + 1);
-  int64_t grid = num_sms() * 3;
+  int64_t grid = num_sms() * attn_decode_ctas(fmt);
   if (grid > kDecodeShares) grid = kDecodeShares;
   if (grid > (slabs + 7) / 8) grid = (slabs + 7) / 8;
   return launched(launch_attn_decode(a, fmt, (int)grid, static_cast<cudaStream_t>(stream)),
@@ -441,7 +472,7 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
                         int max_q, const int32_t* lens, int B, int Hq, int Hkv, int d,
                         int64_t n_init, int64_t n_recent, float scale, void* out, float* lse_out,
                         void* workspace, size_t ws_bytes, void* stream) {
-  AttnArgs a{};
+  PrefillArgs a{};
   int rc = check_batch(B, Hkv, d);
   if (rc) return rc;
   if ((rc = check_groups(1, Hq, Hkv))) return rc;
@@ -457,20 +488,28 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
                             window_attn_prefill_workspace_size(B, Hq, Hkv, d, max_q, kv->l_cap,
                                                                n_init, n_recent))))
     return rc;
-  a.fmt = kFmtBf16;
+  CUtensorMap kmap, vmap;
+  const int box = kv->page_table && kv->page_size < 128 ? kv->page_size : 128;
+  const int64_t rows = kv->page_table ? 0x7fffffff : (int64_t)B * Hkv * kv->l_cap;
+  if (rows > 0x7fffffff) return fail(TSA_ERR_INVALID_ARG, "the cache has 2^31 rows or more");
+  if ((rc = row_map(kv->k, rows, box, &kmap)) || (rc = row_map(kv->v, rows, box, &vmap))) return rc;
   a.cu = cu_q;
   a.T = T;
   a.max_q = max_q;
   a.lens = lens;
-  a.B = B;
   a.Hq = Hq;
+  a.G = Hq / Hkv;
   a.n_init = n_init;
   a.n_recent = n_recent;
-  a.scale_log2 = (float)((double)scale * kLog2e);
-  a.out16 = static_cast<uint16_t*>(out);
+  a.negate = scale < 0;
+  a.zero = scale == 0;
+  a.scale_log2 = a.zero ? 1.f : (float)(std::fabs((double)scale) * kLog2e);
+  a.box = box;
+  a.out = static_cast<uint16_t*>(out);
   a.lse = lse_out;
   a.status = static_cast<int*>(workspace);
-  return launched(launch_attn_plain(a, static_cast<cudaStream_t>(stream)), "attention launch");
+  return launched(launch_window_prefill(kmap, vmap, a, B, static_cast<cudaStream_t>(stream)),
+                  "attention launch");
 }
 
 }  // extern "C"

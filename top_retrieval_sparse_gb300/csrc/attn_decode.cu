@@ -50,16 +50,16 @@ constexpr int kWarps = kDecodeThreads / 32;
 // steps 2^-32.
 constexpr float kRaised = 7.f, kSlack = 15.f;
 
-__device__ __forceinline__ uint4 ld_row(const uint8_t* p, bool on) {
+__device__ __forceinline__ uint4 ld_row(const uint8_t* p) {
   uint4 r;
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
-      " mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
-      " @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
-      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
-      : "l"(p), "r"((uint32_t)on)
-      : "memory");
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
   return r;
+}
+__device__ __forceinline__ uint4 ld_row_if(const uint8_t* p, bool on) {
+  return on ? ld_row(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 __device__ __forceinline__ uint32_t word(const uint4& w, int j) {
   return j == 0 ? w.x : (j == 1 ? w.y : (j == 2 ? w.z : w.w));
@@ -72,6 +72,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Of value scales, powers of two in earnest: a last-place error here would
+// change a weight, and its share of the sum, by 2^-22 of itself.
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -123,17 +135,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 
 // The visible rows of one sequence as a list of slabs: [0, s0), then from sw.
 struct Visible {
-  int64_t L, n0, lo, s0, sw, n;
+  int L, n0, lo, s0, sw, n;
 };
 __device__ __forceinline__ Visible visible(const DecodeArgs& a, int b) {
   Visible v;
-  int64_t L = a.lens[b];
-  v.L = L < 0 ? 0 : (L > a.c.l_cap ? a.c.l_cap : L);
-  v.n0 = a.n_init < v.L ? a.n_init : v.L;
-  v.lo = v.L - a.n_recent > 0 ? v.L - a.n_recent : 0;
-  v.s0 = (v.n0 + 15) >> 4;
+  const int len = a.lens[b], cap = (int)a.c.l_cap;
+  v.L = len < 0 ? 0 : (len > cap ? cap : len);
+  v.n0 = a.n_init < v.L ? (int)a.n_init : v.L;
+  v.lo = a.n_recent < v.L ? v.L - (int)a.n_recent : 0;
+  v.s0 = (int)(((uint32_t)v.n0 + 15) >> 4);
   v.sw = v.lo >> 4 > v.s0 ? v.lo >> 4 : v.s0;
-  const int64_t se = (v.L + 15) >> 4;
+  const int se = (int)(((uint32_t)v.L + 15) >> 4);
   v.n = v.s0 + (v.lo < v.L && se > v.sw ? se - v.sw : 0);
   return v;
 }
@@ -153,10 +165,17 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, in
     a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// Slabs that a warp works on at once, and CTAs of 4 warps an SM: rows of 8 KB
+// a turn for bf16 and e4m3 (their rows wait in 64 registers a lane, 12 warps an SM);
+// int8 codes take twice e4m3's instructions to widen, and 16 warps of one slab
+// each hide those better (16 x 65536 rows: 183 us against 187; e4m3 177 against 173).
+__host__ __device__ constexpr int slabs_of(int fmt) { return fmt == kFmtE4m3 ? 2 : 1; }
+__host__ __device__ constexpr int ctas_of(int fmt) { return fmt == kFmtInt8 ? 4 : 3; }
+
 template <int FMT>
-__global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeArgs a) {
+__global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kernel(DecodeArgs a) {
   constexpr bool B16 = FMT == kFmtBf16;
-  constexpr int NS = B16 ? 1 : 2;        // slabs a warp works on at once
+  constexpr int NS = slabs_of(FMT);      // slabs a warp works on at once
   constexpr int KW = B16 ? 4 : 2;        // 16-byte pieces of a key row a lane takes
   constexpr int VW = B16 ? 2 : 1;        // and of a value row
   constexpr int ROW = B16 ? 2 * kD : kD; // bytes of a row
@@ -181,7 +200,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
     int64_t n = 0;
     if (b < a.B) {
       const Visible v = visible(a, b);
-      n = v.n * Hkv;
+      n = (int64_t)v.n * Hkv;
       if (blockIdx.x == 0 && v.L != a.lens[b]) atomicOr(a.status, kStatusBadLength);
       if (n == 0 && b % gridDim.x == blockIdx.x)  // nothing visible
         for (int h = 0; h < a.Hq; ++h) {
@@ -224,8 +243,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
     while (prefix[b + 1] <= at) ++b;
     const Visible vis = visible(a, b);
     const int g = (int)((at - prefix[b]) / vis.n);
-    const int64_t u0 = prefix[b] + g * vis.n, u1 = u0 + vis.n;  // the unit in the list
-    const int64_t k0 = at - u0, k1 = (u1 < end ? u1 : end) - u0;
+    // the unit in the list, and the slabs of it that are this share's
+    const int64_t u0 = prefix[b] + (int64_t)g * vis.n, u1 = u0 + vis.n;
+    const int k0 = (int)(at - u0), k1 = (int)((u1 < end ? u1 : end) - u0);
 
     // Query fragments (columns: heads), exact in the product's type.
     uint32_t qf[8][2];
@@ -276,63 +296,62 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
     int turns = 0;
 
     uint4 kr[NS][2][KW], vr[NS][4][VW];
-    int64_t row[NS];        // of the slabs whose rows are being requested
-    uint32_t seen[NS], seen_now[NS];
+    // Rows fit 32 bits: 2^32 rows of keys alone are more than the memory.
+    uint32_t row[NS], seen[NS], seen_now[NS];
     float ks[NS], vs[NS], ks_now[NS], vs_now[NS];
     int32_t page[NS];
+    const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
+    const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
+    const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
+    const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
 
-    // Slab k of this unit (first row), or -1 past the share.
-    auto first_row = [&](int64_t k) -> int64_t {
-      return k >= k1 ? -1 : ((k < vis.s0 ? k : vis.sw + (k - vis.s0)) << 4);
-    };
-    auto want_pages = [&](int64_t k) {
-      if (a.c.page_table) {
+    // First row of slab k of this unit.
+    auto first_row = [&](int k) { return (k < vis.s0 ? k : vis.sw + (k - vis.s0)) << 4; };
+    auto want_pages = [&](int k) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const int64_t i = first_row(k + s);
-          page[s] = i < 0 ? 0 : a.c.page_table[(int64_t)b * a.c.max_pages + (i >> a.c.page_shift)];
-        }
-      }
+      for (int s = 0; s < NS; ++s)
+        if (pages && k + s < k1) page[s] = pages[first_row(k + s) >> a.c.page_shift];
     };
-    auto find_rows = [&](int64_t k) {
+    auto find_rows = [&](int k) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int64_t i = first_row(k + s);
-        uint32_t m = 0;
-        int64_t r = 0;
-        if (i >= 0) {
-          if (a.c.page_table) {
-            if ((uint32_t)page[s] < a.c.n_pages) {
-              r = (((int64_t)page[s] * Hkv + g) << a.c.page_shift) +
-                  (i & ((1 << a.c.page_shift) - 1));
-              m = 0xffffu;
-            } else {
-              bad = true;
-            }
-          } else {
-            r = ((int64_t)b * Hkv + g) * a.c.l_cap + i;
-            m = 0xffffu;
-          }
-          const bool whole = (i >= vis.lo && i + 16 <= vis.L) || i + 16 <= vis.n0;
-          if (!whole) {
-            uint32_t w = 0;
+        row[s] = seen[s] = 0u;
+        if (k + s < k1) {
+          const int i = first_row(k + s);
+          seen[s] = 0xffffu;
+          if (!((i >= vis.lo && vis.L - i >= 16) || vis.n0 - i >= 16)) {
+            seen[s] = 0u;
             for (int j = 0; j < 16; ++j)
-              if ((i + j < vis.n0 || i + j >= vis.lo) && i + j < vis.L) w |= 1u << j;
-            m &= w;
+              if ((j < vis.n0 - i || j >= vis.lo - i) && j < vis.L - i) seen[s] |= 1u << j;
+          }
+          if (!pages) {
+            row[s] = unit_row + (uint32_t)i;
+          } else if ((uint32_t)page[s] < a.c.n_pages) {
+            row[s] = (((uint32_t)page[s] * (uint32_t)Hkv + (uint32_t)g) << a.c.page_shift) +
+                     ((uint32_t)i & ((1u << a.c.page_shift) - 1u));
+          } else {
+            bad = true;
+            seen[s] = 0u;
           }
         }
-        row[s] = r;
-        seen[s] = m;
       }
     };
     auto want_keys = [&]() {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const uint8_t* p = a.c.k + row[s] * ROW + gr * ROW + 16 * tq;
+        const uint8_t* p = k_lane + (uint64_t)row[s] * ROW;
+        if (seen[s] == 0xffffu) {
 #pragma unroll
-        for (int c = 0; c < KW; ++c) {
-          kr[s][0][c] = ld_row(p + 64 * c, (seen[s] >> gr) & 1u);
-          kr[s][1][c] = ld_row(p + 8 * ROW + 64 * c, (seen[s] >> (gr + 8)) & 1u);
+          for (int c = 0; c < KW; ++c) {
+            kr[s][0][c] = ld_row(p + 64 * c);
+            kr[s][1][c] = ld_row(p + 8 * ROW + 64 * c);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < KW; ++c) {
+            kr[s][0][c] = ld_row_if(p + 64 * c, (seen[s] >> gr) & 1u);
+            kr[s][1][c] = ld_row_if(p + 8 * ROW + 64 * c, (seen[s] >> (gr + 8)) & 1u);
+          }
         }
         if (!B16) {
           ks[s] = seen[s] ? a.c.ks[row[s] >> a.c.block_shift] : 1.f;
@@ -343,19 +362,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
     auto want_values = [&]() {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const uint8_t* p = a.c.v + row[s] * ROW + 2 * tq * ROW + 16 * VW * gr;
+        const uint8_t* p = v_lane + (uint64_t)row[s] * ROW;
+        // rows 2tq, 2tq + 1, 2tq + 8, 2tq + 9
+        if (seen[s] == 0xffffu) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rows 2tq, 2tq + 1, 2tq + 8, 2tq + 9
-          const int r = (i & 1) + 8 * (i >> 1);
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int c = 0; c < VW; ++c)
-            vr[s][i][c] = ld_row(p + r * ROW + 16 * c, (seen[s] >> (2 * tq + r)) & 1u);
+            for (int c = 0; c < VW; ++c)
+              vr[s][i][c] = ld_row(p + ((i & 1) + 8 * (i >> 1)) * ROW + 16 * c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < VW; ++c) {
+              const int r = (i & 1) + 8 * (i >> 1);
+              vr[s][i][c] = ld_row_if(p + r * ROW + 16 * c, (seen[s] >> (2 * tq + r)) & 1u);
+            }
         }
       }
     };
 
-    const int64_t stride = (int64_t)kWarps * NS;
-    int64_t k = k0 + warp * NS;
+    constexpr int stride = kWarps * NS;
+    int k = k0 + warp * NS;
     want_pages(k);
     find_rows(k);
     want_pages(k + stride);
@@ -400,11 +428,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const float f0 = B16 ? qs0 : qs0 * ks_now[s], f1 = B16 ? qs1 : qs1 * ks_now[s];
-        const float add = B16 ? 0.f : log2f(vs_now[s]);
-        z[s][0] = (seen_now[s] >> gr) & 1u ? fmaf(z[s][0], f0, add) : -INFINITY;
-        z[s][1] = (seen_now[s] >> gr) & 1u ? fmaf(z[s][1], f1, add) : -INFINITY;
-        z[s][2] = (seen_now[s] >> (gr + 8)) & 1u ? fmaf(z[s][2], f0, add) : -INFINITY;
-        z[s][3] = (seen_now[s] >> (gr + 8)) & 1u ? fmaf(z[s][3], f1, add) : -INFINITY;
+        const float add = B16 ? 0.f : lg2(vs_now[s]);
+        z[s][0] = fmaf(z[s][0], f0, add);
+        z[s][1] = fmaf(z[s][1], f1, add);
+        z[s][2] = fmaf(z[s][2], f0, add);
+        z[s][3] = fmaf(z[s][3], f1, add);
+        if (seen_now[s] != 0xffffu) {
+          if (!((seen_now[s] >> gr) & 1u)) z[s][0] = z[s][1] = -INFINITY;
+          if (!((seen_now[s] >> (gr + 8)) & 1u)) z[s][2] = z[s][3] = -INFINITY;
+        }
         top0 = fmaxf(top0, fmaxf(z[s][0], z[s][2]));
         top1 = fmaxf(top1, fmaxf(z[s][1], z[s][3]));
       }
@@ -441,7 +473,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
       for (int s = 0; s < NS; ++s) {
         float p[4] = {ex2(z[s][0] - c0), ex2(z[s][1] - c1), ex2(z[s][2] - c0),
                       ex2(z[s][3] - c1)};
-        const float un = B16 ? 1.f : __frcp_rn(vs_now[s]);
+        const float un = B16 ? 1.f : rcp(vs_now[s]);
         l0 = fmaf(p[0] + p[2], un, l0);
         l1 = fmaf(p[1] + p[3], un, l1);
 #pragma unroll
@@ -607,6 +639,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) attn_decode_kernel(DecodeAr
 }
 
 }  // namespace
+
+int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
 
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st) {
   const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);

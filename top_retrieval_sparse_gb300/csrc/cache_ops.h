@@ -3,6 +3,7 @@
 // contract inside the library; not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -117,29 +118,9 @@ struct ReadArgs {
 };
 cudaError_t launch_kv8_read(const ReadArgs& a, cudaStream_t st);
 
-// Attention of the queries of B sequences (one each with one_token, else
-// ragged tokens) over the rows that window and sinks leave visible.
-struct AttnArgs {
-  RowsView q;
-  CacheView c;
-  int fmt;
-  const int32_t* cu;
-  int64_t T;
-  int max_q;
-  const int32_t* lens;
-  int B, Hq;
-  int64_t n_init, n_recent;
-  float scale_log2;   // scale * log2(e)
-  float* out32;       // fp32 [T][Hq][128] (decode), or
-  uint16_t* out16;    // bf16 [T][Hq][128]
-  float* lse;         // [T][Hq] or nullptr
-  int* status;
-};
-cudaError_t launch_attn_plain(const AttnArgs& a, cudaStream_t st);
-
 // One decode step (attn_decode.cu).
 constexpr int kDecodeThreads = 128;
-constexpr int kDecodeShares = 3 * 152;                      // most CTAs of a call
+constexpr int kDecodeShares = 4 * 152;                      // most CTAs of a call
 constexpr int kDecodeSlot = 2 * kMaxGroup + kMaxGroup * kD; // floats of a partial
 struct DecodeArgs {
   const uint16_t* q;       // bf16 [B][Hq][128]
@@ -154,7 +135,29 @@ struct DecodeArgs {
   float* partial;          // [2 * kDecodeShares][kDecodeSlot]
   uint32_t* arrived;       // [B * Hkv], zero between calls
 };
+int attn_decode_ctas(int fmt);  // resident CTAs of an SM
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st);
+
+// Many tokens per sequence (window_prefill.cu); the maps are the bf16 pool's
+// rows of 128 elements, in boxes of 64 elements by `box` rows.
+struct PrefillArgs {
+  RowsView q;
+  CacheView c;
+  const int32_t* cu;
+  int64_t T;
+  int max_q;
+  const int32_t* lens;
+  int Hq, G;
+  int64_t n_init, n_recent;
+  float scale_log2;    // |scale| * log2(e), > 0
+  int negate, zero;    // scale < 0: the queries' sign turned; scale = 0: zeros in their place
+  int box;
+  uint16_t* out;       // bf16 [T][Hq][128]
+  float* lse;          // [T][Hq] or nullptr
+  int* status;
+};
+cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const PrefillArgs& a, int B, cudaStream_t st);
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // every such kernel calls pdl_wait() before it touches memory.

@@ -1,0 +1,561 @@
+// window_prefill.cu -- attention of many new tokens per sequence over a bf16
+// cache: a query at position p sees the rows j <= p with j < n_init or
+// j > p - n_recent.
+//
+// Per KV head the G query heads of a token share its rows, so a 128-row tile of the
+// tensor core holds the heads of 128 / G tokens.  A CTA takes two such tiles (A and
+// B) over the key tiles of 128 rows that any of their queries sees:
+//   S = Q K^T (tcgen05, fp32 in tensor memory), P = 2^(S c - m c) (bf16, over
+//   S's columns), O += P V (tcgen05, fp32 in tensor memory)
+// with the running maximum m and sum of the softmax in registers, a row a thread.
+// Both products of a key tile are 2 x 128^3: the tensor core bounds the kernel, as long
+// as the exponentials of one tile run under the other tile's products; hence two.
+//
+// Warps.  0-3: softmax of tile A (thread = row = tensor-memory lane), 4-7: of B,
+// 8: the matrix instructions, 9: the copies.  K and V tiles go through a ring of
+// five 32 KB slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a
+// page where pages are smaller than a tile).  The order of the matrix instructions,
+// O_A(j), S_A(j+1), O_B(j), S_B(j+1), leaves tile A's softmax the time of B's products and
+// the other way round, and lets S(j+1) overwrite P(j) without a wait: they execute in
+// order.  A commit covers all of them, so a tile's softmax that sees S(j) also knows O(j-1)
+// done, and may rescale O; it does so only where the maximum has grown by more than 2^8.
+//
+// Masks cost nothing but at the edges of what is seen: there the rows' columns are
+// masked one by one, and rows of V that no query of the CTA sees are zeroed in
+// shared memory (whatever they hold, 0 * NaN would reach the output).
+#include <cuda.h>
+
+#include "cache_ops.h"
+
+namespace tsa {
+
+namespace {
+
+constexpr int kTile = 128;                       // rows of a key tile and of a query tile
+constexpr int kHalf = kTile * 128;               // bytes of 64 columns of a tile
+constexpr int kSlotBytes = 2 * kHalf;
+constexpr int kSlots = 5;
+constexpr int kPreThreads = 320;
+constexpr int kPreSmem = (2 + kSlots) * kSlotBytes + 1024;
+constexpr float kRescale = 8.f;                  // log2 of the growth that rescales O
+
+// Instruction descriptors: fp32 accumulator, bf16 operands, 128 x 128; B of the
+// second product (V) with its rows (keys) as the reduction index.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) |
+                            ((128u / 16) << 24);
+constexpr uint32_t kIdescV = kIdesc | (1u << 16);
+
+// Shared-memory operand, 128-byte swizzle: eight rows of 128 bytes are 1024
+// apart (stride offset); `lead` separates the two halves of 64 columns where they are
+// the outer index (V).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives on the barrier when every matrix instruction so far is complete.
+__device__ __forceinline__ void commit_mma(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 128 columns of this thread's row; the wait is part of it, so that nothing uses
+// the registers before they hold the values.
+__device__ __forceinline__ void load_cols(uint32_t addr, float (&x)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, "
+      "%47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, "
+      "%77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, "
+      "%92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, "
+      "%106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, "
+      "%118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
+      "}, [%128];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), 
+        "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), 
+        "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
+        "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), 
+        "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31]), 
+        "=f"(x[32]), "=f"(x[33]), "=f"(x[34]), "=f"(x[35]), "=f"(x[36]), "=f"(x[37]), 
+        "=f"(x[38]), "=f"(x[39]), "=f"(x[40]), "=f"(x[41]), "=f"(x[42]), "=f"(x[43]), 
+        "=f"(x[44]), "=f"(x[45]), "=f"(x[46]), "=f"(x[47]), "=f"(x[48]), "=f"(x[49]), 
+        "=f"(x[50]), "=f"(x[51]), "=f"(x[52]), "=f"(x[53]), "=f"(x[54]), "=f"(x[55]), 
+        "=f"(x[56]), "=f"(x[57]), "=f"(x[58]), "=f"(x[59]), "=f"(x[60]), "=f"(x[61]), 
+        "=f"(x[62]), "=f"(x[63]), "=f"(x[64]), "=f"(x[65]), "=f"(x[66]), "=f"(x[67]), 
+        "=f"(x[68]), "=f"(x[69]), "=f"(x[70]), "=f"(x[71]), "=f"(x[72]), "=f"(x[73]), 
+        "=f"(x[74]), "=f"(x[75]), "=f"(x[76]), "=f"(x[77]), "=f"(x[78]), "=f"(x[79]), 
+        "=f"(x[80]), "=f"(x[81]), "=f"(x[82]), "=f"(x[83]), "=f"(x[84]), "=f"(x[85]), 
+        "=f"(x[86]), "=f"(x[87]), "=f"(x[88]), "=f"(x[89]), "=f"(x[90]), "=f"(x[91]), 
+        "=f"(x[92]), "=f"(x[93]), "=f"(x[94]), "=f"(x[95]), "=f"(x[96]), "=f"(x[97]), 
+        "=f"(x[98]), "=f"(x[99]), "=f"(x[100]), "=f"(x[101]), "=f"(x[102]), "=f"(x[103]), 
+        "=f"(x[104]), "=f"(x[105]), "=f"(x[106]), "=f"(x[107]), "=f"(x[108]), "=f"(x[109]), 
+        "=f"(x[110]), "=f"(x[111]), "=f"(x[112]), "=f"(x[113]), "=f"(x[114]), "=f"(x[115]), 
+        "=f"(x[116]), "=f"(x[117]), "=f"(x[118]), "=f"(x[119]), "=f"(x[120]), "=f"(x[121]), 
+        "=f"(x[122]), "=f"(x[123]), "=f"(x[124]), "=f"(x[125]), "=f"(x[126]), "=f"(x[127])
+      : "r"(addr)
+      : "memory");
+}
+// 32 columns of this thread's row; the wait is part of it, so that nothing uses
+// the registers before they hold the values.
+__device__ __forceinline__ void load_cols(uint32_t addr, float (&x)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), 
+        "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), 
+        "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
+        "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), 
+        "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void store_cols(uint32_t addr, const float (&x)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+      "};" ::"r"(addr),
+        "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), 
+        "f"(x[8]), "f"(x[9]), "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), 
+        "f"(x[15]), "f"(x[16]), "f"(x[17]), "f"(x[18]), "f"(x[19]), "f"(x[20]), "f"(x[21]), 
+        "f"(x[22]), "f"(x[23]), "f"(x[24]), "f"(x[25]), "f"(x[26]), "f"(x[27]), "f"(x[28]), 
+        "f"(x[29]), "f"(x[30]), "f"(x[31])
+      : "memory");
+}
+__device__ __forceinline__ void store_cols(uint32_t addr, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+      "};" ::"r"(addr),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), 
+        "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), 
+        "r"(x[15])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// (a.x * b + c, a.y * b + c) and the sum of pairs, two lanes an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What a CTA's queries see: rows [0, n0) and [lo, end), as key tiles: [0, s0)
+// and [sw, se).
+struct Span {
+  int n0, lo, end, s0, sw, n;
+  __device__ int tile(int j) const { return j < s0 ? j : sw + (j - s0); }
+  __device__ bool sees(int r) const { return r < end && (r < n0 || r >= lo); }
+};
+
+struct Barriers {
+  uint64_t q[2], s[2], p[2], o[2], full[kSlots], empty[kSlots], drain;
+};
+
+__global__ void __launch_bounds__(kPreThreads, 1)
+    window_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, PrefillArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers bar;
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int abort_s;
+  __shared__ volatile int bad_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.z, g = blockIdx.y;
+  const int G = a.G, TQ = kTile / G;
+  pdl_wait();
+  pdl_trigger();
+
+  // This CTA's tokens [t0, t1) of sequence b, the last blocks first.
+  int64_t tok, n64;
+  bool bad_count = !seq_tokens(a.cu, a.max_q, a.T, b, tok, n64);
+  if (bad_count) {
+    if (tid == 0) atomicOr(a.status, kStatusBadLength);
+    if (tok < 0 || n64 < 0 || tok + n64 > a.T) return;
+    if (n64 > a.max_q) n64 = a.max_q;
+  }
+  const int n = (int)n64;
+  const int t0 = (int)(gridDim.x - 1 - blockIdx.x) * 2 * TQ;
+  if (t0 >= n) return;
+  const int t1 = t0 + 2 * TQ < n ? t0 + 2 * TQ : n;
+  int L = a.lens[b];
+  if (L < 0 || L > a.c.l_cap) {
+    if (tid == 0) atomicOr(a.status, kStatusBadLength);
+    L = L < 0 ? 0 : (int)a.c.l_cap;
+  }
+  const int p0 = L - n + t0;                 // position of the first token
+  Span v;
+  v.end = L - n + t1;                        // rows at or before the last token
+  if (v.end < 0) v.end = 0;
+  v.n0 = a.n_init < v.end ? (int)a.n_init : v.end;
+  {
+    const int64_t lo = (int64_t)p0 + 1 - a.n_recent;
+    v.lo = a.n_recent == 0 ? v.end : (lo < 0 ? 0 : (lo > v.end ? v.end : (int)lo));
+  }
+  v.s0 = (v.n0 + kTile - 1) / kTile;
+  v.sw = v.lo / kTile > v.s0 ? v.lo / kTile : v.s0;
+  const int se = (v.end + kTile - 1) / kTile;
+  v.n = v.s0 + (v.lo < v.end && se > v.sw ? se - v.sw : 0);
+  const bool two = t1 - t0 > TQ;             // tile B has tokens
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, ring = base + 2 * kSlotBytes;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q[i], kTile);
+      mbar_init(&bar.s[i], 1);
+      mbar_init(&bar.p[i], kTile);
+      mbar_init(&bar.o[i], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    mbar_init(&bar.drain, 1);
+    fence_mbar_init();
+    abort_s = 0;
+    bad_s = bad_count;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&tmem_s))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_s;
+  // Bounded; the whole warp agrees, since what follows is a warp's work.
+  auto wait = [&](uint64_t* x, uint32_t parity) {
+    const bool done = mbar_wait_or_abort(x, parity, &abort_s);
+    if (!done) abort_s = 1;
+    return __all_sync(0xffffffffu, done) != 0;
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2;                 // tile A or B
+    const int r = tid & 127;
+    const int my_t = t0 + x * TQ + r / G, h = g * G + r % G;
+    const bool live = r < TQ * G && my_t < t1;
+    const int p = L - n + my_t;              // position (rows past the tokens: unused)
+    if (x == 0 || two) {
+      // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7)
+      const uint32_t qx = q_at + x * kSlotBytes + r * 128;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q.p + (tok + my_t) * a.q.st + h * a.q.sh);
+      const uint32_t flip = a.negate ? 0x80008000u : 0u;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (live && !a.zero) {
+          w = src[c];
+          w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+        }
+        const uint32_t at = qx + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y),
+                     "r"(w.z), "r"(w.w)
+                     : "memory");
+      }
+      fence_proxy_async();
+      mbar_arrive(&bar.q[x]);
+
+      const uint32_t s_at = tmem + x * kTile + ((uint32_t)(warp & 3) << 21);
+      const uint32_t o_at = s_at + 2 * kTile;
+      const float sc = a.scale_log2;
+      float m = -INFINITY, l = 0.f;
+      // The tile's queries see all of a key tile k0 iff every one of them does.
+      const int first = L - n + t0 + x * TQ;
+      const int last = L - n + (t0 + (x + 1) * TQ < t1 ? t0 + (x + 1) * TQ : t1) - 1;
+      bool ok = true;
+      for (int j = 0; j < v.n && ok; ++j) {
+        const int k0 = v.tile(j) * kTile;
+        ok = wait(&bar.s[x], j & 1);
+        if (!ok) break;
+        fence_after();
+        float s[128];
+        load_cols(s_at, s);
+        const bool whole =
+            k0 + kTile - 1 <= first && (k0 + kTile <= a.n_init || k0 > (int64_t)last - a.n_recent);
+        if (!whole) {
+          // columns [0, hi) but [lo, mid): behind the query, between sinks and window
+          const int hi = p - k0 + 1;
+          const int64_t mid64 = (int64_t)p - a.n_recent + 1 - k0;
+          const int mid = mid64 < 0 ? 0 : (mid64 > kTile ? kTile : (int)mid64);
+          const int64_t lo64 = a.n_init - k0;
+          const int lo = lo64 < 0 ? 0 : (lo64 > kTile ? kTile : (int)lo64);
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= hi || (i >= lo && i < mid)) s[i] = -INFINITY;
+        }
+        float t = s[0];
+#pragma unroll
+        for (int i = 1; i + 1 < 128; i += 2) t = fmaxf(fmaxf(t, s[i]), s[i + 1]);
+        t = fmaxf(t, s[127]);
+        const bool grown = (t - m) * sc > kRescale || (m == -INFINITY && t > m);
+        if (__any_sync(0xffffffffu, grown)) {
+          const float f = grown ? (m == -INFINITY ? 0.f : ex2((m - t) * sc)) : 1.f;
+          if (grown) m = t;
+          l *= f;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              load_cols(o_at + 32 * c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              store_cols(o_at + 32 * c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m * sc;
+        float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]),
+                            make_float2(sc, sc), make_float2(off, off));
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            add[i & 1] = add2(add[i & 1], e);
+            w[i] = bf16x2(e.x, e.y);
+          }
+          store_cols(s_at + 16 * c, w);
+        }
+        l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+        wait_stores();
+        fence_before();
+        mbar_arrive(&bar.p[x]);
+      }
+      // O / l; rows without a visible key: 0 and -inf
+      if (ok && v.n > 0) {
+        ok = wait(&bar.o[x], 0);
+        fence_after();
+      }
+      const bool nan = !ok || bad_s;
+      const float inv = nan ? nanf("") : (l > 0.f ? 1.f / l : 0.f);
+      uint4* dst = reinterpret_cast<uint4*>(a.out + ((tok + my_t) * a.Hq + h) * kD);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        if (v.n > 0 && ok) {
+          load_cols(o_at + 32 * c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[4 * c + i] = make_uint4(bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                        bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                        bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                        bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+      }
+      if (live && a.lse)
+        a.lse[(tok + my_t) * a.Hq + h] =
+            nan ? nanf("") : (l > 0.f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------ matrix instructions
+    bool ok = true;
+    auto slot = [&](int it) { return ring + (it % kSlots) * kSlotBytes; };
+    auto filled = [&](int it) { return wait(&bar.full[it % kSlots], (it / kSlots) & 1); };
+    auto qk = [&](int x, int it) {
+      if (lane == 0) {
+        const uint32_t qa = q_at + x * kSlotBytes, ka = slot(it);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+          mma_ss(tmem + x * kTile, operand(qa + at, 16), operand(ka + at, 16), kIdesc, k > 0);
+        }
+      }
+    };
+    auto pv = [&](int x, int it, bool add) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + (2 + x) * kTile, tmem + x * kTile + 8 * k,
+                 operand(slot(it) + k * 16 * 128, kHalf), kIdescV, add || k > 0);
+      }
+    };
+    auto commit = [&](uint64_t* to) {
+      if (lane == 0) commit_mma(to);
+    };
+    const int nx = two ? 2 : 1;
+    for (int j = -1; j < v.n && ok; ++j) {   // O(j), S(j + 1)
+      for (int x = 0; x < nx && ok; ++x) {
+        if (j >= 0) {
+          if (x == 0) {
+            ok = filled(2 * j + 1);
+            if (!ok) break;
+            const int k0 = v.tile(j) * kTile;
+            const bool edge = k0 + kTile > v.end || (k0 + kTile > v.n0 && k0 < v.lo);
+            if (edge) {  // rows of V that nothing sees
+              for (int r = 0; r < kTile; ++r)
+                if (!v.sees(k0 + r))
+                  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(
+                                   slot(2 * j + 1) + (lane >> 4) * kHalf + r * 128 +
+                                   (lane & 15) * 8),
+                               "r"(0)
+                               : "memory");
+              fence_proxy_async();
+              __syncwarp();
+            }
+          }
+          ok = wait(&bar.p[x], j & 1);
+          if (!ok) break;
+          fence_after();
+          pv(x, 2 * j + 1, j > 0);
+          if (x == nx - 1) commit(&bar.empty[(2 * j + 1) % kSlots]);
+          if (j == v.n - 1) commit(&bar.o[x]);
+        } else {
+          ok = wait(&bar.q[x], 0);
+          if (!ok) break;
+        }
+        if (j + 1 < v.n) {
+          if (x == 0) ok = filled(2 * j + 2);
+          if (!ok) break;
+          fence_after();
+          qk(x, 2 * j + 2);
+          commit(&bar.s[x]);
+          if (x == nx - 1) commit(&bar.empty[(2 * j + 2) % kSlots]);
+        }
+      }
+    }
+    if (!ok) {  // nothing may still run on tensor memory when it is given back
+      commit(&bar.drain);
+      mbar_wait(&bar.drain, 0);
+      if (lane == 0) atomicOr(a.status, kStatusTimeout);
+    }
+  } else {
+    // -------------------------------------------------------------- copies
+    const int box = a.box;                   // rows of a box: 128, or a smaller page
+    const int per = kTile / box;             // boxes of a tile
+    const int i_box = lane >> 1, half = lane & 1;
+    const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
+    // Lane's box of tile j: its first row in the pool, or -1 where nothing of it
+    // is seen.
+    auto find = [&](int j) -> int64_t {
+      if (j >= v.n || i_box >= per) return -1;
+      const int r0 = v.tile(j) * kTile + i_box * box;
+      const bool any = r0 < v.end && (r0 < v.n0 || r0 + box > v.lo);
+      if (!any) return -1;
+      if (!pages) return ((int64_t)b * a.c.Hkv + g) * a.c.l_cap + r0;
+      const int32_t page = pages[r0 >> a.c.page_shift];
+      if ((uint32_t)page >= a.c.n_pages) {
+        bad_s = 1;
+        atomicOr(a.status, kStatusBadLength);
+        return -1;
+      }
+      return (((int64_t)page * a.c.Hkv + g) << a.c.page_shift) + (r0 & ((1 << a.c.page_shift) - 1));
+    };
+    int64_t next = find(0);
+    int issued = 0;
+    bool ok = true;
+    for (int j = 0; j < v.n && ok; ++j) {
+      const int64_t row = next;
+      next = find(j + 1);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box * 128;
+      for (int w = 0; w < 2 && ok; ++w) {
+        const int it = 2 * j + w, sl = it % kSlots;
+        if (it >= kSlots) ok = wait(&bar.empty[sl], (it / kSlots - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&bar.full[sl], bytes);
+        __syncwarp();
+        if (row >= 0)
+          copy_box(ring + sl * kSlotBytes + half * kHalf + i_box * box * 128, w ? &vmap : &kmap,
+                   64 * half, (int)row, &bar.full[sl]);
+        issued = it + 1;
+      }
+    }
+    if (!ok)  // let the copies in flight land
+      for (int it = issued > kSlots ? issued - kSlots : 0; it < issued; ++it)
+        mbar_wait(&bar.full[it % kSlots], (it / kSlots) & 1);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const PrefillArgs& a, int B, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute((const void*)window_prefill_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
+  if (e != cudaSuccess) return e;
+  const int tokens = 2 * (kTile / a.G);
+  const dim3 grid((a.max_q + tokens - 1) / tokens, a.c.Hkv, B);
+  return launch_dependent(window_prefill_kernel, grid, dim3(kPreThreads), kPreSmem, st, kmap, vmap,
+                          a);
+}
+
+}  // namespace tsa
