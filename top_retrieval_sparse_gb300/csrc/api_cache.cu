@@ -499,8 +499,8 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
   a.lens = lens;
   a.Hq = Hq;
   a.G = Hq / Hkv;
-  a.n_init = n_init;
-  a.n_recent = n_recent;
+  a.n_init = (int)(n_init < kv->l_cap ? n_init : kv->l_cap);
+  a.n_recent = (int)(n_recent < kv->l_cap ? n_recent : kv->l_cap);
   a.negate = scale < 0;
   a.zero = scale == 0;
   a.scale_log2 = a.zero ? 1.f : (float)(std::fabs((double)scale) * kLog2e);

@@ -148,7 +148,7 @@ struct PrefillArgs {
   int max_q;
   const int32_t* lens;
   int Hq, G;
-  int64_t n_init, n_recent;
+  int n_init, n_recent;  // clipped to l_cap
   float scale_log2;    // |scale| * log2(e), > 0
   int negate, zero;    // scale < 0: the queries' sign turned; scale = 0: zeros in their place
   int box;

@@ -11,14 +11,15 @@
 // Both products of a key tile are 2 x 128^3: the tensor core bounds the kernel, as long
 // as the exponentials of one tile run under the other tile's products; hence two.
 //
-// Warps.  0-3: softmax of tile A (thread = row = tensor-memory lane), 4-7: of B,
-// 8: the matrix instructions, 9: the copies.  K and V tiles go through a ring of
+// Warps.  0 and 3: the matrix instructions of A and of B, 1: the copies, 2: zeroing of
+// V (first, so that the scheduler prefers them), 4-7: softmax of tile A (thread = row = tensor-memory
+// lane), 8-11: of B.  K and V tiles go through a ring of
 // five 32 KB slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a
-// page where pages are smaller than a tile).  The order of the matrix instructions,
-// O_A(j), S_A(j+1), O_B(j), S_B(j+1), leaves tile A's softmax the time of B's products and
-// the other way round, and lets S(j+1) overwrite P(j) without a wait: they execute in
-// order.  A commit covers all of them, so a tile's softmax that sees S(j) also knows O(j-1)
-// done, and may rescale O; it does so only where the maximum has grown by more than 2^8.
+// page where pages are smaller than a tile).  A tile's matrix instructions come in the
+// order O(j), S(j+1), O(j+1) ..., from one thread, so that they execute in that order: S(j+1)
+// may overwrite P(j) without a wait.  A commit covers all of a thread's, so a softmax that
+// sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the weights
+// have grown by more than 2^16.
 //
 // Masks cost nothing but at the edges of what is seen: there the rows' columns are
 // masked one by one, and rows of V that no query of the CTA sees are zeroed in
@@ -35,9 +36,12 @@ constexpr int kTile = 128;                       // rows of a key tile and of a 
 constexpr int kHalf = kTile * 128;               // bytes of 64 columns of a tile
 constexpr int kSlotBytes = 2 * kHalf;
 constexpr int kSlots = 5;
-constexpr int kPreThreads = 320;
+constexpr int kPreThreads = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168 a scheduler
 constexpr int kPreSmem = (2 + kSlots) * kSlotBytes + 1024;
-constexpr float kRescale = 8.f;                  // log2 of the growth that rescales O
+// Weights may grow to 2^16 under an old maximum before O is rescaled: bf16 and
+// fp32 keep their precision at any size, and 2^16 is far from overflow.
+constexpr float kRescale = 16.f, kMost = 65536.f;
 
 // Instruction descriptors: fp32 accumulator, bf16 operands, 128 x 128; B of the
 // second product (V) with its rows (keys) as the reduction index.
@@ -48,9 +52,17 @@ constexpr uint32_t kIdescV = kIdesc | (1u << 16);
 // Shared-memory operand, 128-byte swizzle: eight rows of 128 bytes are 1024
 // apart (stride offset); `lead` separates the two halves of 64 columns where they are
 // the outer index (V).
+// An operand further on is the same descriptor with its address field (16 bytes a
+// count) advanced.
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 |
          (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(on));
+  return on != 0;
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool add) {
@@ -196,6 +208,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -209,8 +226,21 @@ struct Span {
   __device__ bool sees(int r) const { return r < end && (r < n0 || r >= lo); }
 };
 
+// A bounded wait.  One try in line; the loop with the clock and the abort flag
+// is kept out of the way of the usual path.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_wait_or_abort(bar, parity, abort)) return true;
+  *abort = 1;
+  return false;
+}
+
 struct Barriers {
-  uint64_t q[2], s[2], p[2], o[2], full[kSlots], empty[kSlots], drain;
+  uint64_t q[2], s[2], p[2][2], o[2], full[kSlots], empty[kSlots], clean[kSlots], drain[2],
+      turn[2];
 };
 
 __global__ void __launch_bounds__(kPreThreads, 1)
@@ -245,14 +275,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     L = L < 0 ? 0 : (int)a.c.l_cap;
   }
   const int p0 = L - n + t0;                 // position of the first token
+  const int ni = a.n_init, nr = a.n_recent;  // both at most l_cap
   Span v;
   v.end = L - n + t1;                        // rows at or before the last token
   if (v.end < 0) v.end = 0;
-  v.n0 = a.n_init < v.end ? (int)a.n_init : v.end;
-  {
-    const int64_t lo = (int64_t)p0 + 1 - a.n_recent;
-    v.lo = a.n_recent == 0 ? v.end : (lo < 0 ? 0 : (lo > v.end ? v.end : (int)lo));
-  }
+  v.n0 = ni < v.end ? ni : v.end;
+  v.lo = nr == 0 ? v.end : (p0 < nr ? 0 : p0 + 1 - nr);  // of the first token (p0 < v.end)
+  if (v.lo > v.end) v.lo = v.end;
   v.s0 = (v.n0 + kTile - 1) / kTile;
   v.sw = v.lo / kTile > v.s0 ? v.lo / kTile : v.s0;
   const int se = (v.end + kTile - 1) / kTile;
@@ -265,19 +294,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q[i], kTile);
       mbar_init(&bar.s[i], 1);
-      mbar_init(&bar.p[i], kTile);
+      mbar_init(&bar.p[i][0], kTile);
+      mbar_init(&bar.p[i][1], kTile);
       mbar_init(&bar.o[i], 1);
+      mbar_init(&bar.drain[i], 1);
+      mbar_init(&bar.turn[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i], two ? 2 : 1);
+      mbar_init(&bar.clean[i], 32);
     }
-    mbar_init(&bar.drain, 1);
     fence_mbar_init();
     abort_s = 0;
     bad_s = bad_count;
   }
-  if (warp == 8) {
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&tmem_s))
                  : "memory");
@@ -287,20 +319,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_s;
-  // Bounded; the whole warp agrees, since what follows is a warp's work.
+  // The whole warp agrees, where what follows is a warp's work.
   auto wait = [&](uint64_t* x, uint32_t parity) {
-    const bool done = mbar_wait_or_abort(x, parity, &abort_s);
-    if (!done) abort_s = 1;
-    return __all_sync(0xffffffffu, done) != 0;
+    return __all_sync(0xffffffffu, wait_for(x, parity, &abort_s)) != 0;
   };
 
-  if (warp < 8) {
+  if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    const int x = warp >> 2;                 // tile A or B
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int x = (warp >> 2) - 1;           // tile A or B
     const int r = tid & 127;
     const int my_t = t0 + x * TQ + r / G, h = g * G + r % G;
     const bool live = r < TQ * G && my_t < t1;
-    const int p = L - n + my_t;              // position (rows past the tokens: unused)
+    // position (rows past the tokens: unused; below 0 nothing is seen)
+    const int p = L - n + my_t < 0 ? -1 : L - n + my_t;
     if (x == 0 || two) {
       // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7)
       const uint32_t qx = q_at + x * kSlotBytes + r * 128;
@@ -329,34 +361,72 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int first = L - n + t0 + x * TQ;
       const int last = L - n + (t0 + (x + 1) * TQ < t1 ? t0 + (x + 1) * TQ : t1) - 1;
       bool ok = true;
-      for (int j = 0; j < v.n && ok; ++j) {
+      for (int j = 0; j < v.n; ++j) {
         const int k0 = v.tile(j) * kTile;
+        const bool whole = k0 + kTile - 1 <= first && (ni - k0 >= kTile || k0 > last - nr);
         ok = wait(&bar.s[x], j & 1);
         if (!ok) break;
         fence_after();
         float s[128];
         load_cols(s_at, s);
-        const bool whole =
-            k0 + kTile - 1 <= first && (k0 + kTile <= a.n_init || k0 > (int64_t)last - a.n_recent);
         if (!whole) {
           // columns [0, hi) but [lo, mid): behind the query, between sinks and window
-          const int hi = p - k0 + 1;
-          const int64_t mid64 = (int64_t)p - a.n_recent + 1 - k0;
-          const int mid = mid64 < 0 ? 0 : (mid64 > kTile ? kTile : (int)mid64);
-          const int64_t lo64 = a.n_init - k0;
-          const int lo = lo64 < 0 ? 0 : (lo64 > kTile ? kTile : (int)lo64);
+          const int hi = p - k0 + 1, lo = ni - k0, mid = p - nr + 1 - k0;
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i >= hi || (i >= lo && i < mid)) s[i] = -INFINITY;
         }
-        float t = s[0];
+        // Weights of half a tile (64 keys) under the maximum `top`; their sum.
+        auto weights = [&](int half, float top) {
+          const float off = top == -INFINITY ? 0.f : -top * sc;
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 1; i + 1 < 128; i += 2) t = fmaxf(fmaxf(t, s[i]), s[i + 1]);
-        t = fmaxf(t, s[127]);
-        const bool grown = (t - m) * sc > kRescale || (m == -INFINITY && t > m);
-        if (__any_sync(0xffffffffu, grown)) {
-          const float f = grown ? (m == -INFINITY ? 0.f : ex2((m - t) * sc)) : 1.f;
-          if (grown) m = t;
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]),
+                              make_float2(sc, sc), make_float2(off, off));
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              add[i & 1] = add2(add[i & 1], e);
+              w[i] = bf16x2(e.x, e.y);
+            }
+            store_cols(s_at + 16 * c, w);
+          }
+          return (add[0].x + add[0].y) + (add[1].x + add[1].y);
+        };
+        auto publish = [&](int half) {  // their products may begin
+          wait_stores();
+          fence_before();
+          mbar_arrive(&bar.p[x][half]);
+        };
+        // The maximum is off the path from S to P.  Weights are taken under the
+        // maximum so far as long as they stay below 2^kRescale: the first half's sum
+        // tells for itself, the second half's logits are looked at.  Where they do not
+        // (first tiles, rarely later) the maximum is found, O and the sum are rescaled and
+        // the weights taken again.
+        float l0 = 0.f;
+        bool good = m != -INFINITY || !live;  // rows without a query have no say
+        if (__all_sync(0xffffffffu, good)) {
+          float tops[4] = {s[64], s[65], s[66], s[67]};
+#pragma unroll
+          for (int i = 68; i < 124; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
+          const float t = max3(fmaxf(tops[0], s[124]), fmaxf(tops[1], s[125]),
+                               max3(tops[2], s[126], fmaxf(tops[3], s[127])));
+          l0 = weights(0, m);
+          good = (l0 <= kMost && (t - m) * sc <= kRescale) || !live;
+        }
+        if (!__all_sync(0xffffffffu, good)) {
+          float t = s[0];
+#pragma unroll
+          for (int i = 1; i < 127; i += 2) t = max3(t, s[i], s[i + 1]);
+          t = fmaxf(t, s[127]);
+          const float top = fmaxf(m, t);
+          const float f = m == top ? 1.f : ex2((m - top) * sc);
+          m = top;
           l *= f;
           if (j > 0) {
 #pragma unroll
@@ -368,27 +438,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               store_cols(o_at + 32 * c, o);
             }
           }
+          l0 = weights(0, m);
         }
-        const float off = m == -INFINITY ? 0.f : -m * sc;
-        float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]),
-                            make_float2(sc, sc), make_float2(off, off));
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            add[i & 1] = add2(add[i & 1], e);
-            w[i] = bf16x2(e.x, e.y);
-          }
-          store_cols(s_at + 16 * c, w);
-        }
-        l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
-        wait_stores();
-        fence_before();
-        mbar_arrive(&bar.p[x]);
+        publish(0);
+        l += l0 + weights(1, m);
+        publish(1);
       }
       // O / l; rows without a visible key: 0 and -inf
       if (ok && v.n > 0) {
@@ -420,79 +474,75 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         a.lse[(tok + my_t) * a.Hq + h] =
             nan ? nanf("") : (l > 0.f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY);
     }
-  } else if (warp == 8) {
+  } else {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+   if (warp == 0 || warp == 3) {
     // ------------------------------------------------ matrix instructions
-    bool ok = true;
-    auto slot = [&](int it) { return ring + (it % kSlots) * kSlotBytes; };
-    auto filled = [&](int it) { return wait(&bar.full[it % kSlots], (it / kSlots) & 1); };
-    auto qk = [&](int x, int it) {
-      if (lane == 0) {
-        const uint32_t qa = q_at + x * kSlotBytes, ka = slot(it);
+    // One thread for each query tile (issuing all of them is more than one
+    // thread can do in time), by turns: O_A(j), S_A(j+1), then O_B(j), S_B(j+1),
+    // so that one tile's softmax runs under the other's products.  K tile j is in the ring's slot of 2j, V tile j in
+    // that of 2j + 1.
+    const int x = warp == 3;
+    if ((x == 0 || two) && elect_one()) {
+      const uint32_t s_at = tmem + x * kTile, o_at = s_at + 2 * kTile;
+      const uint64_t qd = operand(q_at + x * kSlotBytes, 16);
+      const uint64_t kd = operand(ring, 16), vd = operand(ring, kHalf);
+      auto qk = [&](int slot) {
+        const uint64_t kx = kd + slot * (kSlotBytes >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
-          mma_ss(tmem + x * kTile, operand(qa + at, 16), operand(ka + at, 16), kIdesc, k > 0);
+          const int at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          mma_ss(s_at, qd + at, kx + at, kIdesc, k > 0);
         }
+        commit_mma(&bar.s[x]);
+        commit_mma(&bar.empty[slot]);
+      };
+      bool ok = true;
+      if (v.n > 0) {
+        ok = wait_for(&bar.q[x], 0, &abort_s) && wait_for(&bar.full[0], 0, &abort_s);
+        if (ok && x == 1) ok = wait_for(&bar.turn[1], 0, &abort_s);
+        if (ok) qk(0);
+        mbar_arrive(&bar.turn[x ^ 1]);
       }
-    };
-    auto pv = [&](int x, int it, bool add) {
-      if (lane == 0) {
+      int slot = 1, lap = 0;                 // of V tile j
+      for (int j = 0; j < v.n && ok; ++j) {
+        ok = wait_for(&bar.full[slot], lap, &abort_s);
+        if (ok && (j == v.s0 - 1 || j == v.s0 || j == v.n - 1))  // may hold unseen rows
+          ok = wait_for(&bar.clean[j % kSlots], (j / kSlots) & 1, &abort_s);
+        const uint64_t vx = vd + slot * (kSlotBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + (2 + x) * kTile, tmem + x * kTile + 8 * k,
-                 operand(slot(it) + k * 16 * 128, kHalf), kIdescV, add || k > 0);
-      }
-    };
-    auto commit = [&](uint64_t* to) {
-      if (lane == 0) commit_mma(to);
-    };
-    const int nx = two ? 2 : 1;
-    for (int j = -1; j < v.n && ok; ++j) {   // O(j), S(j + 1)
-      for (int x = 0; x < nx && ok; ++x) {
-        if (j >= 0) {
-          if (x == 0) {
-            ok = filled(2 * j + 1);
-            if (!ok) break;
-            const int k0 = v.tile(j) * kTile;
-            const bool edge = k0 + kTile > v.end || (k0 + kTile > v.n0 && k0 < v.lo);
-            if (edge) {  // rows of V that nothing sees
-              for (int r = 0; r < kTile; ++r)
-                if (!v.sees(k0 + r))
-                  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(
-                                   slot(2 * j + 1) + (lane >> 4) * kHalf + r * 128 +
-                                   (lane & 15) * 8),
-                               "r"(0)
-                               : "memory");
-              fence_proxy_async();
-              __syncwarp();
-            }
+        for (int part = 0; part < 2; ++part) {
+          ok = ok && wait_for(&bar.p[x][part], j & 1, &abort_s);
+          if (part == 0 && two) ok = ok && wait_for(&bar.turn[x], (j + x) & 1, &abort_s);
+          if (ok) {
+            fence_after();
+#pragma unroll
+            for (int k = 4 * part; k < 4 * part + 4; ++k)
+              mma_ts(o_at, s_at + 8 * k, vx + ((k * 16 * 128) >> 4), kIdescV, j > 0 || k > 0);
           }
-          ok = wait(&bar.p[x], j & 1);
-          if (!ok) break;
-          fence_after();
-          pv(x, 2 * j + 1, j > 0);
-          if (x == nx - 1) commit(&bar.empty[(2 * j + 1) % kSlots]);
-          if (j == v.n - 1) commit(&bar.o[x]);
-        } else {
-          ok = wait(&bar.q[x], 0);
-          if (!ok) break;
         }
+        if (!ok) break;
+        commit_mma(&bar.empty[slot]);
+        if (++slot == kSlots) slot = 0, lap ^= 1;
         if (j + 1 < v.n) {
-          if (x == 0) ok = filled(2 * j + 2);
+          ok = wait_for(&bar.full[slot], lap, &abort_s);
           if (!ok) break;
-          fence_after();
-          qk(x, 2 * j + 2);
-          commit(&bar.s[x]);
-          if (x == nx - 1) commit(&bar.empty[(2 * j + 2) % kSlots]);
+          qk(slot);
+          mbar_arrive(&bar.turn[x ^ 1]);
+          if (++slot == kSlots) slot = 0, lap ^= 1;
+        } else {
+          commit_mma(&bar.o[x]);
+          mbar_arrive(&bar.turn[x ^ 1]);
         }
       }
+      if (!ok) {  // nothing may still run on tensor memory when it is given back
+        commit_mma(&bar.drain[x]);
+        mbar_wait(&bar.drain[x], 0);
+        atomicOr(a.status, kStatusTimeout);
+      }
     }
-    if (!ok) {  // nothing may still run on tensor memory when it is given back
-      commit(&bar.drain);
-      mbar_wait(&bar.drain, 0);
-      if (lane == 0) atomicOr(a.status, kStatusTimeout);
-    }
-  } else {
+    __syncwarp();
+   } else if (warp == 1) {
     // -------------------------------------------------------------- copies
     const int box = a.box;                   // rows of a box: 128, or a smaller page
     const int per = kTile / box;             // boxes of a tile
@@ -536,10 +586,29 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     if (!ok)  // let the copies in flight land
       for (int it = issued > kSlots ? issued - kSlots : 0; it < issued; ++it)
         mbar_wait(&bar.full[it % kSlots], (it / kSlots) & 1);
+   } else if (warp == 2) {
+    // ---------------------------------------- rows of V that nothing sees
+    bool ok = true;
+    for (int j = 0; j < v.n && ok; ++j) {
+      const int it = 2 * j + 1, k0 = v.tile(j) * kTile;
+      ok = wait(&bar.full[it % kSlots], (it / kSlots) & 1);
+      if (!ok) break;
+      if (k0 + kTile > v.end || (k0 + kTile > v.n0 && k0 < v.lo)) {
+        const uint32_t at =
+            ring + (it % kSlots) * kSlotBytes + (lane >> 4) * kHalf + (lane & 15) * 8;
+        for (int r = 0; r < kTile; ++r)
+          if (!v.sees(k0 + r))
+            asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(at + r * 128), "r"(0)
+                         : "memory");
+        fence_proxy_async();
+      }
+      mbar_arrive(&bar.clean[j % kSlots]);
+    }
+   }
   }
   fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
