@@ -499,6 +499,7 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
   a.lens = lens;
   a.Hq = Hq;
   a.G = Hq / Hkv;
+  a.inv_g = (65536 + a.G - 1) / a.G;
   a.n_init = (int)(n_init < kv->l_cap ? n_init : kv->l_cap);
   a.n_recent = (int)(n_recent < kv->l_cap ? n_recent : kv->l_cap);
   a.negate = scale < 0;

@@ -147,7 +147,7 @@ struct PrefillArgs {
   int64_t T;
   int max_q;
   const int32_t* lens;
-  int Hq, G;
+  int Hq, G, inv_g;      // inv_g = ceil(2^16 / G): r / G = r * inv_g >> 16 for r < 128
   int n_init, n_recent;  // clipped to l_cap
   float scale_log2;    // |scale| * log2(e), > 0
   int negate, zero;    // scale < 0: the queries' sign turned; scale = 0: zeros in their place

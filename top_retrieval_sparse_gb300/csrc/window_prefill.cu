@@ -37,7 +37,7 @@ constexpr int kHalf = kTile * 128;               // bytes of 64 columns of a til
 constexpr int kSlotBytes = 2 * kHalf;
 constexpr int kSlots = 5;
 constexpr int kPreThreads = 384;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168 a scheduler
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 2 * 216 + 72 = 3 * 168 a scheduler
 constexpr int kPreSmem = (2 + kSlots) * kSlotBytes + 1024;
 // Weights may grow to 2^16 under an old maximum before O is rescaled: bf16 and
 // fp32 keep their precision at any size, and 2^16 is far from overflow.
@@ -213,6 +213,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Bits [0, n) of a word, any n.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -334,21 +338,32 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     // position (rows past the tokens: unused; below 0 nothing is seen)
     const int p = L - n + my_t < 0 ? -1 : L - n + my_t;
     if (x == 0 || two) {
-      // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7)
-      const uint32_t qx = q_at + x * kSlotBytes + r * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q.p + (tok + my_t) * a.q.st + h * a.q.sh);
-      const uint32_t flip = a.negate ? 0x80008000u : 0u;
+      // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7).
+      // A half-warp a row, so that a row's 256 bytes are one request; all of them in
+      // flight before the first is stored.
+      const int r_warp = (warp & 3) * 32, r_half = lane >> 4, piece = lane & 15;
+      const uint32_t q_mine = q_at + x * kSlotBytes;
+      {
+        const uint32_t flip = a.negate ? 0x80008000u : 0u;
+        uint4 w[16];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (live && !a.zero) {
-          w = src[c];
-          w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+        for (int i = 0; i < 16; ++i) {
+          const int rr = r_warp + 2 * i + r_half, tt = (rr * a.inv_g) >> 16;
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (tt < TQ && t0 + x * TQ + tt < t1 && !a.zero)
+            w[i] = *reinterpret_cast<const uint4*>(
+                a.q.p + (tok + t0 + x * TQ + tt) * a.q.st + (g * G + rr - tt * G) * a.q.sh +
+                8 * piece);
         }
-        const uint32_t at = qx + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y),
-                     "r"(w.z), "r"(w.w)
-                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int rr = r_warp + 2 * i + r_half;
+          const uint32_t at = q_mine + (piece >> 3) * kHalf + rr * 128 +
+                              (((piece & 7) ^ (rr & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[i].x ^ flip),
+                       "r"(w[i].y ^ flip), "r"(w[i].z ^ flip), "r"(w[i].w ^ flip)
+                       : "memory");
+        }
       }
       fence_proxy_async();
       mbar_arrive(&bar.q[x]);
@@ -373,8 +388,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           // columns [0, hi) but [lo, mid): behind the query, between sinks and window
           const int hi = p - k0 + 1, lo = ni - k0, mid = p - nr + 1 - k0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= hi || (i >= lo && i < mid)) s[i] = -INFINITY;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t on = below(hi - 32 * c) & ~(below(mid - 32 * c) & ~below(lo - 32 * c));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(on & (1u << i))) s[32 * c + i] = -INFINITY;
+          }
         }
         // Weights of half a tile (64 keys) under the maximum `top`; their sum.
         auto weights = [&](int half, float top) {
@@ -420,11 +439,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           good = (l0 <= kMost && (t - m) * sc <= kRescale) || !live;
         }
         if (!__all_sync(0xffffffffu, good)) {
-          float t = s[0];
+          float tops[4] = {m, m, m, m};
 #pragma unroll
-          for (int i = 1; i < 127; i += 2) t = max3(t, s[i], s[i + 1]);
-          t = fmaxf(t, s[127]);
-          const float top = fmaxf(m, t);
+          for (int i = 0; i < 128; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           const float f = m == top ? 1.f : ex2((m - top) * sc);
           m = top;
           l *= f;
@@ -451,24 +471,39 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       const bool nan = !ok || bad_s;
       const float inv = nan ? nanf("") : (l > 0.f ? 1.f / l : 0.f);
-      uint4* dst = reinterpret_cast<uint4*>(a.out + ((tok + my_t) * a.Hq + h) * kD);
+      // A row's 256 bytes go through the warp's own rows of Q's tile, which the
+      // products have read, so that a half-warp stores them in one request.
+      if (v.n > 0 && ok) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        if (v.n > 0 && ok) {
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
           load_cols(o_at + 32 * c, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (live) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[4 * c + i] = make_uint4(bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                        bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                        bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                        bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             q_mine + r * 256 + (((4 * c + i) ^ (r & 7)) << 4)),
+                         "r"(bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv)),
+                         "r"(bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv)),
+                         "r"(bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv)),
+                         "r"(bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv))
+                         : "memory");
         }
+        __syncwarp();
+      }
+      const uint32_t blank = nan ? 0x7fff7fffu : 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int rr = r_warp + 2 * i + r_half, tt = (rr * a.inv_g) >> 16;
+        uint4 w = make_uint4(blank, blank, blank, blank);
+        if (v.n > 0 && ok)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(q_mine + rr * 256 + ((piece ^ (rr & 7)) << 4))
+                       : "memory");
+        if (tt < TQ && t0 + x * TQ + tt < t1)
+          *reinterpret_cast<uint4*>(a.out +
+                                    ((tok + t0 + x * TQ + tt) * a.Hq + g * G + rr - tt * G) * kD +
+                                    8 * piece) = w;
       }
       if (live && a.lse)
         a.lse[(tok + my_t) * a.Hq + h] =
