@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -598,13 +599,18 @@ def _new(stream, dev: torch.device, shape, dtype, zero: bool = False) -> torch.T
         return make(shape, dtype=dtype, device=dev)
 
 
-def _rows(t: torch.Tensor, name: str) -> _RowsStruct:
+_pack_rows = struct.Struct("=qqq").pack  # tsa_rows
+
+
+def _rows(t: torch.Tensor, name: str) -> bytes:
+    """The tsa_rows of a bf16 [tokens][heads][128] tensor (as its bytes: a
+    quarter of the time of a ctypes structure)."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     st = t.stride()
     if len(st) != 3 or st[2] != 1:
         raise ValueError(f"{name} must be [tokens][heads][128] with contiguous rows")
-    return _RowsStruct(t.data_ptr(), st[0], st[1])
+    return _pack_rows(t.data_ptr(), st[0], st[1])
 
 
 def _offsets(cu, T: int, max_n, B: int, what: str) -> int:
@@ -678,10 +684,10 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
             k_out = _new(stream, dev, k.shape, torch.bfloat16)
         if k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
             raise ValueError("k and k_out must be [tokens][heads][128] with q's tokens")
-        Hkv, ks, kos = k.shape[1], C.byref(_rows(k, "k")), C.byref(_rows(k_out, "k_out"))
+        Hkv, ks, kos = k.shape[1], _rows(k, "k"), _rows(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _run_on(dev, stream, lib().rope_apply, C.byref(_rows(q, "q")), C.byref(_rows(q_out, "q_out")),
+    _run_on(dev, stream, lib().rope_apply, _rows(q, "q"), _rows(q_out, "q_out"),
             Hq, ks, kos, Hkv, T, d, _ptr(positions), table._ref, 1 if inverse else 0)
     return q_out, k_out
 
@@ -779,8 +785,8 @@ def kv8_append(cache: KV8, k_new: torch.Tensor, v_new: torch.Tensor, lens: torch
         if positions.shape != (T,):
             raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
     n = _offsets(cu_new, T, max_new, B, "max_new")
-    _run_on(dev, stream, lib().kv8_append, cache._ref, C.byref(_rows(k_new, "k_new")),
-            C.byref(_rows(v_new, "v_new")), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
+    _run_on(dev, stream, lib().kv8_append, cache._ref, _rows(k_new, "k_new"),
+            _rows(v_new, "v_new"), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
             rope._ref if rope else None, _ptr(positions))
     return cache
 
@@ -806,8 +812,8 @@ def kv8_read(cache: KV8, lens: torch.Tensor, n: Optional[int] = None,
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out and v_out must be {list(shape)}")
     n = _offsets(cu, T, n, B, "n")
-    _run_on(dev, stream, lib().kv8_read, cache._ref, C.byref(_rows(k_out, "k_out")),
-            C.byref(_rows(v_out, "v_out")), _ptr(cu), T, n, _ptr(lens), B, cache.Hkv, cache.d)
+    _run_on(dev, stream, lib().kv8_read, cache._ref, _rows(k_out, "k_out"),
+            _rows(v_out, "v_out"), _ptr(cu), T, n, _ptr(lens), B, cache.Hkv, cache.d)
     return k_out, v_out
 
 
@@ -910,7 +916,7 @@ def window_attn_prefill(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int
         nb = int(lib().window_attn_prefill_workspace_size(B, Hq, kv.Hkv, d, n, kv.l_cap,
                                                           int(n_init), nr))
         workspace = _new(stream, dev, (max(nb, 256),), torch.uint8, zero=True)
-    _run_on(dev, stream, lib().window_attn_prefill, C.byref(_rows(q, "q")), C.byref(kv.struct),
+    _run_on(dev, stream, lib().window_attn_prefill, _rows(q, "q"), C.byref(kv.struct),
             _ptr(cu_q), T, n, _ptr(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale), _ptr(out),
             _ptr(lse_out), _ptr(workspace), workspace.nbytes)
     return out, lse_out

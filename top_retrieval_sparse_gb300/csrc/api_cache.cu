@@ -397,6 +397,8 @@ int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_ne
   if ((rc = check_rows(k_new, T, Hkv, false, "k_new", a.k))) return rc;
   if ((rc = check_rows(v_new, T, Hkv, false, "v_new", a.v))) return rc;
   if (!lens) return fail(TSA_ERR_INVALID_ARG, "lens is NULL");
+  if ((T / cache->block + 2) * 2 * Hkv >= (int64_t)1 << 31)
+    return fail(TSA_ERR_INVALID_ARG, "T * Hkv is too large");
   a.fmt = cache->format == TSA_KV8_INT8 ? kFmtInt8 : kFmtE4m3;
   a.block = cache->block;
   a.cu = cu_new;

@@ -133,6 +133,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     mma_f16(d, a0, a1, a2, a3, b0, b1);
 }
 
+// a / b of numbers that are not negative; 64-bit division takes hundreds of cycles
+// and is only needed past 2^32 slabs.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The visible rows of one sequence as a list of slabs: [0, s0), then from sw.
 struct Visible {
   int L, n0, lo, s0, sw, n;
@@ -192,11 +199,13 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   const int gr = lane >> 2, tq = lane & 3;
   const int Hkv = a.c.Hkv, G = a.Hq / Hkv;
 
-  // The list of all slabs, sequence by sequence.
+  // The list of all slabs, sequence by sequence.  Up to 32 sequences every warp
+  // makes it for itself (all write the same values), else the warps share it.
   if (tid == 0) prefix[0] = 0;
+  const int step = a.B <= 32 ? 32 : kDecodeThreads, me = a.B <= 32 ? lane : tid;
   int64_t carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kDecodeThreads) {
-    const int b = b0 + tid;
+  for (int b0 = 0; b0 < a.B; b0 += step) {
+    const int b = b0 + me;
     int64_t n = 0;
     if (b < a.B) {
       const Visible v = visible(a, b);
@@ -215,6 +224,13 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
+    if (a.B <= 32) {
+      if (b < a.B) prefix[b + 1] = x;
+      if (lane == 0) prefix[0] = 0;
+      carry = __shfl_sync(0xffffffffu, x, 31);
+      __syncwarp();
+      break;
+    }
     if (lane == 31) scan_s[warp] = x;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) {
@@ -225,9 +241,9 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     __syncthreads();
   }
   const int64_t total = carry;
-  constexpr int kLeast = kWarps * 2;  // slabs of the smallest share
-  int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  share = (share + kLeast - 1) / kLeast * kLeast;
+  constexpr int kLeast = kWarps * 2;  // slabs of the smallest share (a power of two)
+  int64_t share = quotient(total + gridDim.x - 1, gridDim.x);
+  share = (share + kLeast - 1) & ~(int64_t)(kLeast - 1);
   if (share < kLeast) share = kLeast;
   int64_t at = (int64_t)blockIdx.x * share;
   const int64_t end = at + share < total ? at + share : total;
@@ -242,7 +258,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   while (at < end) {
     while (prefix[b + 1] <= at) ++b;
     const Visible vis = visible(a, b);
-    const int g = (int)((at - prefix[b]) / vis.n);
+    const int g = (int)quotient(at - prefix[b], vis.n);
     // the unit in the list, and the slabs of it that are this share's
     const int64_t u0 = prefix[b] + (int64_t)g * vis.n, u1 = u0 + vis.n;
     const int k0 = (int)(at - u0), k1 = (int)((u1 < end ? u1 : end) - u0);
@@ -591,7 +607,8 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     }
     if (!all) {
       // The shares of the unit are s0 .. s1; the last to get here joins them.
-      const int s0 = (int)(u0 / share), s1 = (int)((u1 - 1) / share);
+      const int s0 = (int)quotient(u0, share), s1 = (int)quotient(u1 - 1, share);
+      const int which0 = u0 == s0 * share ? 0 : 1;  // the unit's slot of share s0; 0 of the others
       uint32_t* ctr = a.arrived + (int64_t)b * Hkv + g;
       __threadfence();
       __syncthreads();
@@ -602,9 +619,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
         for (int h = warp; h < G; h += kWarps) {
           // lanes look at the shares' maxima and sums, then at the outputs'
           // dimensions; every load of a pass is independent of the others
-          auto part = [&](int s) {
-            return slot_of(a, s, s > s0 || u0 % share == 0 ? 0 : 1);
-          };
+          auto part = [&](int s) { return slot_of(a, s, s > s0 ? 0 : which0); };
           float m = -INFINITY, l = 0.f;
           for (int s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, __ldcg(part(s) + h));
           m = warp_max(m);
@@ -617,7 +632,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
               f = ex2(__ldcg(part(t + lane) + h) - c);
               l = fmaf(__ldcg(part(t + lane) + kMaxGroup + h), f, l);
             }
-#pragma unroll 8
+#pragma unroll 16
             for (int s = 0; s < n; ++s) {
               const float w = __shfl_sync(0xffffffffu, f, s);
               const float4 x = __ldcg(reinterpret_cast<const float4*>(

@@ -8,8 +8,7 @@ namespace tsa {
 
 namespace {
 
-constexpr int kAppendThreads = 256;                // 16 half-warps, a row each
-constexpr int kAppendRows = kAppendThreads / 16;
+constexpr int kAppendThreads = 256;
 
 // Smallest e >= -60 with top * 2^e >= amax (finite), top = 127 or 448:
 // amax = m * 2^x with m in [1, 2) and top = 1.984375 * 2^6 or 1.75 * 2^8.
@@ -23,22 +22,30 @@ __device__ __forceinline__ float scale_for(float amax, int fmt) {
   return ldexpf(1.f, e);
 }
 
+// Codes of eight values.  int8: 1.5 * 2^23 + 128 is added, which rounds to whole
+// numbers (ties to even) and leaves code + 128 in the low byte; infinities
+// saturate and NaN becomes 0.
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-  uint32_t b[8];
+  if constexpr (FMT == kFmtInt8) {
+    uint32_t b[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float y = x[e] * inv;
-    if (FMT == kFmtInt8) {
-      int c = __float2int_rn(y);  // infinities saturate, NaN gives 0
-      c = c < -127 ? -127 : (c > 127 ? 127 : c);
-      b[e] = (uint32_t)(c + 128);
-    } else {
-      b[e] = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    for (int e = 0; e < 8; ++e) {
+      float y = x[e] * inv;
+      y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
+      b[e] = __float_as_uint(y + 12583040.f);
     }
+    const uint32_t lo0 = __byte_perm(b[0], b[1], 0x0040), hi0 = __byte_perm(b[2], b[3], 0x0040);
+    const uint32_t lo1 = __byte_perm(b[4], b[5], 0x0040), hi1 = __byte_perm(b[6], b[7], 0x0040);
+    return make_uint2(__byte_perm(lo0, hi0, 0x5410), __byte_perm(lo1, hi1, 0x5410));
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      h[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv),
+                                      __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   }
-  return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24,
-                    b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
 }
 
 template <int FMT>
@@ -55,16 +62,22 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&x)[8]) {
   }
 }
 
-// One CTA per (touched block, KV head and K or V, sequence): the new rows of
-// the block stay in registers between the search for their largest magnitude
-// and their coding.
-template <int FMT, int BLK>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a) {
-  constexpr int NR = (BLK + kAppendRows - 1) / kAppendRows;
+// Bandwidth-bound: a row's 256 bytes are read once and written as 128.  The new
+// rows of one (block, KV head, K or V) stay in the registers of BLK / 16 warps (a team;
+// 16 rows a warp, eight lanes a row, 128 bytes a lane in flight) between the search
+// for their largest magnitude and their coding.  With ROT the keys' angles are the same for
+// every KV head, so a CTA puts those of the block's rows into shared memory once
+// and its teams go through `heads` heads; blockIdx.x < nb is then the keys of block
+// blockIdx.x, and the rest are the values, a team each, as without a rotation.
+template <int FMT, int BLK, bool ROT>
+__global__ void __launch_bounds__(kAppendThreads, ROT ? 2 : 3)
+    kv8_append_kernel(AppendArgs a, int nb, int heads) {
+  constexpr int TW = BLK / 16, TEAMS = kAppendThreads / 32 / TW;
+  extern __shared__ float2 angle_s[];       // [BLK][pairs] (ROT)
   __shared__ float red[kAppendThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.z, g = blockIdx.y >> 1, which = blockIdx.y & 1;
+  const int b = blockIdx.y, Hkv = a.c.Hkv;
   int64_t tok, n;
   const int64_t L = a.lens[b];
   const bool good = seq_tokens(a.cu, a.max_new, a.T, b, tok, n);
@@ -74,72 +87,156 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendArgs a
   }
   if (n == 0) return;
   const int64_t start = L - n;
-  const int64_t p0 = (start / BLK + blockIdx.x) * BLK;  // the block's first position
-  if (p0 >= L) return;
-  const int64_t row0 = cache_row(a.c, b, g, p0);
-  if (row0 < 0) {
-    if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
-    return;
+  const int warp = threadIdx.x >> 5, team = warp / TW, lane = threadIdx.x & 31, l = lane & 7;
+  const int row_in = (warp % TW) * 16 + (lane >> 3);  // rows row_in + 4 i of the block
+
+  // This CTA's items: (block, head, K or V) of its teams.
+  const int parts = (Hkv + heads - 1) / heads;        // CTAs of a block's keys
+  const bool turn = ROT && (int)blockIdx.x < nb * parts;
+  int64_t j = 0;                                      // block, counted from start's
+  int g0 = 0, g1 = 0, which = 0;                      // team's heads: g0, g0 + TEAMS, ... < g1
+  if (turn) {
+    j = blockIdx.x / parts;
+    g0 = (blockIdx.x % parts) * heads;
+    g1 = g0 + heads < Hkv ? g0 + heads : Hkv;
+    g0 += team;
+  } else {
+    // item i: head i % Hkv of block i / Hkv; K then V within a block without ROT
+    const int64_t i = (int64_t)(blockIdx.x - (ROT ? nb * parts : 0)) * TEAMS + team;
+    which = ROT ? 1 : (int)((i / Hkv) & 1);
+    j = ROT ? i / Hkv : i / (2 * Hkv);
+    g0 = (int)(i % Hkv);
+    g1 = g0 + 1;
   }
-  const int hw = threadIdx.x >> 4, c = threadIdx.x & 15;
-  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+  const int64_t p0 = (start / BLK + j) * BLK;         // the block's first position
+  const bool any = j < nb && p0 < L;
+  RopeLane ln = {2 * l, 2 * l + 1, -1};
+  if (ROT && turn) {
+    if (!any) return;                                 // the whole CTA: one block
+    ln = rope_lane(a.rope, l);
+    for (int e = threadIdx.x; e < BLK * a.rope.pairs; e += kAppendThreads) {
+      const int64_t pos = p0 + e / a.rope.pairs;
+      if (pos < start || pos >= L) continue;
+      const int64_t at = a.positions ? (int64_t)a.positions[tok + pos - start] : pos;
+      angle_s[e] = rope_angle(a.rope, at, e % a.rope.pairs);
+      if ((at < 0 || at >= a.rope.max_pos) && a.status) atomicOr(a.status, kStatusBadLength);
+    }
+    __syncthreads();
+  }
   const RowsView& in = which ? a.v : a.k;
   uint8_t* codes = which ? a.c.v : a.c.k;
   float* scales = which ? a.c.vs : a.c.ks;
-  const bool turn = !which && a.rope.lo != nullptr;
-  const int pair = turn ? rope_pair(a.rope, c) : -1;
-  float x[NR][8];
-  float amax = 0.f;
+  const int turns = ROT && turn ? (heads + TEAMS - 1) / TEAMS : 1;
+  for (int it = 0; it < turns; ++it) {
+    const int g = g0 + it * TEAMS;
+    int64_t row0 = -1;
+    if (any && g < g1) {
+      row0 = cache_row(a.c, b, g, p0);
+      if (row0 < 0 && lane == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+    }
+    const bool live = row0 >= 0;
+    float x[ROT ? 4 : 1][16];  // rotated rows; without ROT they are widened again below
+    float amax = 0.f, had = 0.f;
+    uint4 w[4][2];
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int64_t pos = p0 + hw + i * kAppendRows;
-    const bool mine = pos >= start && pos < L && (BLK >= kAppendRows || hw < BLK);
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    const int64_t t = tok + pos - start;
-    if (mine) w = *reinterpret_cast<const uint4*>(in.p + t * in.st + g * in.sh + 8 * c);
-    unpack8(w, x[i]);
-    if (turn) {
-      float2 cs[8];
-      const int64_t at = !mine ? 0 : (a.positions ? (int64_t)a.positions[t] : pos);
-      if (mine && c == 0 && a.status && (at < 0 || at >= a.rope.max_pos))
-        atomicOr(a.status, kStatusBadLength);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t pos = p0 + row_in + 4 * i;
+      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && pos >= start && pos < L) {
+        const uint16_t* p = in.p + (tok + pos - start) * in.st + g * in.sh;
+        w[i][0] = *reinterpret_cast<const uint4*>(p + 8 * ln.a);
+        w[i][1] = *reinterpret_cast<const uint4*>(p + 8 * ln.b);
+      }
+    }
+    if (live) had = scales[row0 / BLK];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        cs[e] = mine && pair >= 0 && pair + e < a.rope.pairs ? rope_angle(a.rope, at, pair + e)
-                                                             : make_float2(1.f, 0.f);
-      rope_turn(a.rope, c, mask, cs, x[i]);
+    for (int i = 0; i < 4; ++i) {
+      float u[8], v[8];
+      unpack8(w[i][0], u);
+      unpack8(w[i][1], v);
+      if (ROT && turn) {
+        const int64_t pos = p0 + row_in + 4 * i;
+        if (live && ln.pair >= 0 && pos >= start && pos < L) {
+          float2 cs[8];
+          const float4* at =
+              reinterpret_cast<const float4*>(angle_s + (row_in + 4 * i) * a.rope.pairs + ln.pair);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 q = at[e];
+            cs[2 * e] = make_float2(q.x, q.y);
+            cs[2 * e + 1] = make_float2(q.z, q.w);
+          }
+          if (a.rope.interleaved)
+            rope_turn(true, cs, u, v);
+          else
+            rope_turn(false, cs, u, v);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (ROT) {
+          x[i][e] = u[e];
+          x[i][8 + e] = v[e];
+        }
+        const float mu = fabsf(u[e]), mv = fabsf(v[e]);
+        if (mu <= 3.402823466e38f) amax = fmaxf(amax, mu);
+        if (mv <= 3.402823466e38f) amax = fmaxf(amax, mv);
+      }
+    }
+    amax = warp_max(amax);
+    if (TW > 1) {
+      __syncthreads();  // the turn before has read red
+      if (lane == 0) red[warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < TW; ++i) amax = fmaxf(amax, red[team * TW + i]);
+    }
+    if (!live) continue;
+    const float need = scale_for(amax, FMT);
+    const bool older = p0 < start;         // older rows live in the block
+    const float s = older ? fmaxf(had, need) : need;
+    const float inv = 1.f / s;             // exact: a power of two
+    if (older && s != had) {               // grown: the older rows once more
+      for (int64_t r = row_in; r < start - p0 && r < (warp % TW) * 16 + 16; r += 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint2* at = reinterpret_cast<uint2*>(codes + (row0 + r) * kD + 8 * (h ? ln.b : ln.a));
+          float y[8];
+          decode8<FMT>(*at, had, y);
+          *at = encode8<FMT>(y, inv);
+        }
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(x[i][e]);
-      if (mine && m <= 3.402823466e38f) amax = fmaxf(amax, m);
-    }
-  }
-  amax = warp_max(amax);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  const float had = scales[row0 / BLK];
-  __syncthreads();
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = row_in + 4 * i, pos = p0 + r;
+      if (pos >= start && pos < L) {
+        float u[8], v[8];
+        if constexpr (ROT) {
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
-  const float need = scale_for(amax, FMT);
-  const bool shared_block = p0 < start;  // older rows live in it
-  const float s = shared_block ? fmaxf(had, need) : need;
-  const float inv = 1.f / s;             // exact: a power of two
-  if (shared_block && s != had) {        // grown: the older rows once more
-    for (int64_t r = hw; r < start - p0; r += kAppendRows) {
-      uint2* at = reinterpret_cast<uint2*>(codes + (row0 + r) * kD + 8 * c);
-      float y[8];
-      decode8<FMT>(*at, had, y);
-      *at = encode8<FMT>(y, inv);
+          for (int e = 0; e < 8; ++e) {
+            u[e] = x[i][e];
+            v[e] = x[i][8 + e];
+          }
+        } else {
+          unpack8(w[i][0], u);
+          unpack8(w[i][1], v);
+        }
+        const uint2 cu = encode8<FMT>(u, inv), cv = encode8<FMT>(v, inv);
+        uint8_t* at = codes + (row0 + r) * kD;
+        if (ln.b == ln.a + 1) {
+          *reinterpret_cast<uint4*>(at + 8 * ln.a) = make_uint4(cu.x, cu.y, cv.x, cv.y);
+        } else {
+          *reinterpret_cast<uint2*>(at + 8 * ln.a) = cu;
+          *reinterpret_cast<uint2*>(at + 8 * ln.b) = cv;
+        }
+      }
     }
+    // (every lane of the team has read `had` before the barriers above; a team of
+    // one warp is in step)
+    __syncwarp();
+    if (warp % TW == 0 && lane == 0) scales[row0 / BLK] = s;
   }
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int64_t r = hw + i * kAppendRows, pos = p0 + r;
-    if (pos >= start && pos < L && (BLK >= kAppendRows || hw < BLK))
-      *reinterpret_cast<uint2*>(codes + (row0 + r) * kD + 8 * c) = encode8<FMT>(x[i], inv);
-  }
-  if (threadIdx.x == 0) scales[row0 / BLK] = s;
 }
 
 // A half-warp per (token, KV head).  No early start for the next kernel: what
@@ -180,15 +277,37 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
   *reinterpret_cast<uint4*>(a.v.p + t * a.v.st + g * a.v.sh + 8 * c) = wv;
 }
 
+template <int FMT, int BLK>
+cudaError_t append_block(const AppendArgs& a, cudaStream_t st) {
+  constexpr int TEAMS = kAppendThreads / 32 / (BLK / 16);
+  const int Hkv = a.c.Hkv;
+  // blocks that a sequence can touch
+  const int nb = (int)(((a.max_new < a.T ? a.max_new : a.T) + BLK - 2) / BLK + 1);
+  const dim3 th(kAppendThreads);
+  if (!a.rope.lo) {
+    const dim3 grid((unsigned)(((int64_t)nb * 2 * Hkv + TEAMS - 1) / TEAMS), a.B);
+    return launch_dependent(kv8_append_kernel<FMT, BLK, false>, grid, th, 0, st, a, nb, 1);
+  }
+  // All heads of a block's keys in one CTA where the blocks fill the machine,
+  // else a turn of the teams a CTA (single tokens: latency counts).
+  const int heads = (int64_t)nb * a.B >= 4 * 152 || Hkv < TEAMS ? Hkv : TEAMS;
+  const int parts = (Hkv + heads - 1) / heads;
+  const dim3 grid((unsigned)(nb * parts + ((int64_t)nb * Hkv + TEAMS - 1) / TEAMS), a.B);
+  const size_t smem = (size_t)BLK * a.rope.pairs * sizeof(float2);
+  const cudaError_t e =
+      cudaFuncSetAttribute((const void*)kv8_append_kernel<FMT, BLK, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(BLK * kD * 4));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kv8_append_kernel<FMT, BLK, true>, grid, th, smem, st, a, nb, heads);
+}
+
 template <int FMT>
 cudaError_t append_fmt(const AppendArgs& a, cudaStream_t st) {
-  const int nb = (int)(((int64_t)a.max_new + a.block - 2) / a.block + 1);
-  const dim3 grid(nb, 2 * a.c.Hkv, a.B), th(kAppendThreads);
   switch (a.block) {
-    case 16: return launch_dependent(kv8_append_kernel<FMT, 16>, grid, th, 0, st, a);
-    case 32: return launch_dependent(kv8_append_kernel<FMT, 32>, grid, th, 0, st, a);
-    case 64: return launch_dependent(kv8_append_kernel<FMT, 64>, grid, th, 0, st, a);
-    default: return launch_dependent(kv8_append_kernel<FMT, 128>, grid, th, 0, st, a);
+    case 16: return append_block<FMT, 16>(a, st);
+    case 32: return append_block<FMT, 32>(a, st);
+    case 64: return append_block<FMT, 64>(a, st);
+    default: return append_block<FMT, 128>(a, st);
   }
 }
 
@@ -199,7 +318,8 @@ cudaError_t launch_kv8_append(const AppendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv8_read(const ReadArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)a.max_new + 15) / 16), a.c.Hkv, a.B), th(256);
+  const int64_t most = a.max_new < a.T ? a.max_new : a.T;
+  const dim3 grid((unsigned)((most + 15) / 16), a.c.Hkv, a.B), th(256);
   return a.fmt == kFmtInt8 ? launch_dependent(kv8_read_kernel<kFmtInt8>, grid, th, 0, st, a)
                            : launch_dependent(kv8_read_kernel<kFmtE4m3>, grid, th, 0, st, a);
 }

@@ -25,37 +25,77 @@ __global__ void rope_table_kernel(RopeTableArgs a) {
 }
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 5;   // rows of eight lanes in flight
 
-// One CTA per token: 64 threads combine the token's angles once, then every
-// half-warp turns rows.  It does not let the next kernel start early: the
-// key scan reads q and the keys before its dependency wait.
+// Bandwidth-bound: 2 bytes read and written an element for 3 flop.  Eight lanes
+// keep their token's angles in registers (8 pairs a lane) and turn every WAYS-th
+// head of it, kRopeBatch rows in flight at a time: with four tokens a CTA the angles, 1
+// KB of table from L2, serve 40 rows of 512 bytes moved; with one (few tokens) a
+// token's heads are spread over the whole CTA.  A lane holds both elements of its
+// pairs, so no values change lanes (with 16 lanes a row and shuffles a prompt of 32768
+// tokens, 32 + 8 heads, took 144 us).  It does not let the next kernel start
+// early: the key scan reads q and the keys before its dependency wait.
+template <int TOKENS, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
-  __shared__ float2 cs_s[kD / 2];
+  constexpr int WAYS = kRopeThreads / 8 / TOKENS;
   pdl_wait();
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x < a.rope.pairs) {
-    float2 v = rope_angle(a.rope, a.positions[t], threadIdx.x);
-    if (a.inverse) v.y = -v.y;
-    cs_s[threadIdx.x] = v;
-  }
-  __syncthreads();
-  const int c = threadIdx.x & 15;
-  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
-  const int p0 = rope_pair(a.rope, c);
+  const int slot = threadIdx.x >> 3;
+  const int64_t t = (int64_t)blockIdx.x * TOKENS + slot / WAYS;
+  if (t >= a.T) return;
+  const int H = a.Hq + a.Hkv;
+  const RopeLane ln = rope_lane(a.rope, threadIdx.x & 7);
+  const uint16_t* qi = a.q.p + t * a.q.st + 8 * ln.a;
+  const uint16_t* ki = a.k.p + t * a.k.st + 8 * ln.a;
+  uint16_t* qo = a.qo.p + t * a.qo.st + 8 * ln.a;
+  uint16_t* ko = a.ko.p + t * a.ko.st + 8 * ln.a;
+  const int second = 8 * (ln.b - ln.a);
   float2 cs[8];
+  if (ln.pair >= 0) {
+    const int64_t pos = a.positions[t];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    cs[e] = p0 >= 0 && p0 + e < a.rope.pairs ? cs_s[p0 + e] : make_float2(1.f, 0.f);
-  for (int h = threadIdx.x >> 4; h < a.Hq + a.Hkv; h += kRopeThreads / 16) {
-    const bool isq = h < a.Hq;
-    const RowsView& in = isq ? a.q : a.k;
-    const RowsView& out = isq ? a.qo : a.ko;
-    const int hh = isq ? h : h - a.Hq;
-    float x[8];
-    unpack8(*reinterpret_cast<const uint4*>(in.p + t * in.st + hh * in.sh + 8 * c), x);
-    rope_turn(a.rope, c, mask, cs, x);
-    *reinterpret_cast<uint4*>(out.p + t * out.st + hh * out.sh + 8 * c) = pack8(x);
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = rope_angle(a.rope, pos, ln.pair + e);
+      if (a.inverse) cs[e].y = -cs[e].y;
+    }
   }
+  for (int h0 = slot % WAYS; h0 < H; h0 += WAYS * kRopeBatch) {
+    uint4 w[kRopeBatch][2];
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int h = h0 + i * WAYS;
+      if (h < H) {
+        const uint16_t* p = h < a.Hq ? qi + h * a.q.sh : ki + (h - a.Hq) * a.k.sh;
+        w[i][0] = *reinterpret_cast<const uint4*>(p);
+        w[i][1] = *reinterpret_cast<const uint4*>(p + second);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int h = h0 + i * WAYS;
+      if (h < H) {
+        if (ln.pair >= 0) {
+          float x[8], y[8];
+          unpack8(w[i][0], x);
+          unpack8(w[i][1], y);
+          rope_turn(INTER, cs, x, y);
+          w[i][0] = pack8(x);
+          w[i][1] = pack8(y);
+        }
+        uint16_t* p = h < a.Hq ? qo + h * a.qo.sh : ko + (h - a.Hq) * a.ko.sh;
+        *reinterpret_cast<uint4*>(p) = w[i][0];
+        *reinterpret_cast<uint4*>(p + second) = w[i][1];
+      }
+    }
+  }
+}
+
+template <bool INTER>
+cudaError_t launch_layout(const RopeArgs& a, cudaStream_t st) {
+  // Four tokens a CTA from two CTAs an SM on; below that latency counts.
+  const dim3 th(kRopeThreads);
+  if (a.T < 4 * 2 * 152)
+    return launch_dependent(rope_kernel<1, INTER>, dim3((unsigned)a.T), th, 0, st, a);
+  return launch_dependent(rope_kernel<4, INTER>, dim3((unsigned)((a.T + 3) / 4)), th, 0, st, a);
 }
 
 }  // namespace
@@ -69,7 +109,7 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
-  return launch_dependent(rope_kernel, dim3((unsigned)a.T), dim3(kRopeThreads), 0, st, a);
+  return a.rope.interleaved ? launch_layout<true>(a, st) : launch_layout<false>(a, st);
 }
 
 }  // namespace tsa

@@ -1,5 +1,4 @@
-// rope.cuh -- the rotation of one head row by a half-warp: lane c of 16 holds
-// elements [8c, 8c + 8).
+// rope.cuh -- the rotation of one head row by eight lanes.
 #pragma once
 
 #include "cache_ops.h"
@@ -16,36 +15,32 @@ __device__ __forceinline__ float2 rope_angle(const RopeView& r, int64_t t, int i
   return make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
 }
 
-// First pair of lane c's chunk; -1: the chunk is past rot_dim.
-__device__ __forceinline__ int rope_pair(const RopeView& r, int c) {
-  const int n8 = r.pairs >> 3;
-  if (c >= 2 * n8) return -1;
-  return r.interleaved ? 4 * c : 8 * (c < n8 ? c : c - n8);
+// A row is turned by eight lanes, 16 elements each as two pieces of 8 (lane l's
+// pieces `a` and `b`, numbered in the row), such that a lane holds both elements of its
+// eight pairs: the pieces of both halves in the half layout, neighbours in the
+// interleaved one.  Lanes past rot_dim hold two pieces that are only copied
+// (their pairs: -1).
+struct RopeLane {
+  int a, b, pair;
+};
+__device__ __forceinline__ RopeLane rope_lane(const RopeView& r, int l) {
+  const int n8 = r.pairs >> 3;  // lanes that turn
+  RopeLane x;
+  x.pair = l < n8 ? 8 * l : -1;
+  x.a = r.interleaved || l >= n8 ? 2 * l : l;
+  x.b = r.interleaved || l >= n8 ? 2 * l + 1 : l + n8;
+  return x;
 }
-
-// Rotates the row: x is lane c's chunk; cs[e] the (cos, sin) of pair
-// rope_pair(c) + e (8 of them in the half layout, 4 in the interleaved one).
-// All 16 lanes of the half-warp call it (mask: theirs).
-__device__ __forceinline__ void rope_turn(const RopeView& r, int c, uint32_t mask,
-                                          const float2 (&cs)[8], float (&x)[8]) {
-  const int n8 = r.pairs >> 3;
-  if (r.interleaved) {
-    if (c < 2 * n8) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1];
-        x[2 * e] = a * cs[e].x - b * cs[e].y;
-        x[2 * e + 1] = b * cs[e].x + a * cs[e].y;
-      }
-    }
-    return;
-  }
-  const int src = c < n8 ? c + n8 : (c < 2 * n8 ? c - n8 : c);
-  const float sgn = c < n8 ? -1.f : 1.f;
+__device__ __forceinline__ void rope_turn(bool interleaved, const float2 (&cs)[8], float (&x)[8],
+                                          float (&y)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float o = __shfl_sync(mask, x[e], src, 16);
-    if (c < 2 * n8) x[e] = x[e] * cs[e].x + sgn * (o * cs[e].y);
+    // pair e: (x_e, y_e), or elements 2e and 2e + 1 of x then y
+    float& p = interleaved ? (e < 4 ? x[2 * (e & 3)] : y[2 * (e & 3)]) : x[e];
+    float& q = interleaved ? (e < 4 ? x[2 * (e & 3) + 1] : y[2 * (e & 3) + 1]) : y[e];
+    const float u = p, v = q;
+    p = u * cs[e].x - v * cs[e].y;
+    q = v * cs[e].x + u * cs[e].y;
   }
 }
 

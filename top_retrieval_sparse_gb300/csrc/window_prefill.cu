@@ -657,7 +657,8 @@ cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vm
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
   if (e != cudaSuccess) return e;
   const int tokens = 2 * (kTile / a.G);
-  const dim3 grid((a.max_q + tokens - 1) / tokens, a.c.Hkv, B);
+  const int64_t most = a.max_q < a.T ? a.max_q : a.T;  // of a sequence
+  const dim3 grid((unsigned)((most + tokens - 1) / tokens), a.c.Hkv, B);
   return launch_dependent(window_prefill_kernel, grid, dim3(kPreThreads), kPreSmem, st, kmap, vmap,
                           a);
 }
