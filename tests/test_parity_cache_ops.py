@@ -681,7 +681,11 @@ PREFILL_CASES = [  # Hq, Hkv, cap, page, lens, news, n_init, n_recent
     (14, 2, 2048, 128, [2047, 1025], [1000, 1025], 1, 129), (12, 4, 1500, 0, [1499], [1499], 64, 512),
     (7, 1, 1024, 16, list(range(10, 1010, 100)), [10, 100, 3, 7, 200, 1, 64, 65, 128, 9], 2, 77),
     (4, 4, 256, 0, [3, 256], [5, 256], 2, 300),   # more tokens than positions
-    (16, 2, 8192, 0, [8192], [17], 16, None)]
+    (16, 2, 8192, 0, [8192], [17], 16, None),
+    # few queries over many rows: their key tiles are split over CTAs
+    (28, 4, 16384, 16, [16384, 9000], [1, 16], 4, None), (4, 1, 20000, 0, [19999], [40], 0, 9000),
+    (32, 8, 8192, 64, [8000], [2], 130, 700), (1, 1, 30000, 0, [29999], [129], 300, None),
+    (8, 1, 4096, 256, [4096, 5, 0], [3, 5, 1], 0, 600)]
 
 
 @pytest.mark.parametrize("case", PREFILL_CASES, ids=range(len(PREFILL_CASES)))
@@ -730,6 +734,31 @@ def test_prefill_uniform_batch_and_too_many_tokens(tsa):
     assert tsa.workspace_status(ws) == -5
     assert torch.isnan(c[40:80]).all() and torch.equal(c[:40], a[:40])
     assert torch.isfinite(c[81:]).all()
+
+
+def test_prefill_calls_of_all_sizes_share_a_workspace(tsa):
+    """Split and whole calls by turns, eager and captured, on one workspace."""
+    g = gen(14)
+    kv, _ = bf16_cache(tsa, g, 2, 2, 8192, 32)
+    q = randn(g, 700, 8, D).bfloat16()
+    calls = [([8192, 8000], 1), ([8192, 100], 350), ([5000], 16), ([40, 8191], 33), ([8192], 700)]
+    ws = torch.zeros(max(tsa.window_attn_prefill_workspace(len(ls), 8, 2, n, 8192, 4, 6000).numel()
+                         for ls, n in calls), dtype=torch.uint8, device=DEV)
+    want = [tsa.window_attn_prefill(q[:len(ls) * n], kv, i32(ls), 4, 6000)[0] for ls, n in calls]
+    for _ in range(2):
+        for (ls, n), w in zip(calls, want):
+            got, _ = tsa.window_attn_prefill(q[:len(ls) * n], kv, i32(ls), 4, 6000, workspace=ws)
+            assert torch.equal(got, w)
+    lens, out, gr = i32(calls[0][0]), torch.empty_like(want[0]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        tsa.window_attn_prefill(q[:2], kv, lens, 4, 6000, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        gr.replay()
+        assert torch.equal(out, want[0])
+        assert torch.equal(tsa.window_attn_prefill(q[:16], kv, i32(calls[2][0]), 4, 6000,
+                                                   workspace=ws)[0], want[2])
+    assert tsa.workspace_status(ws) == 0
 
 
 def test_prefill_of_one_token_is_the_decode_step(tsa):

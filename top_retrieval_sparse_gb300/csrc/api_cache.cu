@@ -226,6 +226,42 @@ constexpr size_t kDecodePartial = kAlign;
 constexpr size_t kDecodeArrived =
     kDecodePartial + (size_t)2 * kDecodeShares * kDecodeSlot * sizeof(float);
 
+// How the prefill kernel cuts a call: CTAs of 2 * floor(128 / G) tokens each, and
+// where those are at most half the SMs, each one's key tiles over several.  A
+// part saves the tiles that others take (1.3 us each) and costs its partial and a
+// share of joining them: at most 8 for full tiles, more for few rows, never below two
+// tiles (16 tokens late in a window of 4096, 33 tiles a head: 60 us in one CTA).
+struct PrefillCut {
+  int64_t blocks, splits, units;
+};
+PrefillCut prefill_cut(int B, int Hkv, int G, int64_t max_q, int64_t l_cap, int64_t n_init,
+                       int64_t n_recent) {
+  PrefillCut c{0, 1, 0};
+  const int64_t tokens = 2 * (128 / G);
+  c.blocks = (max_q + tokens - 1) / tokens;
+  c.units = c.blocks * B * Hkv;
+  const int64_t sms = 152;  // (not the device's: sizes do not depend on where they are asked)
+  if (c.units < 1 || c.units > sms / 2) return c;
+  const int64_t q = max_q < tokens ? max_q : tokens;
+  auto tiles = [&](int64_t rows) { return ((rows < l_cap ? rows : l_cap) + 127) / 128; };
+  int64_t n = tiles(n_init < l_cap ? n_init : l_cap) + 1 +
+              tiles((n_recent < l_cap ? n_recent : l_cap) + q);
+  if (n > tiles(l_cap)) n = tiles(l_cap);
+  const int64_t rows = max_q * G < 128 ? max_q * G : 128;
+  c.splits = sms / c.units;
+  if (c.splits > (n + 1) / 2) c.splits = (n + 1) / 2;
+  if (c.splits > 8 * 128 / rows) c.splits = 8 * 128 / rows;
+  if (c.splits > 32) c.splits = 32;
+  if (c.splits < 1) c.splits = 1;
+  return c;
+}
+// Workspace: the status word, the partials.
+constexpr size_t kPrePartial = kAlign;
+size_t prefill_bytes(const PrefillCut& c) {
+  return kPrePartial + (c.splits > 1 ? (size_t)(c.units * c.splits) * 2 * kPreSlot * sizeof(float)
+                                     : 0);
+}
+
 // Both decode entry points after their cache's checks.
 int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, int B, int Hq,
                int Hkv, int64_t n_init, int64_t n_recent, float scale, float* out,
@@ -465,9 +501,9 @@ int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int
 size_t window_attn_prefill_workspace_size(int B, int Hq, int Hkv, int d, int max_q, int64_t l_cap,
                                           int64_t n_init, int64_t n_recent) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || d != kD || max_q < 0 || l_cap <= 0 || n_init < 0 ||
-      n_recent < 0)
+      n_recent < 0 || Hq % Hkv || Hq / Hkv > kMaxGroup)
     return 0;
-  return kAlign;
+  return prefill_bytes(prefill_cut(B, Hkv, Hq / Hkv, max_q, l_cap, n_init, n_recent));
 }
 
 int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q, int64_t T,
@@ -486,10 +522,8 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
   if ((rc = check_rows(q, T, Hq, false, "q", a.q))) return rc;
   if (!out || !lens) return fail(TSA_ERR_INVALID_ARG, "out and lens must be non-NULL");
   if (!aligned(out, 16)) return fail(TSA_ERR_INVALID_ARG, "out must be 16-byte aligned");
-  if ((rc = check_workspace(workspace, ws_bytes,
-                            window_attn_prefill_workspace_size(B, Hq, Hkv, d, max_q, kv->l_cap,
-                                                               n_init, n_recent))))
-    return rc;
+  const PrefillCut cut = prefill_cut(B, Hkv, Hq / Hkv, max_q, kv->l_cap, n_init, n_recent);
+  if ((rc = check_workspace(workspace, ws_bytes, prefill_bytes(cut)))) return rc;
   CUtensorMap kmap, vmap;
   const int box = kv->page_table && kv->page_size < 128 ? kv->page_size : 128;
   const int64_t rows = kv->page_table ? 0x7fffffff : (int64_t)B * Hkv * kv->l_cap;
@@ -510,9 +544,17 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
   a.box = box;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse_out;
-  a.status = static_cast<int*>(workspace);
-  return launched(launch_window_prefill(kmap, vmap, a, B, static_cast<cudaStream_t>(stream)),
-                  "attention launch");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<int*>(ws);
+  a.partial = reinterpret_cast<float*>(ws + kPrePartial);
+  a.splits = (int)cut.splits;
+  // no sequence has more than T tokens, whatever max_q says
+  const int64_t tokens = 2 * (128 / a.G), most = max_q < T ? max_q : T;
+  a.blocks = (int)((most + tokens - 1) / tokens);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = launched(launch_window_prefill(kmap, vmap, a, B, st), "attention launch");
+  if (rc || a.splits == 1) return rc;
+  return launched(launch_window_join(a, B, st), "join launch");
 }
 
 }  // extern "C"

@@ -140,6 +140,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStrea
 
 // Many tokens per sequence (window_prefill.cu); the maps are the bf16 pool's
 // rows of 128 elements, in boxes of 64 elements by `box` rows.
+constexpr int kPreSlot = 2 * 128 + 128 * kD;  // floats of a query tile's partial
 struct PrefillArgs {
   RowsView q;
   CacheView c;
@@ -155,9 +156,12 @@ struct PrefillArgs {
   uint16_t* out;       // bf16 [T][Hq][128]
   float* lse;          // [T][Hq] or nullptr
   int* status;
+  int blocks, splits;  // CTAs of a sequence's tokens, and of each one's key tiles
+  float* partial;      // [B * Hkv * blocks][splits][2][kPreSlot] (splits > 1)
 };
 cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const PrefillArgs& a, int B, cudaStream_t st);
+cudaError_t launch_window_join(const PrefillArgs& a, int B, cudaStream_t st);  // splits > 1
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // every such kernel calls pdl_wait() before it touches memory.

@@ -21,6 +21,10 @@
 // sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the weights
 // have grown by more than 2^16.
 //
+// Few queries (fewer CTAs than half the SMs) share the key tiles of a CTA's queries out
+// over several; each leaves (O, maximum, sum) in the workspace, and a second kernel
+// joins them, a warp a row (the last CTA to arrive doing it took 10 us).
+//
 // Masks cost nothing but at the edges of what is seen: there the rows' columns are
 // masked one by one, and rows of V that no query of the CTA sees are zeroed in
 // shared memory (whatever they hold, 0 * NaN would reach the output).
@@ -222,11 +226,19 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// What a CTA's queries see: rows [0, n0) and [lo, end), as key tiles: [0, s0)
-// and [sw, se).
+// What a CTA's queries see: rows [0, n0) and [lo, end), as a list of `all` key tiles:
+// [0, s0) and from sw; the CTA takes n of them from number `from` on.
 struct Span {
-  int n0, lo, end, s0, sw, n;
-  __device__ int tile(int j) const { return j < s0 ? j : sw + (j - s0); }
+  int n0, lo, end, s0, sw, all, from, n;
+  __device__ int tile(int j) const {
+    j += from;
+    return j < s0 ? j : sw + (j - s0);
+  }
+  // Tile j may hold rows that nothing sees.
+  __device__ bool edge(int j) const {
+    j += from;
+    return j == s0 - 1 || j == s0 || j == all - 1;
+  }
   __device__ bool sees(int r) const { return r < end && (r < n0 || r >= lo); }
 };
 
@@ -270,7 +282,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     if (n64 > a.max_q) n64 = a.max_q;
   }
   const int n = (int)n64;
-  const int t0 = (int)(gridDim.x - 1 - blockIdx.x) * 2 * TQ;
+  const int block = a.blocks - 1 - (int)blockIdx.x / a.splits;
+  const int t0 = block * 2 * TQ;
   if (t0 >= n) return;
   const int t1 = t0 + 2 * TQ < n ? t0 + 2 * TQ : n;
   int L = a.lens[b];
@@ -289,7 +302,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   v.s0 = (v.n0 + kTile - 1) / kTile;
   v.sw = v.lo / kTile > v.s0 ? v.lo / kTile : v.s0;
   const int se = (v.end + kTile - 1) / kTile;
-  v.n = v.s0 + (v.lo < v.end && se > v.sw ? se - v.sw : 0);
+  v.all = v.s0 + (v.lo < v.end && se > v.sw ? se - v.sw : 0);
+  const int part = blockIdx.x % a.splits;    // of the key tiles
+  v.from = (int)((int64_t)v.all * part / a.splits);
+  v.n = (int)((int64_t)v.all * (part + 1) / a.splits) - v.from;
   const bool two = t1 - t0 > TQ;             // tile B has tokens
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -469,11 +485,36 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ok = wait(&bar.o[x], 0);
         fence_after();
       }
-      const bool nan = !ok || bad_s;
-      const float inv = nan ? nanf("") : (l > 0.f ? 1.f / l : 0.f);
+      if (!ok || bad_s) {
+        l = nanf("");
+        if (m == -INFINITY) m = 0.f;
+      }
+      if (a.splits > 1) {  // a partial for the kernel that joins them
+        const size_t unit = ((size_t)b * a.c.Hkv + g) * a.blocks + block;
+        float* mine = a.partial + ((unit * a.splits + part) * 2 + x) * kPreSlot;
+        if (live) {
+          mine[r] = m * sc;
+          mine[kTile + r] = l;
+        }
+        if (v.n > 0 && ok) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            load_cols(o_at + 32 * c, o);
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(mine + 2 * kTile + r * kD + 32 * c + 4 * i) =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      const bool sums = v.n > 0 && ok, write = a.splits == 1;
+      const bool nan = l != l;
+      const float inv = nan ? l : (l > 0.f ? 1.f / l : 0.f);
       // A row's 256 bytes go through the warp's own rows of Q's tile, which the
       // products have read, so that a half-warp stores them in one request.
-      if (v.n > 0 && ok) {
+      if (write && sums) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float o[32];
@@ -490,24 +531,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         __syncwarp();
       }
+      // without sums every row of the CTA is blank: 0, or NaN after a failure
       const uint32_t blank = nan ? 0x7fff7fffu : 0u;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int rr = r_warp + 2 * i + r_half, tt = (rr * a.inv_g) >> 16;
         uint4 w = make_uint4(blank, blank, blank, blank);
-        if (v.n > 0 && ok)
+        if (sums)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                        : "r"(q_mine + rr * 256 + ((piece ^ (rr & 7)) << 4))
                        : "memory");
-        if (tt < TQ && t0 + x * TQ + tt < t1)
+        if (write && tt < TQ && t0 + x * TQ + tt < t1)
           *reinterpret_cast<uint4*>(a.out +
                                     ((tok + t0 + x * TQ + tt) * a.Hq + g * G + rr - tt * G) * kD +
                                     8 * piece) = w;
       }
-      if (live && a.lse)
+      if (write && live && a.lse)
         a.lse[(tok + my_t) * a.Hq + h] =
-            nan ? nanf("") : (l > 0.f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY);
+            nan ? l : (l > 0.f ? (m * sc + log2f(l)) * 0.6931471805599453f : -INFINITY);
     }
   } else {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -515,8 +557,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     // ------------------------------------------------ matrix instructions
     // One thread for each query tile (issuing all of them is more than one
     // thread can do in time), by turns: O_A(j), S_A(j+1), then O_B(j), S_B(j+1),
-    // so that one tile's softmax runs under the other's products.  K tile j is in the ring's slot of 2j, V tile j in
-    // that of 2j + 1.
+    // so that one tile's softmax runs under the other's products.  K tile j is in
+    // the ring's slot of 2j, V tile j in that of 2j + 1.
     const int x = warp == 3;
     if ((x == 0 || two) && elect_one()) {
       const uint32_t s_at = tmem + x * kTile, o_at = s_at + 2 * kTile;
@@ -542,7 +584,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       int slot = 1, lap = 0;                 // of V tile j
       for (int j = 0; j < v.n && ok; ++j) {
         ok = wait_for(&bar.full[slot], lap, &abort_s);
-        if (ok && (j == v.s0 - 1 || j == v.s0 || j == v.n - 1))  // may hold unseen rows
+        if (ok && v.edge(j))
           ok = wait_for(&bar.clean[j % kSlots], (j / kSlots) & 1, &abort_s);
         const uint64_t vx = vd + slot * (kSlotBytes >> 4);
 #pragma unroll
@@ -649,6 +691,50 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
 }
 
+// Joins the partials of a row (token, query head): a warp a row, lanes over the
+// partials' maxima and sums, then over the columns.
+__global__ void __launch_bounds__(256) window_join_kernel(PrefillArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.z;
+  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int64_t tok, n;
+  if (!seq_tokens(a.cu, a.max_q, a.T, b, tok, n)) {
+    if (tok < 0 || n < 0 || tok + n > a.T) return;
+    if (n > a.max_q) n = a.max_q;
+  }
+  const int64_t j = item / a.Hq;
+  const int h = (int)(item % a.Hq), g = h / a.G, TQ = kTile / a.G;
+  if (j >= n) return;
+  const int block = (int)(j / (2 * TQ)), in = (int)(j % (2 * TQ)), x = in / TQ;
+  const int r = (in % TQ) * a.G + h % a.G;
+  const size_t unit = ((size_t)b * a.c.Hkv + g) * a.blocks + block;
+  const float* p = a.partial + (unit * a.splits * 2 + x) * kPreSlot;
+  const size_t step = 2 * (size_t)kPreSlot;  // to the next part; there are at most 32
+  const float m = lane < a.splits ? p[lane * step + r] : -INFINITY;
+  const float top = warp_max(m);
+  const float f = m == -INFINITY ? 0.f : ex2(m - top);
+  const float l = warp_sum(lane < a.splits ? p[lane * step + kTile + r] * f : 0.f);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < a.splits; ++k) {
+    const float w = __shfl_sync(0xffffffffu, f, k);
+    if (w > 0.f) {  // (a part that has seen nothing has left no sums)
+      const float4 u =
+          *reinterpret_cast<const float4*>(p + k * step + 2 * kTile + r * kD + 4 * lane);
+      o.x = fmaf(u.x, w, o.x); o.y = fmaf(u.y, w, o.y);
+      o.z = fmaf(u.z, w, o.z); o.w = fmaf(u.w, w, o.w);
+    }
+  }
+  const bool nan = l != l;
+  const float inv = nan ? l : (l > 0.f ? 1.f / l : 0.f);
+  const int64_t at = (tok + j) * a.Hq + h;
+  *reinterpret_cast<uint2*>(a.out + at * kD + 4 * lane) =
+      make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[at] = nan ? l : (l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY);
+}
+
 }  // namespace
 
 cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
@@ -656,11 +742,15 @@ cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vm
   cudaError_t e = cudaFuncSetAttribute((const void*)window_prefill_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
   if (e != cudaSuccess) return e;
-  const int tokens = 2 * (kTile / a.G);
-  const int64_t most = a.max_q < a.T ? a.max_q : a.T;  // of a sequence
-  const dim3 grid((unsigned)((most + tokens - 1) / tokens), a.c.Hkv, B);
+  const dim3 grid((unsigned)(a.blocks * a.splits), a.c.Hkv, B);
   return launch_dependent(window_prefill_kernel, grid, dim3(kPreThreads), kPreSmem, st, kmap, vmap,
                           a);
+}
+
+cudaError_t launch_window_join(const PrefillArgs& a, int B, cudaStream_t st) {
+  const int64_t rows = (a.max_q < a.T ? a.max_q : a.T) * a.Hq;  // of a sequence
+  return launch_dependent(window_join_kernel, dim3((unsigned)((rows + 7) / 8), 1, B), dim3(256), 0,
+                          st, a);
 }
 
 }  // namespace tsa
