@@ -8,32 +8,53 @@ namespace tsa {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+enum { kStraight = 0, kTurnHalf = 1, kTurnInterleaved = 2 };
 
-// Smallest e >= -60 with top * 2^e >= amax (finite), top = 127 or 448:
-// amax = m * 2^x with m in [1, 2) and top = 1.984375 * 2^6 or 1.75 * 2^8.
+// Threads of an append CTA: one team of warps, so that none waits at another's
+// barriers (128K tokens of 8 heads, blocks of 64: 157 us with two teams a CTA, 117 us with
+// one); teams of one warp have no barriers, and there are eight.
+__host__ __device__ constexpr int append_threads(int blk) { return blk == 16 ? 256 : 2 * blk; }
+
+// 2^e for the smallest e >= -60 with top * 2^e >= amax (finite, >= 0), top = 127
+// or 448 = 1.984375 * 2^6 or 1.75 * 2^8: from amax's exponent and mantissa.
 __device__ __forceinline__ float scale_for(float amax, int fmt) {
-  if (!(amax > 0.f)) return ldexpf(1.f, -60);
-  int x;
-  const float m = 2.f * frexpf(amax, &x);  // in [1, 2), amax = m * 2^(x - 1)
-  --x;
-  int e = fmt == kFmtInt8 ? (m <= 1.984375f ? x - 6 : x - 5) : (m <= 1.75f ? x - 8 : x - 7);
-  if (e < -60) e = -60;
-  return ldexpf(1.f, e);
+  const uint32_t u = __float_as_uint(amax), m = u & 0x7fffffu;
+  int e = (int)(u >> 23) - 127 - (fmt == kFmtInt8 ? 6 : 8) +
+          (m > (fmt == kFmtInt8 ? 0x7e0000u : 0x600000u));
+  e = e < -60 ? -60 : e;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  float r;
+  asm("{\n .reg .f32 t;\n abs.f32 t, %2;\n max.NaN.f32 %0, %1, t;\n}\n"
+      : "=f"(r) : "f"(m), "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {  // of bf16 pairs
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+  return r;
 }
 
 // Codes of eight values.  int8: 1.5 * 2^23 + 128 is added, which rounds to whole
-// numbers (ties to even) and leaves code + 128 in the low byte; infinities
+// numbers (ties to even) and leaves code + 128 in the low byte: one fused operation
+// where every value is finite (CLEAN: the scale then holds them); else infinities
 // saturate and NaN becomes 0.
-template <int FMT>
+template <int FMT, bool CLEAN>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   if constexpr (FMT == kFmtInt8) {
     uint32_t b[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float y = x[e] * inv;
-      y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
-      b[e] = __float_as_uint(y + 12583040.f);
+      if (CLEAN) {
+        b[e] = __float_as_uint(fmaf(x[e], inv, 12583040.f));
+      } else {
+        float y = x[e] * inv;
+        y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
+        b[e] = __float_as_uint(y + 12583040.f);
+      }
     }
     const uint32_t lo0 = __byte_perm(b[0], b[1], 0x0040), hi0 = __byte_perm(b[2], b[3], 0x0040);
     const uint32_t lo1 = __byte_perm(b[4], b[5], 0x0040), hi1 = __byte_perm(b[6], b[7], 0x0040);
@@ -48,36 +69,49 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   }
 }
 
+// Values of eight codes (exact).  int8: a byte under the exponent of 2^23 is the
+// number 2^23 + code + 128.
 template <int FMT>
 __device__ __forceinline__ void decode8(uint2 w, float scale, float (&x)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = ((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xffu;
-    if (FMT == kFmtInt8) {
-      x[e] = (float)((int)b - 128) * scale;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u = h ? w.y : w.x;
+    if constexpr (FMT == kFmtInt8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[4 * h + e] =
+            (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + e)) - 8388736.f) * scale;
     } else {
-      const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
-      x[e] = __half2float(__half(h)) * scale;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const __half2_raw r =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> (16 * e)), __NV_E4M3);
+        const float2 f = __half22float2(__half2(r));
+        x[4 * h + 2 * e] = f.x * scale;
+        x[4 * h + 2 * e + 1] = f.y * scale;
+      }
     }
   }
 }
 
 // Bandwidth-bound: a row's 256 bytes are read once and written as 128.  The new
-// rows of one (block, KV head, K or V) stay in the registers of BLK / 16 warps (a team;
-// 16 rows a warp, eight lanes a row, 128 bytes a lane in flight) between the search
-// for their largest magnitude and their coding.  With ROT the keys' angles are the same for
-// every KV head, so a CTA puts those of the block's rows into shared memory once
-// and its teams go through `heads` heads; blockIdx.x < nb is then the keys of block
-// blockIdx.x, and the rest are the values, a team each, as without a rotation.
-template <int FMT, int BLK, bool ROT>
-__global__ void __launch_bounds__(kAppendThreads, ROT ? 2 : 3)
-    kv8_append_kernel(AppendArgs a, int nb, int heads) {
-  constexpr int TW = BLK / 16, TEAMS = kAppendThreads / 32 / TW;
-  extern __shared__ float2 angle_s[];       // [BLK][pairs] (ROT)
-  __shared__ float red[kAppendThreads / 32];
+// rows of one (block, KV head, K or V) stay in the registers of BLK / 16 warps (a team; 16
+// rows a warp, eight lanes a row, 128 bytes a lane in flight) between the search for
+// their largest magnitude and their coding.  Neighbouring teams take the heads of one
+// block, whose rows are neighbours in memory.  Keys are rotated (KIND) by angles from the
+// table in L2, 512 bytes a row, which each head's team reads for itself: sharing them
+// between the heads in shared memory made a CTA go through the heads one after another
+// over strided reads (227 us for 128K tokens of 8 heads, 194 us so).  128K tokens without a
+// rotation: 117 us, 6.9 TB/s; with it the rotated rows' registers leave 16 warps an SM, and
+// what they wait for bounds it.
+template <int FMT, int BLK, int KIND>
+__global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / append_threads(BLK))
+    kv8_append_kernel(AppendArgs a, int nb) {
+  constexpr int TW = BLK / 16, TEAMS = append_threads(BLK) / 32 / TW;
+  __shared__ float red[append_threads(BLK) / 32];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.y, Hkv = a.c.Hkv;
+  const int b = blockIdx.y;
   int64_t tok, n;
   const int64_t L = a.lens[b];
   const bool good = seq_tokens(a.cu, a.max_new, a.T, b, tok, n);
@@ -89,216 +123,251 @@ __global__ void __launch_bounds__(kAppendThreads, ROT ? 2 : 3)
   const int64_t start = L - n;
   const int warp = threadIdx.x >> 5, team = warp / TW, lane = threadIdx.x & 31, l = lane & 7;
   const int row_in = (warp % TW) * 16 + (lane >> 3);  // rows row_in + 4 i of the block
-
-  // This CTA's items: (block, head, K or V) of its teams.
-  const int parts = (Hkv + heads - 1) / heads;        // CTAs of a block's keys
-  const bool turn = ROT && (int)blockIdx.x < nb * parts;
-  int64_t j = 0;                                      // block, counted from start's
-  int g0 = 0, g1 = 0, which = 0;                      // team's heads: g0, g0 + TEAMS, ... < g1
-  if (turn) {
-    j = blockIdx.x / parts;
-    g0 = (blockIdx.x % parts) * heads;
-    g1 = g0 + heads < Hkv ? g0 + heads : Hkv;
-    g0 += team;
-  } else {
-    // item i: head i % Hkv of block i / Hkv; K then V within a block without ROT
-    const int64_t i = (int64_t)(blockIdx.x - (ROT ? nb * parts : 0)) * TEAMS + team;
-    which = ROT ? 1 : (int)((i / Hkv) & 1);
-    j = ROT ? i / Hkv : i / (2 * Hkv);
-    g0 = (int)(i % Hkv);
-    g1 = g0 + 1;
-  }
-  const int64_t p0 = (start / BLK + j) * BLK;         // the block's first position
-  const bool any = j < nb && p0 < L;
+  // Team's item: head g of K, then of V, of block j (counted from start's).
+  const uint32_t item = blockIdx.x * TEAMS + team, half = item / a.c.Hkv;
+  const int g = (int)(item - half * a.c.Hkv);
+  const bool values = half & 1;
+  const int64_t j = half >> 1, p0 = (start / BLK + j) * BLK;  // the block's first position
+  const int64_t tok0 = tok + p0 - start;                      // token of its row 0
+  // rows [r0, r1) are new
+  const int r0 = start > p0 ? (int)(start - p0) : 0;
+  const int r1 = j >= nb || p0 >= L ? 0 : (L - p0 < BLK ? (int)(L - p0) : BLK);
+  const bool turn = KIND && !values;
   RopeLane ln = {2 * l, 2 * l + 1, -1};
-  if (ROT && turn) {
-    if (!any) return;                                 // the whole CTA: one block
-    ln = rope_lane(a.rope, l);
-    for (int e = threadIdx.x; e < BLK * a.rope.pairs; e += kAppendThreads) {
-      const int64_t pos = p0 + e / a.rope.pairs;
-      if (pos < start || pos >= L) continue;
-      const int64_t at = a.positions ? (int64_t)a.positions[tok + pos - start] : pos;
-      angle_s[e] = rope_angle(a.rope, at, e % a.rope.pairs);
-      if ((at < 0 || at >= a.rope.max_pos) && a.status) atomicOr(a.status, kStatusBadLength);
-    }
-    __syncthreads();
+  if (turn) ln = rope_lane(a.rope, l);
+  const RowsView& in = values ? a.v : a.k;
+  uint8_t* codes = values ? a.c.v : a.c.k;
+  float* scales = values ? a.c.vs : a.c.ks;
+  int64_t row0 = -1;                                  // of the block in the pool
+  float old = 0.f;
+  if (r1 > 0) {
+    row0 = cache_row(a.c, b, g, p0);
+    if (row0 < 0 && lane == 0 && a.status) atomicOr(a.status, kStatusBadLength);
   }
-  const RowsView& in = which ? a.v : a.k;
-  uint8_t* codes = which ? a.c.v : a.c.k;
-  float* scales = which ? a.c.vs : a.c.ks;
-  const int turns = ROT && turn ? (heads + TEAMS - 1) / TEAMS : 1;
-  for (int it = 0; it < turns; ++it) {
-    const int g = g0 + it * TEAMS;
-    int64_t row0 = -1;
-    if (any && g < g1) {
-      row0 = cache_row(a.c, b, g, p0);
-      if (row0 < 0 && lane == 0 && a.status) atomicOr(a.status, kStatusBadLength);
-    }
-    const bool live = row0 >= 0;
-    float x[ROT ? 4 : 1][16];  // rotated rows; without ROT they are widened again below
-    float amax = 0.f, had = 0.f;
-    uint4 w[4][2];
+  const bool live = row0 >= 0;
+  if (live) old = scales[row0 / BLK];
+  uint4 w[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t pos = p0 + row_in + 4 * i;
-      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && pos >= start && pos < L) {
-        const uint16_t* p = in.p + (tok + pos - start) * in.st + g * in.sh;
-        w[i][0] = *reinterpret_cast<const uint4*>(p + 8 * ln.a);
-        w[i][1] = *reinterpret_cast<const uint4*>(p + 8 * ln.b);
+  for (int i = 0; i < 4; ++i) {
+    const int r = row_in + 4 * i;
+    w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (live && r >= r0 && r < r1) {
+      const uint16_t* p = in.p + (tok0 + r) * in.st + g * in.sh;
+      w[i][0] = *reinterpret_cast<const uint4*>(p + 8 * ln.a);
+      w[i][1] = *reinterpret_cast<const uint4*>(p + 8 * ln.b);
+    }
+  }
+  // Rotated rows in 32 bits (KIND); otherwise they are widened where they are used.
+  // A block's own positions share the table's high angle (128 divides kRopeLow), and
+  // the low ones are asked for with the rows, not after them.
+  float x[KIND ? 4 : 1][16];
+  if constexpr (KIND != kStraight) {
+    const bool own = turn && live && !a.positions && p0 + r1 <= a.rope.max_pos;
+    float4 lo[4][4], hi[4];
+    if (own && ln.pair >= 0) {
+      const int n8 = a.rope.pairs >> 3;
+      const float4* h = reinterpret_cast<const float4*>(
+                            a.rope.hi + (p0 >> kRopeLowBits) * a.rope.pairs) + l;
+      const float4* q = reinterpret_cast<const float4*>(
+                            a.rope.lo + ((p0 & (kRopeLow - 1)) + row_in) * a.rope.pairs) + l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = h[n8 * e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i][e] = q[2 * a.rope.pairs * i + n8 * e];
       }
     }
-    if (live) had = scales[row0 / BLK];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int r = row_in + 4 * i;
       float u[8], v[8];
       unpack8(w[i][0], u);
       unpack8(w[i][1], v);
-      if (ROT && turn) {
-        const int64_t pos = p0 + row_in + 4 * i;
-        if (live && ln.pair >= 0 && pos >= start && pos < L) {
-          float2 cs[8];
-          const float4* at =
-              reinterpret_cast<const float4*>(angle_s + (row_in + 4 * i) * a.rope.pairs + ln.pair);
+      if (ln.pair >= 0 && live && r >= r0 && r < r1) {
+        float2 cs[8];
+        if (own) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 q = at[e];
-            cs[2 * e] = make_float2(q.x, q.y);
-            cs[2 * e + 1] = make_float2(q.z, q.w);
-          }
-          if (a.rope.interleaved)
-            rope_turn(true, cs, u, v);
-          else
-            rope_turn(false, cs, u, v);
+          for (int e = 0; e < 4; ++e) rope_sum(lo[i][e], hi[e], cs[2 * e], cs[2 * e + 1]);
+        } else {
+          const int64_t at = a.positions ? (int64_t)a.positions[tok0 + r] : p0 + r;
+          rope_angles(a.rope, at, l, cs);
+          if (l == 0 && (at < 0 || at >= a.rope.max_pos) && a.status)
+            atomicOr(a.status, kStatusBadLength);
         }
+        rope_turn(KIND == kTurnInterleaved, cs, u, v);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if constexpr (ROT) {
-          x[i][e] = u[e];
-          x[i][8 + e] = v[e];
-        }
+        x[i][e] = u[e];
+        x[i][8 + e] = v[e];
+      }
+    }
+  }
+  auto row_values = [&](int i, float (&u)[8], float (&v)[8]) {
+    if constexpr (KIND != kStraight) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[e] = x[i][e];
+        v[e] = x[i][8 + e];
+      }
+    } else {
+      unpack8(w[i][0], u);
+      unpack8(w[i][1], v);
+    }
+  };
+  // Largest magnitude, NaN or infinite where a value is (rows that are not new are
+  // zeros here).
+  float amax = 0.f;
+  if constexpr (KIND != kStraight) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = max_abs(amax, x[i][e]);
+  } else {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        m = max_abs2(max_abs2(max_abs2(max_abs2(m, w[i][h].x), w[i][h].y), w[i][h].z), w[i][h].w);
+    amax = max_abs(bf_lo(m), bf_hi(m));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const bool clean = amax <= 3.402823466e38f;  // of this warp
+  if (!clean) {                                // once more, of what is finite
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float u[8], v[8];
+      row_values(i, u, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
         const float mu = fabsf(u[e]), mv = fabsf(v[e]);
         if (mu <= 3.402823466e38f) amax = fmaxf(amax, mu);
         if (mv <= 3.402823466e38f) amax = fmaxf(amax, mv);
       }
     }
     amax = warp_max(amax);
-    if (TW > 1) {
-      __syncthreads();  // the turn before has read red
-      if (lane == 0) red[warp] = amax;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < TW; ++i) amax = fmaxf(amax, red[team * TW + i]);
-    }
-    if (!live) continue;
-    const float need = scale_for(amax, FMT);
-    const bool older = p0 < start;         // older rows live in the block
-    const float s = older ? fmaxf(had, need) : need;
-    const float inv = 1.f / s;             // exact: a power of two
-    if (older && s != had) {               // grown: the older rows once more
-      for (int64_t r = row_in; r < start - p0 && r < (warp % TW) * 16 + 16; r += 4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint2* at = reinterpret_cast<uint2*>(codes + (row0 + r) * kD + 8 * (h ? ln.b : ln.a));
-          float y[8];
-          decode8<FMT>(*at, had, y);
-          *at = encode8<FMT>(y, inv);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = row_in + 4 * i, pos = p0 + r;
-      if (pos >= start && pos < L) {
-        float u[8], v[8];
-        if constexpr (ROT) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            u[e] = x[i][e];
-            v[e] = x[i][8 + e];
-          }
-        } else {
-          unpack8(w[i][0], u);
-          unpack8(w[i][1], v);
-        }
-        const uint2 cu = encode8<FMT>(u, inv), cv = encode8<FMT>(v, inv);
-        uint8_t* at = codes + (row0 + r) * kD;
-        if (ln.b == ln.a + 1) {
-          *reinterpret_cast<uint4*>(at + 8 * ln.a) = make_uint4(cu.x, cu.y, cv.x, cv.y);
-        } else {
-          *reinterpret_cast<uint2*>(at + 8 * ln.a) = cu;
-          *reinterpret_cast<uint2*>(at + 8 * ln.b) = cv;
-        }
-      }
-    }
-    // (every lane of the team has read `had` before the barriers above; a team of
-    // one warp is in step)
-    __syncwarp();
-    if (warp % TW == 0 && lane == 0) scales[row0 / BLK] = s;
   }
+  if (TW > 1) {
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TW; ++i) amax = fmaxf(amax, red[team * TW + i]);
+  }
+  if (!live) return;
+  const float need = scale_for(amax, FMT);
+  const bool older = r0 > 0;                   // older rows live in the block
+  const float s = older ? fmaxf(old, need) : need;
+  const float inv = 1.f / s;                   // exact: a power of two
+  uint8_t* out = codes + row0 * kD;
+  if (older && s != old) {                     // grown: the older rows once more
+    for (int r = row_in; r < r0 && r < (warp % TW + 1) * 16; r += 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2* at = reinterpret_cast<uint2*>(out + r * kD + 8 * (h ? ln.b : ln.a));
+        float y[8];
+        decode8<FMT>(*at, old, y);
+        *at = encode8<FMT, true>(y, inv);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row_in + 4 * i;
+    if (r >= r0 && r < r1) {
+      float u[8], v[8];
+      row_values(i, u, v);
+      const uint2 cu = clean ? encode8<FMT, true>(u, inv) : encode8<FMT, false>(u, inv);
+      const uint2 cv = clean ? encode8<FMT, true>(v, inv) : encode8<FMT, false>(v, inv);
+      if (KIND == kTurnHalf && ln.b != ln.a + 1) {
+        *reinterpret_cast<uint2*>(out + r * kD + 8 * ln.a) = cu;
+        *reinterpret_cast<uint2*>(out + r * kD + 8 * ln.b) = cv;
+      } else {
+        *reinterpret_cast<uint4*>(out + r * kD + 8 * ln.a) = make_uint4(cu.x, cu.y, cv.x, cv.y);
+      }
+    }
+  }
+  // (every lane of the team has read the old scale before the barrier above; a
+  // team of one warp is in step)
+  __syncwarp();
+  if (warp % TW == 0 && lane == 0) scales[row0 / BLK] = s;
 }
 
-// A half-warp per (token, KV head).  No early start for the next kernel: what
-// is read back may be a cache that the key scan streams before its wait.
+constexpr int kReadRows = 64;  // rows of a CTA of kv8_read_kernel
+
+// Bandwidth-bound: eight lanes a row, 16 codes a lane, keys and values of two
+// rows in flight a lane.  No early start for the next kernel: what is read
+// back may be a cache that the key scan streams before its wait.
 template <int FMT>
 __global__ void __launch_bounds__(256) kv8_read_kernel(ReadArgs a) {
   pdl_wait();
-  const int b = blockIdx.z, g = blockIdx.y;
-  const int c = threadIdx.x & 15;
+  const int b = blockIdx.z, g = blockIdx.y, l = threadIdx.x & 7;
   int64_t tok, n;
   const bool good = seq_tokens(a.cu, a.max_new, a.T, b, tok, n);
-  const int64_t j = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   if (!good) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
     if (tok < 0 || tok + n > a.T) return;
     n = n < 0 ? 0 : (n > a.max_new ? a.max_new : n);
   }
-  if (j >= n) return;
+  const int64_t j0 = (int64_t)blockIdx.x * kReadRows + (threadIdx.x >> 3);
+  if (j0 >= n) return;
   const int64_t L = a.lens[b];
-  const int64_t pos = L - n + j;
   const bool bad_len = !good || L < 0 || L > a.c.l_cap;
-  const int64_t row = bad_len || pos < 0 ? -1 : cache_row(a.c, b, g, pos);
-  uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
-  if (row >= 0) {
-    float x[8];
-    decode8<FMT>(*reinterpret_cast<const uint2*>(a.c.k + row * kD + 8 * c),
-                 a.c.ks[row >> a.c.block_shift], x);
-    wk = pack8(x);
-    decode8<FMT>(*reinterpret_cast<const uint2*>(a.c.v + row * kD + 8 * c),
-                 a.c.vs[row >> a.c.block_shift], x);
-    wv = pack8(x);
-  } else if (bad_len || pos >= 0) {
-    wk = wv = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-    if (c == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+  int64_t row[2];
+  uint4 code[2][2];
+  float scale[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t j = j0 + 32 * i, pos = L - n + j;
+    row[i] = bad_len || pos < 0 || j >= n ? -1 : cache_row(a.c, b, g, pos);
+    if (row[i] >= 0) {
+      code[i][0] = *reinterpret_cast<const uint4*>(a.c.k + row[i] * kD + 16 * l);
+      code[i][1] = *reinterpret_cast<const uint4*>(a.c.v + row[i] * kD + 16 * l);
+      scale[i][0] = a.c.ks[row[i] >> a.c.block_shift];
+      scale[i][1] = a.c.vs[row[i] >> a.c.block_shift];
+    }
   }
-  const int64_t t = tok + j;
-  *reinterpret_cast<uint4*>(a.k.p + t * a.k.st + g * a.k.sh + 8 * c) = wk;
-  *reinterpret_cast<uint4*>(a.v.p + t * a.v.st + g * a.v.sh + 8 * c) = wv;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t j = j0 + 32 * i, pos = L - n + j, t = tok + j;
+    if (j >= n) break;
+    const bool nan = row[i] < 0 && (bad_len || pos >= 0);
+    if (nan && l == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const RowsView& out = w ? a.v : a.k;
+      const uint32_t blank = nan ? 0x7fff7fffu : 0u;
+      uint4 lo = make_uint4(blank, blank, blank, blank), hi = lo;
+      if (row[i] >= 0) {
+        float x[8];
+        decode8<FMT>(make_uint2(code[i][w].x, code[i][w].y), scale[i][w], x);
+        lo = pack8(x);
+        decode8<FMT>(make_uint2(code[i][w].z, code[i][w].w), scale[i][w], x);
+        hi = pack8(x);
+      }
+      uint4* to = reinterpret_cast<uint4*>(out.p + t * out.st + g * out.sh + 16 * l);
+      to[0] = lo;
+      to[1] = hi;
+    }
+  }
+}
+
+template <int FMT, int BLK, int KIND>
+cudaError_t append_kind(const AppendArgs& a, cudaStream_t st) {
+  constexpr int THREADS = append_threads(BLK), TEAMS = THREADS / 32 / (BLK / 16);
+  // blocks that a sequence can touch
+  const int nb = (int)(((a.max_new < a.T ? a.max_new : a.T) + BLK - 2) / BLK + 1);
+  const dim3 grid((unsigned)(((int64_t)nb * 2 * a.c.Hkv + TEAMS - 1) / TEAMS), a.B);
+  return launch_dependent(kv8_append_kernel<FMT, BLK, KIND>, grid, dim3(THREADS), 0, st, a, nb);
 }
 
 template <int FMT, int BLK>
 cudaError_t append_block(const AppendArgs& a, cudaStream_t st) {
-  constexpr int TEAMS = kAppendThreads / 32 / (BLK / 16);
-  const int Hkv = a.c.Hkv;
-  // blocks that a sequence can touch
-  const int nb = (int)(((a.max_new < a.T ? a.max_new : a.T) + BLK - 2) / BLK + 1);
-  const dim3 th(kAppendThreads);
-  if (!a.rope.lo) {
-    const dim3 grid((unsigned)(((int64_t)nb * 2 * Hkv + TEAMS - 1) / TEAMS), a.B);
-    return launch_dependent(kv8_append_kernel<FMT, BLK, false>, grid, th, 0, st, a, nb, 1);
-  }
-  // All heads of a block's keys in one CTA where the blocks fill the machine,
-  // else a turn of the teams a CTA (single tokens: latency counts).
-  const int heads = (int64_t)nb * a.B >= 4 * 152 || Hkv < TEAMS ? Hkv : TEAMS;
-  const int parts = (Hkv + heads - 1) / heads;
-  const dim3 grid((unsigned)(nb * parts + ((int64_t)nb * Hkv + TEAMS - 1) / TEAMS), a.B);
-  const size_t smem = (size_t)BLK * a.rope.pairs * sizeof(float2);
-  const cudaError_t e =
-      cudaFuncSetAttribute((const void*)kv8_append_kernel<FMT, BLK, true>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(BLK * kD * 4));
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kv8_append_kernel<FMT, BLK, true>, grid, th, smem, st, a, nb, heads);
+  if (!a.rope.lo) return append_kind<FMT, BLK, kStraight>(a, st);
+  return a.rope.interleaved ? append_kind<FMT, BLK, kTurnInterleaved>(a, st)
+                            : append_kind<FMT, BLK, kTurnHalf>(a, st);
 }
 
 template <int FMT>
@@ -319,7 +388,7 @@ cudaError_t launch_kv8_append(const AppendArgs& a, cudaStream_t st) {
 
 cudaError_t launch_kv8_read(const ReadArgs& a, cudaStream_t st) {
   const int64_t most = a.max_new < a.T ? a.max_new : a.T;
-  const dim3 grid((unsigned)((most + 15) / 16), a.c.Hkv, a.B), th(256);
+  const dim3 grid((unsigned)((most + kReadRows - 1) / kReadRows), a.c.Hkv, a.B), th(256);
   return a.fmt == kFmtInt8 ? launch_dependent(kv8_read_kernel<kFmtInt8>, grid, th, 0, st, a)
                            : launch_dependent(kv8_read_kernel<kFmtE4m3>, grid, th, 0, st, a);
 }

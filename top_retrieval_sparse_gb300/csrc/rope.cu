@@ -11,6 +11,7 @@ __global__ void rope_table_kernel(RopeTableArgs a) {
        e += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = e / a.pairs;
     const int i = (int)(e % a.pairs);
+    const int64_t at = row * a.pairs + rope_place(i, a.pairs);
     const bool low = row < kRopeLow;
     const double t = low ? (double)row : (double)(row - kRopeLow) * kRopeLow;
     double s, c;
@@ -18,9 +19,9 @@ __global__ void rope_table_kernel(RopeTableArgs a) {
     const double m = low ? a.amplitude : 1.0;
     const float2 v = make_float2((float)(c * m), (float)(s * m));
     if (low)
-      a.lo[e] = v;
+      a.lo[at] = v;
     else
-      a.hi[e - (int64_t)kRopeLow * a.pairs] = v;
+      a.hi[at - (int64_t)kRopeLow * a.pairs] = v;
   }
 }
 
@@ -51,12 +52,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   const int second = 8 * (ln.b - ln.a);
   float2 cs[8];
   if (ln.pair >= 0) {
-    const int64_t pos = a.positions[t];
+    rope_angles(a.rope, a.positions[t], threadIdx.x & 7, cs);
+    if (a.inverse)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = rope_angle(a.rope, pos, ln.pair + e);
-      if (a.inverse) cs[e].y = -cs[e].y;
-    }
+      for (int e = 0; e < 8; ++e) cs[e].y = -cs[e].y;
   }
   for (int h0 = slot % WAYS; h0 < H; h0 += WAYS * kRopeBatch) {
     uint4 w[kRopeBatch][2];

@@ -5,14 +5,36 @@
 
 namespace tsa {
 
-// cos and sin of position t, pair i: the sum of the two table angles,
-// (cos(x + y), sin(x + y)) from (cos x, sin x) and (cos y, sin y).  Each factor
-// is within half a step of 32 bits, so each result is within about 2^-23.
-__device__ __forceinline__ float2 rope_angle(const RopeView& r, int64_t t, int i) {
-  if (t < 0 || t >= r.max_pos) return make_float2(nanf(""), nanf(""));
-  const float2 a = r.lo[(t & (kRopeLow - 1)) * r.pairs + i];
-  const float2 b = r.hi[(t >> kRopeLowBits) * r.pairs + i];
-  return make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+// Place of pair i in a table row of n pairs: lane i / 8 of a row's lanes (below)
+// takes its eight pairs as four pieces of 16 bytes, and the lanes' pieces of one load
+// lie side by side.
+__host__ __device__ __forceinline__ int rope_place(int i, int n) {
+  return 2 * ((n >> 3) * ((i & 7) >> 1) + (i >> 3)) + (i & 1);
+}
+
+// The angles of two pairs from a piece of the low row and of the high row.
+__device__ __forceinline__ void rope_sum(const float4& a, const float4& b, float2& c0,
+                                         float2& c1) {
+  c0 = make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+  c1 = make_float2(a.z * b.z - a.w * b.w, a.w * b.z + a.z * b.w);
+}
+
+// cos and sin of position t for the eight pairs of lane l (l < pairs / 8): the sum
+// of the two table angles, (cos(x + y), sin(x + y)) from (cos x, sin x) and (cos y,
+// sin y).  Each factor is within half a step of 32 bits, so each result is within
+// about 2^-23.
+__device__ __forceinline__ void rope_angles(const RopeView& r, int64_t t, int l,
+                                            float2 (&cs)[8]) {
+  if (t < 0 || t >= r.max_pos) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = make_float2(nanf(""), nanf(""));
+    return;
+  }
+  const int n8 = r.pairs >> 3;
+  const float4* lo = reinterpret_cast<const float4*>(r.lo + (t & (kRopeLow - 1)) * r.pairs) + l;
+  const float4* hi = reinterpret_cast<const float4*>(r.hi + (t >> kRopeLowBits) * r.pairs) + l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) rope_sum(lo[n8 * e], hi[n8 * e], cs[2 * e], cs[2 * e + 1]);
 }
 
 // A row is turned by eight lanes, 16 elements each as two pieces of 8 (lane l's
