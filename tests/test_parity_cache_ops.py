@@ -524,6 +524,62 @@ def test_kv8_attn_decode(tsa, case, fmt, block):
     assert torch.equal(out, again)
 
 
+def test_decode_of_the_largest_batches(tsa):
+    """4096 sequences over one page each (empty ones among them), 1024 KV heads."""
+    g = gen(50)
+    B, ps = 4096, 16
+    pt = torch.randperm(B, generator=g, device=DEV).view(B, 1).int()
+    lens = torch.randint(0, ps + 1, (B,), generator=g, device=DEV).int()
+    k, v = randn(g, B, 2, ps, D).bfloat16(), randn(g, B, 2, ps, D).bfloat16()
+    cache = tsa.KV8.paged(B, 2, ps, pt.contiguous())
+    x = k[pt[:, 0].long()].transpose(1, 2), v[pt[:, 0].long()].transpose(1, 2)
+    tsa.kv8_append(cache, *(t.reshape(-1, 2, D) for t in x), i32([ps] * B))
+    val = values(cache)
+    q = randn(g, B, 8, D).bfloat16()
+    for call, kk, vv in ((tsa.window_attn_decode, k, v), (tsa.kv8_attn_decode, *val)):
+        kv = tsa.kv_paged(k, v, pt) if kk is k else cache
+        lse = torch.empty((B, 8), device=DEV)
+        out, _ = call(q, kv, lens, 0, None, lse_out=lse)
+        kk, vv = (t[pt[:, 0].long()].double() for t in (kk, vv))       # [B, 2, ps, D]
+        z = torch.einsum("bgid,bgjd->bgij", q.double().view(B, 2, 4, D), kk) / math.sqrt(D)
+        on = torch.arange(ps, device=DEV) < lens[:, None, None, None]
+        z = z.masked_fill(~on, -math.inf)
+        p = torch.softmax(z, -1).nan_to_num(0.0)
+        ref = (p @ vv).view(B, 8, D)
+        # logits of order 5, 16 rows: 32-bit arithmetic is within 1e-5 of the values
+        assert ((out - ref).abs() <= 1e-5 * vv.abs().max()).all()
+        full = lens > 0
+        want = torch.logsumexp(z, -1).view(B, 8)
+        assert torch.equal(lse.isinf().all(1), ~full)
+        assert ((lse - want).abs()[full] <= 1e-4).all()
+    B, H = 1, 1024
+    kv, rows = bf16_cache(tsa, g, B, H, 48, 0)
+    q = randn(g, B, H, D).bfloat16()
+    lse = torch.empty((B, H), device=DEV)
+    out, _ = tsa.window_attn_decode(q, kv, i32([37]), 3, 20, lse_out=lse)
+    check_decode(q, lambda b, h: (rows(kv.k, b, h), rows(kv.v, b, h)), [37], H, 3, 20, out, lse)
+
+
+def test_two_streams_at_once(tsa):
+    """Calls on two streams, a workspace each, give what each gives alone."""
+    g = gen(51)
+    kv, _ = bf16_cache(tsa, g, 4, 4, 8192, 16)
+    cache, _ = quant_cache(tsa, g, 4, 4, 8192, 16, "e4m3", 16)
+    q, qp = randn(g, 4, 28, D).bfloat16(), randn(g, 800, 28, D).bfloat16()
+    lens = i32([8192, 5000, 77, 2500])
+    want = [tsa.kv8_attn_decode(q, cache, lens)[0],
+            tsa.window_attn_prefill(qp, kv, lens, 4, 1000)[0]]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(5):
+        got[0].append(tsa.kv8_attn_decode(q, cache, lens, stream=a)[0])
+        got[1].append(tsa.window_attn_prefill(qp, kv, lens, 4, 1000, stream=b)[0])
+    torch.cuda.synchronize()
+    for w, xs in zip(want, got):
+        assert all(torch.equal(w, x) for x in xs)
+
+
 def test_decode_logits_and_scales_over_a_wide_range(tsa):
     """Large logits of both signs (one row takes all the weight), blocks whose
     scales differ by 2^60, a block of zeros, and a scale of the logits below 0."""

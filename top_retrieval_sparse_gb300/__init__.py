@@ -760,6 +760,8 @@ class KV8:
 
 def _cache_batch(cache, lens: torch.Tensor) -> int:
     _want(lens, torch.int32, "lens")
+    if cache.d != 128:
+        raise ValueError(f"cache rows have {cache.d} elements: only 128 is compiled")
     B = lens.shape[0]
     if lens.dim() != 1 or B > cache.B:
         raise ValueError(f"lens must be int32 [B] with B <= {cache.B}, the cache's sequences")

@@ -660,9 +660,15 @@ int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st) {
   const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
   const dim3 g(grid), th(kDecodeThreads);
-  if (fmt == kFmtInt8) return launch_dependent(attn_decode_kernel<kFmtInt8>, g, th, smem, st, a);
-  if (fmt == kFmtE4m3) return launch_dependent(attn_decode_kernel<kFmtE4m3>, g, th, smem, st, a);
-  return launch_dependent(attn_decode_kernel<kFmtBf16>, g, th, smem, st, a);
+  const auto kernel = fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8>
+                      : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3>
+                                        : attn_decode_kernel<kFmtBf16>;
+  if (smem > 24 * 1024) {  // with the static arrays: past the default limit
+    const cudaError_t e = cudaFuncSetAttribute(
+        (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(kernel, g, th, smem, st, a);
 }
 
 }  // namespace tsa

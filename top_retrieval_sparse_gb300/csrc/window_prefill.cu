@@ -271,7 +271,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int b = blockIdx.z, g = blockIdx.y;
   const int G = a.G, TQ = kTile / G;
   pdl_wait();
-  pdl_trigger();
+  // Only the joining kernel may start early: the output is bf16, and the key scan
+  // reads its queries before its dependency wait.
+  if (a.splits > 1) pdl_trigger();
 
   // This CTA's tokens [t0, t1) of sequence b, the last blocks first.
   int64_t tok, n64;
