@@ -7,7 +7,10 @@
  * the window separately, and merge the two partial results with the
  * log-sum-exp rescale.  A second entry point runs ReTopK's reuse path, which
  * recalls candidate keys from a per-head cache of past queries instead of
- * scanning every key on most steps.
+ * scanning every key on most steps.  Beside them stand the operators that a
+ * program needs around the cache: rotary positions, an 8-bit cache (written with
+ * rotated keys, read back, attended), and attention with a sliding window and
+ * sinks for one token or many.
  *
  * Sources (page title, section / equation):
  *   [RA]  "RetrievalAttention: Accelerating Long-Context LLM Inference via
@@ -521,7 +524,8 @@ TSA_API int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows
  *   lse_out: fp32 [B][Hq] or NULL (log sum e^z): (out, lse) is a partial that
  *     lse_merge takes.  No visible row: out 0, lse -inf.
  *   Products and sums are as those of 32-bit arithmetic: codes, keys and
- *   queries enter the tensor cores exactly, the softmax weights in two parts.
+ *   queries enter the tensor cores exactly, the softmax weights in parts that
+ *   add up to 22 bits (kv8) or 24.
  *   Limits: Hq / Hkv <= 8, B <= 4096, Hkv <= 1024, B * Hq <= 65535.
  *   workspace: tsa_attn_decode_workspace_size() bytes, 256-byte aligned,
  *   zero-filled before its first use; calls leave it ready for any call that it

@@ -37,7 +37,8 @@ int fail(int code, const char* fmt, ...) {
 }
 
 int launched(cudaError_t e, const char* what) {
-  if (count_launch(e) != cudaSuccess) return fail(TSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  if (count_launch(e) != cudaSuccess)
+    return fail(TSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return report_ok();
 }
 
@@ -109,7 +110,8 @@ int check_batch(int B, int Hkv, int d) {
 }
 
 int check_groups(int B, int Hq, int Hkv) {
-  if (Hq <= 0 || Hq % Hkv) return fail(TSA_ERR_INVALID_ARG, "Hq %% Hkv != 0 (Hq=%d Hkv=%d)", Hq, Hkv);
+  if (Hq <= 0 || Hq % Hkv)
+    return fail(TSA_ERR_INVALID_ARG, "Hq %% Hkv != 0 (Hq=%d Hkv=%d)", Hq, Hkv);
   if (Hq / Hkv > kMaxGroup)
     return fail(TSA_ERR_INVALID_ARG, "group size %d > %d", Hq / Hkv, kMaxGroup);
   if ((int64_t)B * Hq > 65535)

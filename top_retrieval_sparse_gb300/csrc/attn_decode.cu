@@ -9,33 +9,39 @@
 // long as its instructions keep up.
 //
 // Split.  The rows are cut into slabs of 16 (aligned, so a slab lies in one page and
-// one scale block); the slabs of all sequences and KV heads form one list,
-// which the CTAs of a resident grid take in equal contiguous shares, whatever the
-// sequences' lengths (they are only known on the device).  A share that holds all of a
-// unit (sequence, KV head) writes its output; other shares leave (o, max, sum) in the
-// workspace and the last to arrive joins them in share order, so results do not
-// depend on the order of arrival.
+// one scale block); the slabs of all sequences and KV heads form one list, which the
+// CTAs of a resident grid take in equal contiguous shares, whatever the sequences'
+// lengths (they are only known on the device).  A share that holds all of a unit
+// (sequence, KV head) writes its output; other shares leave (o, max, sum) in the
+// workspace and the last to arrive joins them in share order, so results do not depend
+// on the order of arrival.
 //
 // A warp's slab.  mma.m16n8k16 with the rows as M for the logits (heads are the 8
 // columns) and the head dimension as M for the output, so that no column of the
-// products is wasted on more than 8 - G heads, and the tensor pipe has time to
-// spare.  tcgen05 would want 64 or 128 rows of queries; here there are 8.  Rows go from
-// global memory straight into the registers of the fragments: the reduction
-// index of a product may be permuted at will as long as both operands agree, so
-// each lane takes whole 16-byte pieces.  The next slabs' keys are requested when this
-// slab's logits are done, their values when the output products are, which keeps
-// about 8 KB a warp and 12 warps an SM in flight without shared memory.
+// products is wasted on more than 8 - G heads, and the tensor pipe has time to spare
+// (16 % busy).  tcgen05 would want 64 or 128 rows of queries; here there are 8.  Rows
+// go from global memory straight into the registers of the fragments: the reduction
+// index of a product may be permuted at will as long as both operands agree, so each
+// lane takes whole 16-byte pieces.  The next slabs' keys are requested when this slab's
+// logits are done, their values when the output products are, which keeps up to 8 KB a
+// warp and 12 or 16 warps an SM in flight without shared memory (a ring of asynchronous
+// copies in shared memory was slower: a million rows 406 us).
 //
 // Numbers.  Codes are exact in fp16 (whole numbers to 127, 4-bit significands), and so
-// are queries after a shift of their exponents; bf16 rows and queries meet as bf16.  The
-// softmax weights enter the second product as the sum of two fp16 or three
-// bf16 parts (2^-22 and 2^-24 of the weight at most), so the result is that of 32-bit
-// arithmetic.  Matrix instructions truncate their 32-bit sums, which over the
-// hundreds of slabs of a long share would lose 2^-17 (measured at a million rows: 1.0e-5
-// off 64 bits); every 16 slabs they are added to sums in shared memory, with rounding.  Value scales differ by block, so the weights carry them: w_i =
-// e^z_i s_i relative to the largest such product, while the sum adds w_i / s_i.  The
-// maximum is raised only when a weight would pass 2^15: one vote a slab in place of six
-// shuffles.
+// are queries after a shift of their exponents; bf16 rows and queries meet as bf16.
+// The softmax weights enter the second product as the sum of two fp16 or three bf16
+// parts (2^-22 and 2^-24 of the weight at most), so the result is that of 32-bit
+// arithmetic.  Matrix instructions truncate their 32-bit sums, which over the hundreds
+// of slabs of a long share would lose 2^-17 (measured at a million rows: 1.0e-5 off 64
+// bits, 6e-7 now); every 16 slabs they are added to sums in shared memory, with
+// rounding.  Value scales differ by block, so the weights carry them: w_i = e^z_i s_i
+// relative to the largest such product, while the sum adds w_i / s_i.  The maximum is
+// raised only when a weight would pass 2^15: one vote a slab in place of six shuffles.
+//
+// What bounds it.  bf16: bandwidth (16 x 65536 rows of 4 KV heads, 308 us, 7.0 TB/s).
+// e4m3: a million rows of 8 KV heads 324 us, 6.6 TB/s.  int8: its codes take twice the
+// instructions to widen (400 a slab; issue slots 45 % busy), 183 us for the first
+// case's rows, 5.9 TB/s; pages of 16 cost 3 % more.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"

@@ -11,15 +11,22 @@
 // Both products of a key tile are 2 x 128^3: the tensor core bounds the kernel, as long
 // as the exponentials of one tile run under the other tile's products; hence two.
 //
-// Warps.  0 and 3: the matrix instructions of A and of B, 1: the copies, 2: zeroing of
-// V (first, so that the scheduler prefers them), 4-7: softmax of tile A (thread = row = tensor-memory
-// lane), 8-11: of B.  K and V tiles go through a ring of
-// five 32 KB slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a
-// page where pages are smaller than a tile).  A tile's matrix instructions come in the
-// order O(j), S(j+1), O(j+1) ..., from one thread, so that they execute in that order: S(j+1)
-// may overwrite P(j) without a wait.  A commit covers all of a thread's, so a softmax that
-// sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the weights
-// have grown by more than 2^16.
+// Warps.  0 and 3: the matrix instructions of A and of B, 1: the copies, 2: zeroing
+// of V (first, so that the scheduler prefers them), 4-7: softmax of tile A (thread =
+// row = tensor-memory lane), 8-11: of B.  K and V tiles go through a ring of five 32 KB
+// slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a page where pages
+// are smaller than a tile).  A tile's matrix instructions come in the order O(j),
+// S(j+1), O(j+1) ..., from one thread, so that they execute in that order: S(j+1) may
+// overwrite P(j) without a wait.  A commit covers all of a thread's, so a softmax that
+// sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the
+// weights have grown by more than 2^16.
+//
+// What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 ms, 1670
+// TFLOP/s of visible pairs, 0.87 of the measured burst of a library matrix product (0.97
+// of its sustained rate; a full causal 32K prompt 1780 to 1840).  A step of two tiles
+// takes 2400 cycles for 2048 of matrix instructions; what is left is the path from S to
+// P where it is longer than the other tile's products, 10K cycles a CTA for its
+// queries and its output, and key tiles that the window's edges only partly need.
 //
 // Few queries (fewer CTAs than half the SMs) share the key tiles of a CTA's queries out
 // over several; each leaves (O, maximum, sum) in the workspace, and a second kernel
@@ -398,11 +405,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int k0 = v.tile(j) * kTile;
         const bool whole = k0 + kTile - 1 <= first && (ni - k0 >= kTile || k0 > last - nr);
         ok = wait(&bar.s[x], j & 1);
-        if (!ok) break;
+        if (__builtin_expect(!ok, 0)) break;
         fence_after();
         float s[128];
         load_cols(s_at, s);
-        if (!whole) {
+        // (the unlikely blocks out of the usual path's instruction stream: 1.29 -> 1.27 ms)
+        if (__builtin_expect(!whole, 0)) {
           // columns [0, hi) but [lo, mid): behind the query, between sinks and window
           const int hi = p - k0 + 1, lo = ni - k0, mid = p - nr + 1 - k0;
 #pragma unroll
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // the weights taken again.
         float l0 = 0.f;
         bool good = m != -INFINITY || !live;  // rows without a query have no say
-        if (__all_sync(0xffffffffu, good)) {
+        if (__builtin_expect(__all_sync(0xffffffffu, good), 1)) {
           float tops[4] = {s[64], s[65], s[66], s[67]};
 #pragma unroll
           for (int i = 68; i < 124; i += 8)
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           l0 = weights(0, m);
           good = (l0 <= kMost && (t - m) * sc <= kRescale) || !live;
         }
-        if (!__all_sync(0xffffffffu, good)) {
+        if (__builtin_expect(!__all_sync(0xffffffffu, good), 0)) {
           float tops[4] = {m, m, m, m};
 #pragma unroll
           for (int i = 0; i < 128; i += 8)
