@@ -80,6 +80,8 @@ def library_path() -> str:
 def lib():
     """Load libtsa.so (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -567,20 +569,26 @@ def _gpu(*named) -> torch.device:
     return dev
 
 
+# The current device and the raw handle of its current stream: the public
+# calls (torch.cuda.current_device, current_stream) take several times as long,
+# which a decode step's call would notice.
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
+_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _run_on(dev: torch.device, stream, fn, *args) -> None:
-    """fn(*args, stream) with dev current; stream None: dev's current one
-    (its raw handle: torch.cuda.current_stream() costs several microseconds)."""
+    """fn(*args, stream) with dev current; stream None: dev's current one."""
     i = dev.index
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(i)
+        handle = _stream_now(i)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if i == torch.cuda.current_device():
+    if i == _device_now():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, handle)
-    if rc != TSA_OK:
+    if rc:
         _check(rc)
 
 
@@ -657,6 +665,7 @@ class RopeTable:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.table = _new(stream, dev, (n,), torch.uint8)
+        self.device = self.table.device
         _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table, C.byref(spec),
                 _ptr(self.table), n, self._ref)
 
@@ -668,22 +677,25 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
 
     Rows may be strided (a slice of a fused projection); q_out=q rotates in
     place.  Returns (q_out, k_out)."""
-    dev = _gpu((q, "q"), (positions, "positions"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"),
-               (table.table, "table"))
+    dev = q.device
+    if positions.device != dev or table.device != dev or not q.is_cuda or \
+            k is not None and k.device != dev or q_out is not None or k_out is not None:
+        _gpu((q, "q"), (positions, "positions"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"),
+             (table.table, "table"))
     _want(positions, torch.int32, "positions")
     T, Hq, d = q.shape
     if positions.shape != (T,):
         raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
     if q_out is None:
-        q_out = _new(stream, dev, q.shape, torch.bfloat16)
-    if q_out.shape != q.shape:
+        q_out = _new(stream, dev, (T, Hq, d), torch.bfloat16)
+    elif q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
     Hkv, ks, kos = 0, None, None
     if k is not None:
+        if k.shape[0] != T or k.shape[2] != d or k_out is not None and k_out.shape != k.shape:
+            raise ValueError("k and k_out must be [tokens][heads][128] with q's tokens")
         if k_out is None:
             k_out = _new(stream, dev, k.shape, torch.bfloat16)
-        if k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != d:
-            raise ValueError("k and k_out must be [tokens][heads][128] with q's tokens")
         Hkv, ks, kos = k.shape[1], _rows(k, "k"), _rows(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -832,10 +844,14 @@ def _attn_decode(fn, ref, q, cache, lens, n_init, n_recent, scale, out, lse_out,
     Bq, Hq, d = q.shape
     if Bq != B:
         raise ValueError(f"q has {Bq} sequences, lens {B}")
-    dev = _gpu((q, "q"), (cache.k, "cache"), (lens, "lens"), (out, "out"), (lse_out, "lse_out"),
-               (workspace, "workspace"))
+    dev = q.device
+    if cache.k.device != dev or lens.device != dev or not q.is_cuda or \
+            lse_out is not None and lse_out.device != dev or out is not None or \
+            workspace is not None and workspace.device != dev:
+        _gpu((q, "q"), (cache.k, "cache"), (lens, "lens"), (out, "out"), (lse_out, "lse_out"),
+             (workspace, "workspace"))
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        scale = d ** -0.5
     if out is None:
         out = _new(stream, dev, (B, Hq, d), torch.float32)
     elif out.shape != q.shape:
