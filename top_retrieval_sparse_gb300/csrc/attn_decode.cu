@@ -321,14 +321,19 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     // Rows fit 32 bits: 2^32 rows of keys alone are more than the memory.
     uint32_t row[NS], seen[NS], seen_now[NS];
     float ks[NS], vs[NS], ks_now[NS], vs_now[NS];
-    int32_t page[NS];
+    int32_t page[NS] = {};
     const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
     const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
     const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
     const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
 
-    // First row of slab k of this unit.
-    auto first_row = [&](int k) { return (k < vis.s0 ? k : vis.sw + (k - vis.s0)) << 4; };
+    // All rows are seen of the sinks' slabs but the last, and of the window's but
+    // the first and the last: those three take the long way.
+    const int inside = vis.s0 + 1, shift = vis.sw - vis.s0;
+    const uint32_t insides = vis.n - 1 > inside ? vis.n - 1 - inside : 0;
+    auto first_row = [&](int k) {
+      return (int)((uint32_t)(k < vis.s0 ? k : k + shift) << 4);
+    };
     auto want_pages = [&](int k) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
@@ -337,32 +342,32 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     auto find_rows = [&](int k) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        row[s] = seen[s] = 0u;
-        if (k + s < k1) {
-          const int i = first_row(k + s);
-          seen[s] = 0xffffu;
-          if (!((i >= vis.lo && vis.L - i >= 16) || vis.n0 - i >= 16)) {
-            seen[s] = 0u;
+        const int i = first_row(k + s);
+        seen[s] = 0xffffu;
+        if (__builtin_expect(((uint32_t)(k + s - inside) >= insides && k + s >= vis.s0 - 1) ||
+                                 k + s >= k1, 0)) {
+          seen[s] = 0u;
+          if (k + s < k1)
             for (int j = 0; j < 16; ++j)
               if ((j < vis.n0 - i || j >= vis.lo - i) && j < vis.L - i) seen[s] |= 1u << j;
-          }
-          if (!pages) {
-            row[s] = unit_row + (uint32_t)i;
-          } else if ((uint32_t)page[s] < a.c.n_pages) {
-            row[s] = (((uint32_t)page[s] * (uint32_t)Hkv + (uint32_t)g) << a.c.page_shift) +
-                     ((uint32_t)i & ((1u << a.c.page_shift) - 1u));
-          } else {
-            bad = true;
+        }
+        row[s] = unit_row + (uint32_t)i;
+        if (pages) {
+          row[s] = (((uint32_t)page[s] * (uint32_t)Hkv + (uint32_t)g) << a.c.page_shift) +
+                   ((uint32_t)i & ((1u << a.c.page_shift) - 1u));
+          if (__builtin_expect((uint32_t)page[s] >= a.c.n_pages, 0)) {
+            bad |= seen[s] != 0u;
             seen[s] = 0u;
           }
         }
+        if (__builtin_expect(seen[s] == 0u, 0)) row[s] = 0u;  // (nothing is read)
       }
     };
     auto want_keys = [&]() {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const uint8_t* p = k_lane + (uint64_t)row[s] * ROW;
-        if (seen[s] == 0xffffu) {
+        if (__builtin_expect(seen[s] == 0xffffu, 1)) {
 #pragma unroll
           for (int c = 0; c < KW; ++c) {
             kr[s][0][c] = ld_row(p + 64 * c);
@@ -376,8 +381,11 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
           }
         }
         if (!B16) {
-          ks[s] = seen[s] ? a.c.ks[row[s] >> a.c.block_shift] : 1.f;
-          vs[s] = seen[s] ? a.c.vs[row[s] >> a.c.block_shift] : 1.f;
+          ks[s] = vs[s] = 1.f;
+          if (__builtin_expect(seen[s] != 0u, 1)) {
+            ks[s] = a.c.ks[row[s] >> a.c.block_shift];
+            vs[s] = a.c.vs[row[s] >> a.c.block_shift];
+          }
         }
       }
     };
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
       for (int s = 0; s < NS; ++s) {
         const uint8_t* p = v_lane + (uint64_t)row[s] * ROW;
         // rows 2tq, 2tq + 1, 2tq + 8, 2tq + 9
-        if (seen[s] == 0xffffu) {
+        if (__builtin_expect(seen[s] == 0xffffu, 1)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -455,14 +463,15 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
         z[s][1] = fmaf(z[s][1], f1, add);
         z[s][2] = fmaf(z[s][2], f0, add);
         z[s][3] = fmaf(z[s][3], f1, add);
-        if (seen_now[s] != 0xffffu) {
+        if (__builtin_expect(seen_now[s] != 0xffffu, 0)) {
           if (!((seen_now[s] >> gr) & 1u)) z[s][0] = z[s][1] = -INFINITY;
           if (!((seen_now[s] >> (gr + 8)) & 1u)) z[s][2] = z[s][3] = -INFINITY;
         }
         top0 = fmaxf(top0, fmaxf(z[s][0], z[s][2]));
         top1 = fmaxf(top1, fmaxf(z[s][1], z[s][3]));
       }
-      if (__any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
+      if (__builtin_expect(
+              __any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack), 0)) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
