@@ -556,6 +556,10 @@ TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* l
  * on are left as they were.
  * workspace: window_attn_prefill_workspace_size() bytes (from the same max_q,
  * l_cap and window), 256-byte aligned, zero-filled before its first use.
+ * Device-detected errors (on the workspace): a lens[b] outside [0, l_cap] is
+ * clamped and flagged; a visible row on a negative page is flagged and gives NaN to
+ * every query computed with it (a block of tokens of that KV head's query heads);
+ * offsets outside [0, T] are flagged and nothing of their sequence is written.
  * Limits: Hq / Hkv <= 8, B <= 4096, B * Hkv <= 65535. */
 TSA_API size_t window_attn_prefill_workspace_size(int B, int Hq, int Hkv, int d, int max_q,
                                                   int64_t l_cap, int64_t n_init,

@@ -935,6 +935,6 @@ def window_attn_prefill(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int
                                                           int(n_init), nr))
         workspace = _new(stream, dev, (max(nb, 256),), torch.uint8, zero=True)
     _run_on(dev, stream, lib().window_attn_prefill, _rows(q, "q"), C.byref(kv.struct),
-            _ptr(cu_q), T, n, _ptr(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale), _ptr(out),
-            _ptr(lse_out), _ptr(workspace), workspace.nbytes)
+            _ptr(cu_q), T, n, _ptr(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale),
+            _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.nbytes)
     return out, lse_out

@@ -19,7 +19,7 @@
 // A warp's slab.  mma.m16n8k16 with the rows as M for the logits (heads are the 8
 // columns) and the head dimension as M for the output, so that no column of the
 // products is wasted on more than 8 - G heads, and the tensor pipe has time to spare
-// (16 % busy).  tcgen05 would want 64 or 128 rows of queries; here there are 8.  Rows
+// (17 % busy).  tcgen05 would want 64 or 128 rows of queries; here there are 8.  Rows
 // go from global memory straight into the registers of the fragments: the reduction
 // index of a product may be permuted at will as long as both operands agree, so each
 // lane takes whole 16-byte pieces.  The next slabs' keys are requested when this slab's
@@ -39,9 +39,9 @@
 // raised only when a weight would pass 2^15: one vote a slab in place of six shuffles.
 //
 // What bounds it.  bf16: bandwidth (16 x 65536 rows of 4 KV heads, 308 us, 7.0 TB/s).
-// e4m3: a million rows of 8 KV heads 324 us, 6.6 TB/s.  int8: its codes take twice the
-// instructions to widen (400 a slab; issue slots 45 % busy), 183 us for the first
-// case's rows, 5.9 TB/s; pages of 16 cost 3 % more.
+// e4m3: a million rows of 8 KV heads 319 us, 6.7 TB/s.  int8: its codes take twice the
+// instructions to widen (375 a slab; issue slots 44 % busy), 172 us for the first
+// case's rows, 6.2 TB/s; pages of 16 cost 2 % more.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -181,7 +181,8 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, in
 // Slabs that a warp works on at once, and CTAs of 4 warps an SM: rows of 8 KB
 // a turn for bf16 and e4m3 (their rows wait in 64 registers a lane, 12 warps an SM);
 // int8 codes take twice e4m3's instructions to widen, and 16 warps of one slab
-// each hide those better (16 x 65536 rows: 183 us against 187; e4m3 177 against 173).
+// each hide those better (16 x 65536 rows, both before slabs' usual case was put first:
+// int8 183 us against 187 with two slabs; e4m3 177 against 173).
 __host__ __device__ constexpr int slabs_of(int fmt) { return fmt == kFmtE4m3 ? 2 : 1; }
 __host__ __device__ constexpr int ctas_of(int fmt) { return fmt == kFmtInt8 ? 4 : 3; }
 

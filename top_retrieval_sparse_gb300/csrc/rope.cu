@@ -33,7 +33,7 @@ constexpr int kRopeBatch = 5;   // rows of eight lanes in flight
 // head of it, kRopeBatch rows in flight at a time: with four tokens a CTA the angles, 1
 // KB of table from L2, serve 40 rows of 512 bytes moved; with one (few tokens) a
 // token's heads are spread over the whole CTA.  A lane holds both elements of its
-// pairs, so no values change lanes.  A prompt of 32768 tokens, 32 + 8 heads: 115 us,
+// pairs, so no values change lanes.  A prompt of 32768 tokens, 32 + 8 heads: 113 us,
 // 5.9 TB/s (144 us with 16 lanes a row and shuffles).  It does not let the next kernel start
 // early: the key scan reads q and the keys before its dependency wait.
 template <int TOKENS, bool INTER>

@@ -21,11 +21,12 @@
 // sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the
 // weights have grown by more than 2^16.
 //
-// What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 ms, 1670
-// TFLOP/s of visible pairs, 0.87 of the measured burst of a library matrix product (0.97
-// of its sustained rate; a full causal 32K prompt 1780 to 1840).  A step of two tiles
+// What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 to 1.31 ms
+// in runs of 40 calls (1620 to 1670 TFLOP/s of visible pairs, 0.84 to 0.87 of the measured
+// burst of a library matrix product) and 1.40 ms in longer ones (1510, 0.87 of its
+// sustained rate); a full causal 32K prompt 4.9 ms, 1785 TFLOP/s.  A step of two tiles
 // takes 2400 cycles for 2048 of matrix instructions; what is left is the path from S to
-// P where it is longer than the other tile's products, 10K cycles a CTA for its
+// P where it is longer than the other tile's products, 12K cycles of a CTA's 95K for its
 // queries and its output, and key tiles that the window's edges only partly need.
 //
 // Few queries (fewer CTAs than half the SMs) share the key tiles of a CTA's queries out
