@@ -20,6 +20,10 @@
 // overwrite P(j) without a wait.  A commit covers all of a thread's, so a softmax that
 // sees S(j) also knows O(j-1) done, and may rescale O; it does so only where the
 // weights have grown by more than 2^16.
+// A slot is filled again when all its readers have given it back: the matrix threads
+// (for the last of their instructions) and the zeroing warp, which passes every slot
+// in order, K's too.  A wait tells a barrier's last two phases apart and no more, so
+// nobody may fall behind by two laps of the ring; this count is what excludes it.
 //
 // What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 to 1.31 ms
 // in runs of 40 calls (1620 to 1670 TFLOP/s of visible pairs, 0.84 to 0.87 of the measured
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], two ? 2 : 1);
+      mbar_init(&bar.empty[i], two ? 3 : 2);  // matrix threads, zeroing warp
       mbar_init(&bar.clean[i], 32);
     }
     fence_mbar_init();
@@ -679,6 +683,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     bool ok = true;
     for (int j = 0; j < v.n && ok; ++j) {
       const int it = 2 * j + 1, k0 = v.tile(j) * kTile;
+      ok = wait(&bar.full[(it - 1) % kSlots], ((it - 1) / kSlots) & 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&bar.empty[(it - 1) % kSlots]);
       ok = wait(&bar.full[it % kSlots], (it / kSlots) & 1);
       if (!ok) break;
       if (k0 + kTile > v.end || (k0 + kTile > v.n0 && k0 < v.lo)) {
@@ -691,6 +698,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         fence_proxy_async();
       }
       mbar_arrive(&bar.clean[j % kSlots]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.empty[it % kSlots]);
     }
    }
   }
