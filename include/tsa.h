@@ -552,10 +552,12 @@ TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* l
  * position lens[b] - n_b + j (below 0: it sees nothing).  max_q: the most tokens
  * of a sequence (a sequence with more is flagged, its outputs NaN up to max_q).
  * out: bf16 [T][Hq][128], rounded once from 32-bit sums (the softmax weights
- * enter the products in bf16); lse_out: fp32 [T][Hq] or NULL.  Rows from cu_q[B]
+ * enter the products in bf16; the sums of at most 16384 rows are truncated, by 1e-4
+ * of them at most, and added with rounding); lse_out: fp32 [T][Hq] or NULL.  Rows from cu_q[B]
  * on are left as they were.
  * workspace: window_attn_prefill_workspace_size() bytes (from the same max_q,
- * l_cap and window), 256-byte aligned, zero-filled before its first use.
+ * l_cap and window), 256-byte aligned, zero-filled before its first use; calls
+ * leave it ready for any call that it is large enough for.
  * Device-detected errors (on the workspace): a lens[b] outside [0, l_cap] is
  * clamped and flagged; a visible row on a negative page is flagged and gives NaN to
  * every query computed with it (a block of tokens of that KV head's query heads);

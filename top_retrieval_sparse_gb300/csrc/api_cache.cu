@@ -235,33 +235,42 @@ constexpr size_t kDecodeArrived =
 // tiles (16 tokens late in a window of 4096, 33 tiles a head: 60 us in one CTA).
 struct PrefillCut {
   int64_t blocks, splits, units;
+  bool folds;  // a CTA may have more than kFoldTiles key tiles
 };
 PrefillCut prefill_cut(int B, int Hkv, int G, int64_t max_q, int64_t l_cap, int64_t n_init,
                        int64_t n_recent) {
-  PrefillCut c{0, 1, 0};
+  PrefillCut c{0, 1, 0, false};
   const int64_t tokens = 2 * (128 / G);
   c.blocks = (max_q + tokens - 1) / tokens;
   c.units = c.blocks * B * Hkv;
   const int64_t sms = 152;  // (not the device's: sizes do not depend on where they are asked)
-  if (c.units < 1 || c.units > sms / 2) return c;
   const int64_t q = max_q < tokens ? max_q : tokens;
   auto tiles = [&](int64_t rows) { return ((rows < l_cap ? rows : l_cap) + 127) / 128; };
   int64_t n = tiles(n_init < l_cap ? n_init : l_cap) + 1 +
               tiles((n_recent < l_cap ? n_recent : l_cap) + q);
   if (n > tiles(l_cap)) n = tiles(l_cap);
+  c.folds = n > kFoldTiles;
+  if (c.units < 1 || c.units > sms / 2) return c;
   const int64_t rows = max_q * G < 128 ? max_q * G : 128;
   c.splits = sms / c.units;
   if (c.splits > (n + 1) / 2) c.splits = (n + 1) / 2;
   if (c.splits > 8 * 128 / rows) c.splits = 8 * 128 / rows;
   if (c.splits > 32) c.splits = 32;
   if (c.splits < 1) c.splits = 1;
+  c.folds = (n + c.splits - 1) / c.splits > kFoldTiles;
   return c;
 }
-// Workspace: the status word, the partials.
-constexpr size_t kPrePartial = kAlign;
-size_t prefill_bytes(const PrefillCut& c) {
+// Workspace: the status word, which places of the long sums are taken (zero between
+// calls of whatever sizes, so at a fixed offset), the partials, the long sums.
+constexpr size_t kPrePlaces = kAlign;
+constexpr size_t kPrePartial =
+    kPrePlaces + (kFoldPlaces * sizeof(uint32_t) + kAlign - 1) / kAlign * kAlign;
+size_t prefill_sums(const PrefillCut& c) {
   return kPrePartial + (c.splits > 1 ? (size_t)(c.units * c.splits) * 2 * kPreSlot * sizeof(float)
                                      : 0);
+}
+size_t prefill_bytes(const PrefillCut& c) {
+  return prefill_sums(c) + (c.folds ? (size_t)kFoldPlaces * 2 * 128 * kD * sizeof(float) : 0);
 }
 
 // Both decode entry points after their cache's checks.
@@ -549,6 +558,8 @@ int window_attn_prefill(const tsa_rows* q, const tsa_kv* kv, const int32_t* cu_q
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
   a.partial = reinterpret_cast<float*>(ws + kPrePartial);
+  a.sums = cut.folds ? reinterpret_cast<float*>(ws + prefill_sums(cut)) : nullptr;
+  a.places = reinterpret_cast<uint32_t*>(ws + kPrePlaces);
   a.splits = (int)cut.splits;
   // no sequence has more than T tokens, whatever max_q says
   const int64_t tokens = 2 * (128 / a.G), most = max_q < T ? max_q : T;

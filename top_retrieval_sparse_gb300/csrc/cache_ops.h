@@ -141,6 +141,10 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStrea
 // Many tokens per sequence (window_prefill.cu); the maps are the bf16 pool's
 // rows of 128 elements, in boxes of 64 elements by `box` rows.
 constexpr int kPreSlot = 2 * 128 + 128 * kD;  // floats of a query tile's partial
+// Key tiles between two additions of O to a CTA's sums in the workspace, and how many
+// CTAs can have such sums at once (one runs on an SM).
+constexpr int kFoldTiles = 128;
+constexpr int kFoldPlaces = 152;
 struct PrefillArgs {
   RowsView q;
   CacheView c;
@@ -158,6 +162,8 @@ struct PrefillArgs {
   int* status;
   int blocks, splits;  // CTAs of a sequence's tokens, and of each one's key tiles
   float* partial;      // [B * Hkv * blocks][splits][2][kPreSlot] (splits > 1)
+  float* sums;         // [kFoldPlaces][2][128 * kD], or nullptr: no part has so many tiles
+  uint32_t* places;    // [kFoldPlaces], zero between calls
 };
 cudaError_t launch_window_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                   const PrefillArgs& a, int B, cudaStream_t st);

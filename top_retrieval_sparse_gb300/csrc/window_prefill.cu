@@ -37,6 +37,14 @@
 // over several; each leaves (O, maximum, sum) in the workspace, and a second kernel
 // joins them, a warp a row (the last CTA to arrive doing it took 10 us).
 //
+// Long sums.  Matrix instructions truncate their 32-bit sums, all in one direction: values
+// of one sign came out 6.3e-9 of themselves too small for every row (6.6e-3 for a million,
+// more than bf16's rounding).  So every kFoldTiles tiles a row's O is added, with rounding,
+// to a sum in the workspace that carries its own maximum, and begins again from nothing:
+// 128 tiles lose 1e-4 at most and cost a full causal 32K prompt 5.14 -> 5.18 ms (64
+// tiles 5.26), 704 tokens after a million rows 10.7 -> 10.9 ms.  The sums are of the CTAs
+// that run, not of the call: 20 MB that stay in L2.
+//
 // Masks cost nothing but at the edges of what is seen: there the rows' columns are
 // masked one by one, and rows of V that no query of the CTA sees are zeroed in
 // shared memory (whatever they hold, 0 * NaN would reach the output).
@@ -254,6 +262,21 @@ struct Span {
   __device__ bool sees(int r) const { return r < end && (r < n0 || r >= lo); }
 };
 
+// A place for a CTA's sums that no other CTA uses: its SM's, as a rule (a CTA fills an
+// SM, so there are as many places as CTAs).  -1: none came free (bounded).
+__device__ int take_place(uint32_t* used) {
+  uint32_t sm;
+  asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+  for (uint32_t i = 0; i < 1u << 20; ++i) {
+    const int at = (int)((sm + i) % kFoldPlaces);
+    if (atomicExch(used + at, 1u) == 0u) {
+      __threadfence();
+      return at;
+    }
+  }
+  return -1;
+}
+
 // A bounded wait.  One try in line; the loop with the clock and the abort flag
 // is kept out of the way of the usual path.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -279,6 +302,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
   __shared__ volatile int bad_s;
+  __shared__ volatile int place_s;           // of the long sums; set before the first copies
+  __shared__ float under_s[2][kTile];        // the maximum a row's sum outside is under
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.z, g = blockIdx.y;
   const int G = a.G, TQ = kTile / G;
@@ -342,6 +367,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     fence_mbar_init();
     abort_s = 0;
     bad_s = bad_count;
+    place_s = -1;
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -402,6 +428,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint32_t o_at = s_at + 2 * kTile;
       const float sc = a.scale_log2;
       float m = -INFINITY, l = 0.f;
+      // Columns 32 c + 4 i of that sum (neighbouring rows side by side).
+      auto outside = [&](int c, int i) {
+        return reinterpret_cast<float4*>(a.sums) +
+               (((size_t)place_s * 2 + x) * (kD / 4) + 8 * c + i) * kTile + r;
+      };
+      // 32 columns of O, the sum outside (if any of it is there yet) added.
+      auto whole_sums = [&](int c, bool more, float f, float (&o)[32]) {
+        load_cols(o_at + 32 * c, o);
+        if (more) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 u = __ldcg(outside(c, i));
+            o[4 * i] = fmaf(u.x, f, o[4 * i]);
+            o[4 * i + 1] = fmaf(u.y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(u.z, f, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(u.w, f, o[4 * i + 3]);
+          }
+        }
+      };
       // The tile's queries see all of a key tile k0 iff every one of them does.
       const int first = L - n + t0 + x * TQ;
       const int last = L - n + (t0 + (x + 1) * TQ < t1 ? t0 + (x + 1) * TQ : t1) - 1;
@@ -412,6 +457,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ok = wait(&bar.s[x], j & 1);
         if (__builtin_expect(!ok, 0)) break;
         fence_after();
+        if (__builtin_expect(j % kFoldTiles == 0 && j > 0 && place_s >= 0, 0)) {
+          const bool more = j > kFoldTiles;
+          const float was = more ? under_s[x][r] : m, f = was == m ? 1.f : ex2((was - m) * sc);
+          under_s[x][r] = m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            whole_sums(c, more, f, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              __stcg(outside(c, i),
+                     make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+          }
+        }
         float s[128];
         load_cols(s_at, s);
         // (the unlikely blocks out of the usual path's instruction stream: 1.29 -> 1.27 ms)
@@ -500,6 +559,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ok = wait(&bar.o[x], 0);
         fence_after();
       }
+      const bool folds = place_s >= 0;
+      const float was = folds ? under_s[x][r] : m, fs = was == m ? 1.f : ex2((was - m) * sc);
       if (!ok || bad_s) {
         l = nanf("");
         if (m == -INFINITY) m = 0.f;
@@ -515,7 +576,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float o[32];
-            load_cols(o_at + 32 * c, o);
+            whole_sums(c, folds, fs, o);
             if (live)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -533,7 +594,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float o[32];
-          load_cols(o_at + 32 * c, o);
+          whole_sums(c, folds, fs, o);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -602,6 +663,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (ok && v.edge(j))
           ok = wait_for(&bar.clean[j % kSlots], (j / kSlots) & 1, &abort_s);
         const uint64_t vx = vd + slot * (kSlotBytes >> 4);
+        // O begins again every kFoldTiles tiles
+        const bool more = j % kFoldTiles > 0 || (j > 0 && place_s < 0);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           ok = ok && wait_for(&bar.p[x][part], j & 1, &abort_s);
@@ -610,7 +673,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             fence_after();
 #pragma unroll
             for (int k = 4 * part; k < 4 * part + 4; ++k)
-              mma_ts(o_at, s_at + 8 * k, vx + ((k * 16 * 128) >> 4), kIdescV, j > 0 || k > 0);
+              mma_ts(o_at, s_at + 8 * k, vx + ((k * 16 * 128) >> 4), kIdescV, more || k > 0);
           }
         }
         if (!ok) break;
@@ -656,6 +719,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       return (((int64_t)page * a.c.Hkv + g) << a.c.page_shift) + (r0 & ((1 << a.c.page_shift) - 1));
     };
+    if (a.sums && v.n > kFoldTiles && lane == 0) {
+      const int at = take_place(a.places);
+      place_s = at;
+      if (at < 0) {
+        bad_s = 1;
+        atomicOr(a.status, kStatusTimeout);
+      }
+    }
+    __syncwarp();
     int64_t next = find(0);
     int issued = 0;
     bool ok = true;
@@ -705,6 +777,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (tid == 0 && place_s >= 0) {  // the place is free again
+    __threadfence();
+    atomicExch(a.places + place_s, 0u);
+  }
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
