@@ -523,6 +523,8 @@ TSA_API int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows
  *   out: fp32 [B][Hq][128] = softmax(scale q.k) . v over the visible rows;
  *   lse_out: fp32 [B][Hq] or NULL (log sum e^z): (out, lse) is a partial that
  *     lse_merge takes.  No visible row: out 0, lse -inf.
+ *   A value scale below 2^-60 (0: a cache that was zeroed and not written there)
+ *     counts as 2^-60.
  *   Products and sums are as those of 32-bit arithmetic: codes, keys and
  *   queries enter the tensor cores exactly, the softmax weights in parts that
  *   add up to 22 bits (kv8) or 24.

@@ -749,21 +749,21 @@ class KV8:
     @classmethod
     def contiguous(cls, B: int, Hkv: int, l_cap: int, block: int = 64, fmt: str = "int8",
                    device="cuda") -> "KV8":
-        """A zeroed contiguous cache with a status word."""
+        """A contiguous cache of zeros with a status word."""
         return cls._made(B, Hkv, l_cap, block, fmt, None, device)
 
     @classmethod
     def paged(cls, pages: int, Hkv: int, page_size: int, page_table: torch.Tensor,
               block: int = 16, fmt: str = "int8") -> "KV8":
-        """A zeroed pool of pages with a status word."""
+        """A pool of pages of zeros with a status word."""
         return cls._made(pages, Hkv, page_size, block, fmt, page_table, page_table.device)
 
     @classmethod
     def _made(cls, n, Hkv, rows, block, fmt, page_table, device):
         if rows % block:
             raise ValueError(f"block {block} does not divide {rows} rows")
-        code = [torch.zeros((n, Hkv, rows, 128), dtype=torch.uint8, device=device)
-                for _ in range(2)]
+        code = [torch.full((n, Hkv, rows, 128), 128 if fmt == "int8" else 0, dtype=torch.uint8,
+                           device=device) for _ in range(2)]
         scale = [torch.zeros((n, Hkv, rows // block), dtype=torch.float32, device=device)
                  for _ in range(2)]
         status = torch.zeros(64, dtype=torch.int32, device=device)

@@ -55,6 +55,7 @@ constexpr int kWarps = kDecodeThreads / 32;
 // not: fp16's normal numbers then reach 2^-21 below the first, its smallest
 // steps 2^-32.
 constexpr float kRaised = 7.f, kSlack = 15.f;
+constexpr float kLeastScale = 1.f / (1ll << 60);  // the smallest that the cache's writer gives
 
 __device__ __forceinline__ uint4 ld_row(const uint8_t* p) {
   uint4 r;
@@ -80,12 +81,16 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Of value scales, powers of two in earnest: a last-place error here would
-// change a weight, and its share of the sum, by 2^-22 of itself.
+// Of value scales: the exponent and the logarithm of what is left, so that it is
+// exact for powers of two (an error would change a weight, and its share of the sum).
 __device__ __forceinline__ float lg2(float x) {
+  const uint32_t u = __float_as_uint(x);
   float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+  asm("lg2.approx.ftz.f32 %0, %1;"
+      : "=f"(r)
+      : "f"(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
+  // the exponent's bits under the exponent of 2^23
+  return r + (__uint_as_float((u >> 23) | 0x4b000000u) - 8388735.f);
 }
 __device__ __forceinline__ float rcp(float x) {
   float r;
@@ -174,8 +179,15 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, in
   const int64_t at = (int64_t)b * a.Hq + head;
   *reinterpret_cast<float4*>(a.out + at * kD + 4 * lane) =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (a.lse && lane == 0)
-    a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.lse && lane == 0) {
+    // m carries a value scale and l its inverse (2^60 at most), so the exponents are
+    // added first: log2(l) as one number would be off by up to 2^-18.
+    const uint32_t u = __float_as_uint(l);
+    const float e = (float)((int)(u >> 23) - 127);
+    const float f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+    a.lse[at] = l == 0.f ? -INFINITY
+                         : (l < INFINITY ? ((m + e) + log2f(f)) * 0.6931471805599453f : l);
+  }
 }
 
 // Slabs that a warp works on at once, and CTAs of 4 warps an SM: rows of 8 KB
@@ -425,7 +437,9 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
       for (int s = 0; s < NS; ++s) {
         seen_now[s] = seen[s];
         ks_now[s] = ks[s];
-        vs_now[s] = vs[s];
+        // (a cache that was zeroed and not written here has scales of 0, which have no
+        // logarithm: its values count as codes of the least scale, 4e-16 at most)
+        vs_now[s] = fmaxf(vs[s], kLeastScale);
       }
       find_rows(k + stride);
       want_pages(k + 2 * stride);
