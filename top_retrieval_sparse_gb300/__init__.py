@@ -621,6 +621,14 @@ def _rows(t: torch.Tensor, name: str) -> bytes:
     return _pack_rows(t.data_ptr(), st[0], st[1])
 
 
+def _count(n, what: str) -> int:
+    """A number of tokens as the library's 32 bits hold it (ctypes cuts silently)."""
+    n = int(n)
+    if not 0 <= n < 1 << 31:
+        raise ValueError(f"{what} = {n}: must be in [0, 2^31)")
+    return n
+
+
 def _offsets(cu, T: int, max_n, B: int, what: str) -> int:
     """The most tokens of a sequence (max_n, or T / B without offsets)."""
     if cu is None:
@@ -634,7 +642,7 @@ def _offsets(cu, T: int, max_n, B: int, what: str) -> int:
         raise ValueError(f"offsets must be int32 [{B + 1}], got {tuple(cu.shape)}")
     if max_n is None:
         raise ValueError(f"{what} is needed with offsets")
-    return int(max_n)
+    return _count(max_n, what)
 
 
 class RopeTable:
@@ -899,7 +907,7 @@ def window_attn_prefill_workspace(B: int, Hq: int, Hkv: int, max_q: int, l_cap: 
                                   device="cuda") -> torch.Tensor:
     """A zeroed workspace of window_attn_prefill for these sizes."""
     n = int(lib().window_attn_prefill_workspace_size(
-        B, Hq, Hkv, d, max_q, l_cap, n_init, l_cap if n_recent is None else n_recent))
+        B, Hq, Hkv, d, _count(max_q, "max_q"), l_cap, n_init, l_cap if n_recent is None else n_recent))
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
