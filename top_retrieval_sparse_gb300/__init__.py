@@ -218,6 +218,11 @@ class KV:
     def __init__(self, k, v, page_table=None, page_size=0):
         _want(k, torch.bfloat16, "k")
         _want(v, torch.bfloat16, "v")
+        if v.shape != k.shape:
+            raise ValueError(f"v must have k's shape {tuple(k.shape)}, got {tuple(v.shape)}")
+        for t, name in ((v, "v"), (page_table, "page_table")):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.page_table = k, v, page_table
         if page_table is None:
             if k.dim() != 4:
