@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], two ? 3 : 2);  // matrix threads, zeroing warp
-      mbar_init(&bar.clean[i], 32);
+      mbar_init(&bar.clean[i], 1);
     }
     fence_mbar_init();
     abort_s = 0;
@@ -758,12 +758,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     bool ok = true;
     for (int j = 0; j < v.n && ok; ++j) {
       const int it = 2 * j + 1, k0 = v.tile(j) * kTile;
-      ok = wait(&bar.full[(it - 1) % kSlots], ((it - 1) / kSlots) & 1);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&bar.empty[(it - 1) % kSlots]);
-      ok = wait(&bar.full[it % kSlots], (it / kSlots) & 1);
+      if (lane == 0) {
+        ok = wait_for(&bar.full[(it - 1) % kSlots], ((it - 1) / kSlots) & 1, &abort_s);
+        if (ok) mbar_arrive(&bar.empty[(it - 1) % kSlots]);
+        ok = ok && wait_for(&bar.full[it % kSlots], (it / kSlots) & 1, &abort_s);
+      }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (k0 + kTile > v.end || (k0 + kTile > v.n0 && k0 < v.lo)) {
+        __syncwarp();
         const uint32_t at =
             ring + (it % kSlots) * kSlotBytes + (lane >> 4) * kHalf + (lane & 15) * 8;
         for (int r = 0; r < kTile; ++r)
@@ -771,10 +774,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(at + r * 128), "r"(0)
                          : "memory");
         fence_proxy_async();
+        __syncwarp();
       }
-      mbar_arrive(&bar.clean[j % kSlots]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.empty[it % kSlots]);
+      if (lane == 0) {
+        mbar_arrive(&bar.clean[j % kSlots]);
+        mbar_arrive(&bar.empty[it % kSlots]);
+      }
     }
    }
   }
