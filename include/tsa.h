@@ -527,7 +527,9 @@ TSA_API int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows
  *     counts as 2^-60.
  *   Products and sums are as those of 32-bit arithmetic: codes, keys and
  *   queries enter the tensor cores exactly, the softmax weights in parts that
- *   add up to 22 bits (kv8) or 24.
+ *   add up to 22 bits (kv8) or 24.  kv8: out takes a row's weight times value scale in
+ *   steps of 2^-31 of the largest such product that the same warp has met (lse does
+ *   not), and logits are rounded together with log2 of their block's value scale.
  *   Limits: Hq / Hkv <= 8, B <= 4096, Hkv <= 1024, B * Hq <= 65535.
  *   workspace: tsa_attn_decode_workspace_size() bytes, 256-byte aligned,
  *   zero-filled before its first use; calls leave it ready for any call that it

@@ -33,15 +33,18 @@
 // parts (2^-22 and 2^-24 of the weight at most), so the result is that of 32-bit
 // arithmetic.  Matrix instructions truncate their 32-bit sums, which over the hundreds
 // of slabs of a long share would lose 2^-17 (measured at a million rows: 1.0e-5 off 64
-// bits, 6e-7 now); every 16 slabs they are added to sums in shared memory, with
+// bits, 6e-7 now; four million rows of values of one sign: 1e-4 too small, 9e-6 at most
+// now); every 16 slabs they are added to sums in shared memory, with
 // rounding.  Value scales differ by block, so the weights carry them: w_i = e^z_i s_i
-// relative to the largest such product, while the sum adds w_i / s_i.  The maximum is
+// relative to the largest such product, while the sum adds w_i / s_i.  (fp16 has steps of
+// 2^-24 below 2^-14, so what is under 2^-32 of a warp's largest w is lost from the output
+// and not from the sum: at most 2^-32 of that w times the row's code.)  The maximum is
 // raised only when a weight would pass 2^15: one vote a slab in place of six shuffles.
 //
 // What bounds it.  bf16: bandwidth (16 x 65536 rows of 4 KV heads, 308 us, 7.0 TB/s).
-// e4m3: a million rows of 8 KV heads 319 us, 6.7 TB/s.  int8: its codes take twice the
-// instructions to widen (375 a slab; issue slots 44 % busy), 172 us for the first
-// case's rows, 6.2 TB/s; pages of 16 cost 2 % more.
+// e4m3: a million rows of 8 KV heads 318 us, 6.7 TB/s.  int8: its codes take twice the
+// instructions to widen (380 a slab; issue slots 43 % busy), 173 us for the same 16 x
+// 65536 rows, 6.2 TB/s; pages of 16 cost 2 % more.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"

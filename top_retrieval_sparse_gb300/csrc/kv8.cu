@@ -102,8 +102,9 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&x)[8]) {
 // table in L2, 512 bytes a row, which each head's team reads for itself: sharing them
 // between the heads in shared memory made a CTA go through the heads one after another
 // over strided reads (227 us for 128K tokens of 8 heads, 194 us so).  128K tokens without a
-// rotation: 117 us, 6.9 TB/s; with it the rotated rows' registers leave 16 warps an SM, and
-// what they wait for bounds it.
+// rotation: 117 us, 6.9 TB/s; with it the rotated rows in 32 bits beside the rows as read
+// and the angles reach the limit of 128 registers (16 warps an SM; 80 to 112 bytes a
+// thread spill, 204 at blocks of 16), and what those warps wait for bounds it.
 template <int FMT, int BLK, int KIND>
 __global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / append_threads(BLK))
     kv8_append_kernel(AppendArgs a, int nb) {

@@ -25,13 +25,18 @@
 // in order, K's too.  A wait tells a barrier's last two phases apart and no more, so
 // nobody may fall behind by two laps of the ring; this count is what excludes it.
 //
-// What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 to 1.31 ms
-// in runs of 40 calls (1620 to 1670 TFLOP/s of visible pairs, 0.84 to 0.87 of the measured
-// burst of a library matrix product) and 1.40 ms in longer ones (1510, 0.87 of its
-// sustained rate); a full causal 32K prompt 4.9 ms, 1785 TFLOP/s.  A step of two tiles
-// takes 2400 cycles for 2048 of matrix instructions; what is left is the path from S to
-// P where it is longer than the other tile's products, 12K cycles of a CTA's 95K for its
-// queries and its output, and key tiles that the window's edges only partly need.
+// Weights are rounded to bf16 for the second product, as its operands are of one type and
+// V is bf16: half a step of 2^-8 each, both ways.  Against 64 bits the output is off by 2.0e-3
+// to 2.4e-3 where 32-bit weights rounded once are off by 1.5e-3 to 1.7e-3; a second part
+// would take half as many matrix instructions again.
+//
+// What bounds it: 32K tokens, 32/8 heads, window 4096 + 128 sinks take 1.27 ms in single
+// calls (1660 TFLOP/s of visible pairs, 0.86 of the measured burst of a library matrix
+// product) and 1.37 ms under a sustained load (1550, 0.89 of its sustained rate); a full
+// causal 32K prompt 4.9 ms, 1800 TFLOP/s.  A step of two tiles takes 2400 to 2500 cycles for
+// 2048 of matrix instructions; what is left is the path from S to P where it is longer
+// than the other tile's products, 12K cycles of a CTA's 95K for its queries and its
+// output, and key tiles that the window's edges only partly need.
 //
 // Few queries (fewer CTAs than half the SMs) share the key tiles of a CTA's queries out
 // over several; each leaves (O, maximum, sum) in the workspace, and a second kernel
@@ -41,8 +46,8 @@
 // of one sign came out 6.3e-9 of themselves too small for every row (6.6e-3 for a million,
 // more than bf16's rounding).  So every kFoldTiles tiles a row's O is added, with rounding,
 // to a sum in the workspace that carries its own maximum, and begins again from nothing:
-// 128 tiles lose 1e-4 at most and cost a full causal 32K prompt 5.14 -> 5.18 ms (64
-// tiles 5.26), 704 tokens after a million rows 10.7 -> 10.9 ms.  The sums are of the CTAs
+// 128 tiles lose 1e-4 at most and cost a full causal 32K prompt 5.14 -> 5.18 ms under a
+// sustained load (64 tiles 5.26), 704 tokens after a million rows 10.7 -> 10.9 ms.  The sums are of the CTAs
 // that run, not of the call: 20 MB that stay in L2.
 //
 // Masks cost nothing but at the edges of what is seen: there the rows' columns are
