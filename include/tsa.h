@@ -561,7 +561,7 @@ TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* l
  * on are left as they were.
  * workspace: window_attn_prefill_workspace_size() bytes (from the same max_q,
  * l_cap and window), 256-byte aligned, zero-filled before its first use; calls
- * leave it ready for any call that it is large enough for.
+ * leave it ready for any call of this entry point that it is large enough for.
  * Device-detected errors (on the workspace): a lens[b] outside [0, l_cap] is
  * clamped and flagged; a visible row on a negative page is flagged and gives NaN to
  * every query computed with it (a block of tokens of that KV head's query heads);
