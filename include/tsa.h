@@ -510,6 +510,83 @@ TSA_API int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows
                      int Hkv, int d, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* Pages of a paged cache: which page of the pool every sequence's positions are in.
+ *
+ * table: int32 [B][max_pages], the page table of tsa_kv and tsa_kv8 (one for all layers);
+ *   an entry without a page is negative (-1).  refs: int32 [n_pages], how many entries
+ *   name a page; 0: the page is free.  A pool starts with refs 0 and table -1.
+ * Everything is device memory, and what the calls decide is decided on the device: no
+ * call synchronises, and all can be captured.  Pages are always the lowest free ones,
+ * in the order of sequences and positions, so results do not depend on scheduling.
+ * workspace: tsa_pages_workspace_size() bytes, 256-byte aligned, zero-filled before its
+ *   first use (the status word; the rest is scratch of one call).
+ * Limits: page_size a power of two in [16, 256], B <= 4096, n_pages <= 2^23,
+ *   B * max_pages < 2^31, max_pages * page_size < 2^31.
+ * Device-detected errors (tsa_workspace_status on the workspace): see each call. */
+typedef struct tsa_pages {
+  int32_t* table;
+  int32_t* refs;
+  int32_t B;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_size;
+} tsa_pages;
+
+TSA_API size_t tsa_pages_workspace_size(int B, int max_pages, int n_pages);
+
+/* pages_alloc -- gives sequence b a free page for every entry that holds a position of
+ * [lo[b], hi[b]) and has none (lo, hi: int32 [B], device; hi <= lo: nothing).  A decode
+ * step passes its lengths before and after the new token.  Where the sequences' entries
+ * exceed the free pages nothing changes, and that is flagged; so is a range outside [0,
+ * max_pages * page_size], which is clipped. */
+TSA_API int pages_alloc(const tsa_pages* pages, const int32_t* lo, const int32_t* hi,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* pages_free -- takes from sequence b the entries whose pages lie in [lo[b], hi[b])
+ * altogether (a whole sequence: 0 and max_pages * page_size; what has left a window:
+ * n_init and length - n_recent; after a cut to n positions: n and the capacity).  They
+ * become -1, and their pages count one entry less.  Entries outside the pool, and pages
+ * whose count was 0, are flagged. */
+TSA_API int pages_free(const tsa_pages* pages, const int32_t* lo, const int32_t* hi,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* pages_fork -- sequence children[i] becomes a copy of the first lens[i] positions of
+ * parents[i], i < n <= B (int32 [n], device).  Whole pages are shared; a last page that
+ * is only partly covered gets a page of its own, and src[i], dst[i] (int32 [n], device)
+ * name the two for pages_copy, or are -1.  Entries of the child's row from there on are
+ * -1; the pages that it held count one entry less (and are not given out by this call).
+ * Entries that the parent has not are -1 in the child too.  One parent may have many
+ * children.  If a child is named twice or is a parent of the same call, an index or a
+ * length is out of range, a parent's entry is outside the pool, or the free pages do not
+ * suffice, nothing changes, src and dst are -1, and that is flagged. */
+TSA_API int pages_fork(const tsa_pages* pages, const int32_t* parents, const int32_t* children,
+                       const int32_t* lens, int n, int32_t* src, int32_t* dst, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* pages_compact -- the pages in use move to the front: with n of them, the k-th free page
+ * below n takes the k-th page in use from n on.  Tables and counts are rewritten, the
+ * moves are given in src and dst (int32 [n_pages / 2], device, -1 after the last) with
+ * their number in count (int32 [1], device); pages_copy with them moves the rows, before
+ * anything else uses the cache.  Entries that name a page outside the pool or one that
+ * counts as free are left and flagged. */
+TSA_API int pages_compact(const tsa_pages* pages, int32_t* src, int32_t* dst, int32_t* count,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* pages_copy -- copies page src[i] over page dst[i] in every buffer, i < n (int32 [n],
+ * device), or i < *count (int32 [1], device) where count is not NULL and less.  src[i] <
+ * 0: nothing.  No dst may be named twice or be a src as well.  bufs: host array; a buffer
+ * is [n_pages][bytes] (the K, V or scales of a layer: Hkv * page_size rows or blocks).
+ * data 4-byte aligned, bytes a multiple of 4 (16 for both is faster).  Pages outside
+ * [0, n_pages) are skipped, and flagged in status (NULL, or as tsa_kv8's). */
+typedef struct tsa_page_buf {
+  void* data;
+  int64_t bytes;
+} tsa_page_buf;
+TSA_API int pages_copy(const tsa_page_buf* bufs, int n_bufs, int n_pages, const int32_t* src,
+                       const int32_t* dst, const int32_t* count, int n, int32_t* status,
+                       void* stream);
+
+/* ------------------------------------------------------------------ */
 /* Attention with a sliding window and sinks, and attention over the 8-bit
  * cache.  A query at position p sees the positions j <= p with j < n_init (the
  * sinks) or j > p - n_recent (the window): the static W of sparse_attn_decode.

@@ -5,19 +5,9 @@
 // device memory, synchronises or prints.
 #include <atomic>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
-#include "../../include/tsa.h"
+#include "api_util.h"
 #include "cache_ops.h"
-
-namespace tsa {
-int report_error(int code, const char* msg);
-int report_ok();
-int validate_kv(const tsa_kv* kv);
-cudaError_t count_launch(cudaError_t e);
-int num_sms();
-}  // namespace tsa
 
 using namespace tsa;
 
@@ -25,24 +15,6 @@ namespace {
 
 constexpr double kPi = 3.14159265358979323846;
 constexpr double kLog2e = 1.4426950408889634;
-constexpr size_t kAlign = 256;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return report_error(code, buf);
-}
-
-int launched(cudaError_t e, const char* what) {
-  if (count_launch(e) != cudaSuccess)
-    return fail(TSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  return report_ok();
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // ------------------------------------------------------------- rotation
 bool rope_sizes(int rot_dim, int64_t max_pos) {
@@ -178,14 +150,6 @@ int check_cache(const tsa_kv* kv, int Hkv, CacheView& v) {
   v.max_pages = kv->max_pages;
   v.n_pages = 0x80000000u;  // the pool's size is not known: any page that is not negative
   v.Hkv = Hkv;
-  return TSA_OK;
-}
-
-int check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (!ws || !aligned(ws, kAlign))
-    return fail(TSA_ERR_WORKSPACE, "workspace NULL or not 256-byte aligned");
-  if (bytes < need)
-    return fail(TSA_ERR_WORKSPACE, "workspace too small: %zu bytes, %zu needed", bytes, need);
   return TSA_OK;
 }
 
