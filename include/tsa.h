@@ -443,6 +443,37 @@ TSA_API int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const t
                        const int32_t* positions, const tsa_rope* rope, int inverse,
                        void* stream);
 
+/* Several axes (time, height, width of images and video): a token has a position on
+ * each of n axes, and every pair of the rotation belongs to one of them.
+ *
+ * pairs[a]: how many of the rot_dim / 2 pairs axis a has (1 or more, they add up).
+ * order: TSA_AXES_BLOCKS, the first pairs[0] pairs are axis 0's, the next axis 1's, and
+ *   so on; TSA_AXES_TURNS, the pairs are dealt to the axes by turns (0, 1, 2, 0, ...),
+ *   leaving out those that have all of theirs.
+ * rates: TSA_RATES_JOINT, pair i turns at the rate w_i of the whole table, whatever its
+ *   axis; TSA_RATES_OWN, the j-th pair of axis a turns at the rate w_j of a table of
+ *   2 * pairs[a] elements.
+ * With equal positions on all axes and joint rates this is the plain rotation. */
+enum { TSA_AXES_BLOCKS = 0, TSA_AXES_TURNS = 1 };
+enum { TSA_RATES_JOINT = 0, TSA_RATES_OWN = 1 };
+typedef struct tsa_rope_axes {
+  int32_t n;         /* 1 .. 4 */
+  int32_t order;
+  int32_t rates;
+  int32_t pairs[4];
+} tsa_rope_axes;
+
+/* tsa_rope_table with the rates of `axes` (the same memory). */
+TSA_API int tsa_rope_table_axes(const tsa_rope_spec* spec, const tsa_rope_axes* axes,
+                                void* table, size_t bytes, tsa_rope* rope, void* stream);
+/* rope_apply with axes->n positions a token: axis a's are int32 [T] (device) at positions +
+ * a * stride (in elements; 0: all axes' are the same).  Where the position of an axis is
+ * outside [0, max_pos), the pairs of that axis are NaN. */
+TSA_API int rope_apply_axes(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
+                            const tsa_rows* k_out, int Hkv, int64_t T, int d,
+                            const int32_t* positions, int64_t stride, const tsa_rope* rope,
+                            const tsa_rope_axes* axes, int inverse, void* stream);
+
 /* ------------------------------------------------------------------ */
 /* 8-bit KV cache: keys and values in one byte an element, with one scale for
  * each block of `block` consecutive positions and KV head (K and V apart).
@@ -498,6 +529,14 @@ TSA_API int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_ro
                        const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens, int B,
                        int Hkv, int d, const tsa_rope* rope, const int32_t* positions,
                        void* stream);
+
+/* kv8_append with keys rotated by positions of several axes, laid out as in
+ * rope_apply_axes (rope and positions are needed here). */
+TSA_API int kv8_append_axes(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
+                            const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens,
+                            int B, int Hkv, int d, const tsa_rope* rope,
+                            const tsa_rope_axes* axes, const int32_t* positions, int64_t stride,
+                            void* stream);
 
 /* kv8_read -- the last n_b positions of every sequence, back in bf16 (exact).
  *

@@ -41,6 +41,44 @@ int check_rope(const tsa_rope* r, RopeView& v) {
   return TSA_OK;
 }
 
+// The axis of every pair of a rotation of rot_dim elements.
+int axes_of(const tsa_rope_axes* x, int rot_dim, int (&axis)[kD / 2]) {
+  if (!x) return fail(TSA_ERR_INVALID_ARG, "axes is NULL");
+  if (x->n < 1 || x->n > 4) return fail(TSA_ERR_INVALID_ARG, "axes: n %d not in [1, 4]", x->n);
+  if (x->order != TSA_AXES_BLOCKS && x->order != TSA_AXES_TURNS)
+    return fail(TSA_ERR_INVALID_ARG, "axes: unknown order %d", x->order);
+  if (x->rates != TSA_RATES_JOINT && x->rates != TSA_RATES_OWN)
+    return fail(TSA_ERR_INVALID_ARG, "axes: unknown rates %d", x->rates);
+  int left[4] = {}, all = 0;
+  for (int a = 0; a < x->n; ++a) {
+    if (x->pairs[a] < 1 || x->pairs[a] > kD / 2)
+      return fail(TSA_ERR_INVALID_ARG, "axes: pairs[%d] = %d", a, x->pairs[a]);
+    all += left[a] = x->pairs[a];
+  }
+  if (all != rot_dim / 2)
+    return fail(TSA_ERR_INVALID_ARG, "axes: %d pairs, the rotation has %d", all, rot_dim / 2);
+  for (int i = 0, a = 0; i < all; ++i) {
+    while (left[a] == 0) a = (a + 1) % x->n;
+    axis[i] = a;
+    --left[a];
+    if (x->order == TSA_AXES_TURNS) a = (a + 1) % x->n;
+  }
+  return TSA_OK;
+}
+
+int check_axes(const tsa_rope_axes* x, const tsa_rope* rope, int64_t stride, AxesView& v) {
+  v = AxesView{};
+  int axis[kD / 2] = {};
+  const int rc = axes_of(x, rope->rot_dim, axis);
+  if (rc) return rc;
+  if (stride < 0 || stride >= (int64_t)1 << 40)
+    return fail(TSA_ERR_INVALID_ARG, "the positions' stride must be in [0, 2^40)");
+  v.n = x->n;
+  v.stride = stride;
+  for (int i = 0; i < rope->rot_dim / 2; ++i) v.of[i / 8] |= (uint16_t)(axis[i] << (2 * (i % 8)));
+  return TSA_OK;
+}
+
 // Rows of T tokens and H heads (written rows must not overlap).
 int check_rows(const tsa_rows* r, int64_t T, int H, bool written, const char* name, RowsView& v) {
   v = RowsView{};
@@ -281,17 +319,41 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
                   "attention launch");
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t tsa_rope_table_size(int rot_dim, int64_t max_pos) {
-  if (!rope_sizes(rot_dim, max_pos)) return 0;
-  return (size_t)(kRopeLow + rope_high(max_pos)) * (rot_dim / 2) * sizeof(float2);
+// The rates w_i of a rotation of `rot` elements.
+void rope_rates(const tsa_rope_spec* s, double low, double high, int rot, double* w_out) {
+  const bool parts = s->scaling == TSA_ROPE_BY_PARTS, yarn = s->scaling == TSA_ROPE_YARN;
+  const int n = rot / 2;
+  double theta = s->theta;
+  if (s->scaling == TSA_ROPE_NTK) theta *= std::pow(s->factor, rot / (rot - 2.0));
+  double lo = 0, hi = 0;
+  if (yarn) {
+    const double per = rot / (2 * std::log(theta));
+    lo = std::floor(per * std::log(s->orig_len / (2 * kPi * high)));
+    hi = std::ceil(per * std::log(s->orig_len / (2 * kPi * low)));
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > rot - 1 ? rot - 1 : hi;
+  }
+  for (int i = 0; i < n; ++i) {
+    double w = std::pow(theta, -2.0 * i / rot);
+    if (s->scaling == TSA_ROPE_LINEAR) w /= s->factor;
+    if (parts) {
+      double t = (s->orig_len * w / (2 * kPi) - low) / (high - low);
+      t = t < 0 ? 0 : (t > 1 ? 1 : t);
+      w = (1 - t) * w / s->factor + t * w;
+    }
+    if (yarn) {
+      const double span = hi - lo > 0.001 ? hi - lo : 0.001;
+      double r = (i - lo) / span;
+      r = r < 0 ? 0 : (r > 1 ? 1 : r);
+      w = r * w / s->factor + (1 - r) * w;
+    }
+    w_out[i] = w;
+  }
 }
 
-int tsa_rope_table(const tsa_rope_spec* s, void* table, size_t bytes, tsa_rope* rope,
-                   void* stream) {
+// tsa_rope_table and tsa_rope_table_axes (own: the axes' rates, and every pair's axis).
+int rope_table(const tsa_rope_spec* s, const tsa_rope_axes* own, const int* axis, void* table,
+               size_t bytes, tsa_rope* rope, void* stream) {
   if (!s || !rope) return fail(TSA_ERR_INVALID_ARG, "spec or rope is NULL");
   if (!rope_sizes(s->rot_dim, s->max_pos))
     return fail(TSA_ERR_INVALID_ARG,
@@ -324,33 +386,19 @@ int tsa_rope_table(const tsa_rope_spec* s, void* table, size_t bytes, tsa_rope* 
   if (bytes < tsa_rope_table_size(s->rot_dim, s->max_pos))
     return fail(TSA_ERR_INVALID_ARG, "table too small (%zu < %zu)", bytes,
                 tsa_rope_table_size(s->rot_dim, s->max_pos));
+  if (own && s->scaling == TSA_ROPE_NTK)
+    for (int x = 0; x < own->n; ++x)
+      if (own->pairs[x] < 2)
+        return fail(TSA_ERR_INVALID_ARG, "axes: this scaling needs 2 pairs of every axis");
   const int rot = s->rot_dim, n = rot / 2;
-  double theta = s->theta;
-  if (s->scaling == TSA_ROPE_NTK) theta *= std::pow(s->factor, rot / (rot - 2.0));
   RopeTableArgs a{};
-  double lo = 0, hi = 0;
-  if (yarn) {
-    const double per = rot / (2 * std::log(theta));
-    lo = std::floor(per * std::log(s->orig_len / (2 * kPi * high)));
-    hi = std::ceil(per * std::log(s->orig_len / (2 * kPi * low)));
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > rot - 1 ? rot - 1 : hi;
-  }
-  for (int i = 0; i < n; ++i) {
-    double w = std::pow(theta, -2.0 * i / rot);
-    if (s->scaling == TSA_ROPE_LINEAR) w /= s->factor;
-    if (parts) {
-      double t = (s->orig_len * w / (2 * kPi) - low) / (high - low);
-      t = t < 0 ? 0 : (t > 1 ? 1 : t);
-      w = (1 - t) * w / s->factor + t * w;
-    }
-    if (yarn) {
-      const double span = hi - lo > 0.001 ? hi - lo : 0.001;
-      double r = (i - lo) / span;
-      r = r < 0 ? 0 : (r > 1 ? 1 : r);
-      w = r * w / s->factor + (1 - r) * w;
-    }
-    a.w[i] = w;
+  if (own) {
+    double w[4][kD / 2];
+    int seen[4] = {};
+    for (int x = 0; x < own->n; ++x) rope_rates(s, low, high, 2 * own->pairs[x], w[x]);
+    for (int i = 0; i < n; ++i) a.w[i] = w[axis[i]][seen[axis[i]]++];
+  } else {
+    rope_rates(s, low, high, rot, a.w);
   }
   a.amplitude = s->amplitude > 0 ? s->amplitude : (yarn ? 0.1 * std::log(s->factor) + 1.0 : 1.0);
   a.pairs = n;
@@ -364,9 +412,11 @@ int tsa_rope_table(const tsa_rope_spec* s, void* table, size_t bytes, tsa_rope* 
   return launched(launch_rope_table(a, static_cast<cudaStream_t>(stream)), "table launch");
 }
 
-int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
-               const tsa_rows* k_out, int Hkv, int64_t T, int d, const int32_t* positions,
-               const tsa_rope* rope, int inverse, void* stream) {
+// rope_apply, with axes (many) or without.
+int rope_run(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
+             const tsa_rows* k_out, int Hkv, int64_t T, int d, const int32_t* positions,
+             int64_t stride, const tsa_rope* rope, const tsa_rope_axes* axes, bool many,
+             int inverse, void* stream) {
   if (d != kD) return fail(TSA_ERR_INVALID_ARG, "d = %d: only d = 128 is compiled", d);
   if (Hq <= 0 || Hq > 8192 || Hkv < 0 || Hkv > 8192)
     return fail(TSA_ERR_INVALID_ARG, "Hq must be in [1, 8192], Hkv in [0, 8192]");
@@ -375,6 +425,7 @@ int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows*
   if (!rope) return fail(TSA_ERR_INVALID_ARG, "rope is NULL");
   int rc = check_rope(rope, a.rope);
   if (rc) return rc;
+  if (many && (rc = check_axes(axes, rope, stride, a.axes))) return rc;
   if (T == 0) return report_ok();
   if ((rc = check_rows(q, T, Hq, false, "q", a.q))) return rc;
   if ((rc = check_rows(q_out, T, Hq, true, "q_out", a.qo))) return rc;
@@ -395,19 +446,26 @@ int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows*
   return launched(launch_rope(a, static_cast<cudaStream_t>(stream)), "rotation launch");
 }
 
-int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
+// kv8_append, with axes (many) or without.
+int append_run(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
                const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens, int B, int Hkv,
-               int d, const tsa_rope* rope, const int32_t* positions, void* stream) {
+               int d, const tsa_rope* rope, const tsa_rope_axes* axes, bool many,
+               const int32_t* positions, int64_t stride, void* stream) {
   AppendArgs a{};
   int rc = check_batch(B, Hkv, d);
   if (rc) return rc;
   if ((rc = check_kv8(cache, Hkv, a.c))) return rc;
   if ((rc = check_tokens(T, max_new, cu_new, B, "max_new"))) return rc;
   if ((rc = check_rope(rope, a.rope))) return rc;
+  if (many) {
+    if (!rope) return fail(TSA_ERR_INVALID_ARG, "axes without rope");
+    if ((rc = check_axes(axes, rope, stride, a.axes))) return rc;
+  }
   if (B == 0 || T == 0 || max_new == 0) return report_ok();
   if ((rc = check_rows(k_new, T, Hkv, false, "k_new", a.k))) return rc;
   if ((rc = check_rows(v_new, T, Hkv, false, "v_new", a.v))) return rc;
   if (!lens) return fail(TSA_ERR_INVALID_ARG, "lens is NULL");
+  if (many && !positions) return fail(TSA_ERR_INVALID_ARG, "axes without positions");
   if ((T / cache->block + 2) * 2 * Hkv >= (int64_t)1 << 31)
     return fail(TSA_ERR_INVALID_ARG, "T * Hkv is too large");
   a.fmt = cache->format == TSA_KV8_INT8 ? kFmtInt8 : kFmtE4m3;
@@ -420,6 +478,62 @@ int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_ne
   a.positions = positions;
   a.status = cache->status;
   return launched(launch_kv8_append(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tsa_rope_table_size(int rot_dim, int64_t max_pos) {
+  if (!rope_sizes(rot_dim, max_pos)) return 0;
+  return (size_t)(kRopeLow + rope_high(max_pos)) * (rot_dim / 2) * sizeof(float2);
+}
+
+int tsa_rope_table(const tsa_rope_spec* s, void* table, size_t bytes, tsa_rope* rope,
+                   void* stream) {
+  return rope_table(s, nullptr, nullptr, table, bytes, rope, stream);
+}
+
+int tsa_rope_table_axes(const tsa_rope_spec* s, const tsa_rope_axes* axes, void* table,
+                        size_t bytes, tsa_rope* rope, void* stream) {
+  if (!s) return fail(TSA_ERR_INVALID_ARG, "spec is NULL");
+  int axis[kD / 2] = {};
+  if (rope_sizes(s->rot_dim, s->max_pos)) {  // (else refused below)
+    const int rc = axes_of(axes, s->rot_dim, axis);
+    if (rc) return rc;
+  }
+  const bool own = axes && axes->rates == TSA_RATES_OWN;
+  return rope_table(s, own ? axes : nullptr, axis, table, bytes, rope, stream);
+}
+
+int rope_apply(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
+               const tsa_rows* k_out, int Hkv, int64_t T, int d, const int32_t* positions,
+               const tsa_rope* rope, int inverse, void* stream) {
+  return rope_run(q, q_out, Hq, k, k_out, Hkv, T, d, positions, 0, rope, nullptr, false, inverse,
+                  stream);
+}
+
+int rope_apply_axes(const tsa_rows* q, const tsa_rows* q_out, int Hq, const tsa_rows* k,
+                    const tsa_rows* k_out, int Hkv, int64_t T, int d, const int32_t* positions,
+                    int64_t stride, const tsa_rope* rope, const tsa_rope_axes* axes, int inverse,
+                    void* stream) {
+  return rope_run(q, q_out, Hq, k, k_out, Hkv, T, d, positions, stride, rope, axes, true, inverse,
+                  stream);
+}
+
+int kv8_append(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
+               const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens, int B, int Hkv,
+               int d, const tsa_rope* rope, const int32_t* positions, void* stream) {
+  return append_run(cache, k_new, v_new, cu_new, T, max_new, lens, B, Hkv, d, rope, nullptr, false,
+                    positions, 0, stream);
+}
+
+int kv8_append_axes(const tsa_kv8* cache, const tsa_rows* k_new, const tsa_rows* v_new,
+                    const int32_t* cu_new, int64_t T, int max_new, const int32_t* lens, int B,
+                    int Hkv, int d, const tsa_rope* rope, const tsa_rope_axes* axes,
+                    const int32_t* positions, int64_t stride, void* stream) {
+  return append_run(cache, k_new, v_new, cu_new, T, max_new, lens, B, Hkv, d, rope, axes, true,
+                    positions, stride, stream);
 }
 
 int kv8_read(const tsa_kv8* cache, const tsa_rows* k_out, const tsa_rows* v_out,

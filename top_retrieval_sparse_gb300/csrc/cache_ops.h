@@ -38,12 +38,20 @@ struct RowsView {
   int64_t st, sh;
 };
 
+// Axes of the pairs: pair i's in bits 2 (i % 8) of half i / 8; n = 0: one position a token.
+struct AxesView {
+  int n;
+  int64_t stride;      // between the axes' positions
+  uint16_t of[kD / 16];
+};
+
 struct RopeArgs {
   RowsView q, qo, k, ko;
   int Hq, Hkv;
   int64_t T;
   const int32_t* positions;
   RopeView rope;
+  AxesView axes;
   int inverse;
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
@@ -100,6 +108,7 @@ struct AppendArgs {
   const int32_t* lens;
   int B;
   RopeView rope;
+  AxesView axes;
   const int32_t* positions;
   int* status;
 };

@@ -8,7 +8,11 @@ namespace tsa {
 
 namespace {
 
-enum { kStraight = 0, kTurnHalf = 1, kTurnInterleaved = 2 };
+// How keys are rotated: not, by one position a token (half, interleaved), by one on each
+// of several axes.
+enum { kStraight = 0, kTurnHalf = 1, kTurnInterleaved = 2, kAxesHalf = 3, kAxesInterleaved = 4 };
+constexpr bool is_axes(int kind) { return kind >= kAxesHalf; }
+constexpr bool is_half(int kind) { return kind == kTurnHalf || kind == kAxesHalf; }
 
 // Threads of an append CTA: one team of warps, so that none waits at another's
 // barriers (128K tokens of 8 heads, blocks of 64: 157 us with two teams a CTA, 117 us with
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / appe
   // the low ones are asked for with the rows, not after them.
   float x[KIND ? 4 : 1][16];
   if constexpr (KIND != kStraight) {
-    const bool own = turn && live && !a.positions && p0 + r1 <= a.rope.max_pos;
+    const bool own = !is_axes(KIND) && turn && live && !a.positions && p0 + r1 <= a.rope.max_pos;
     float4 lo[4][4], hi[4];
     if (own && ln.pair >= 0) {
       const int n8 = a.rope.pairs >> 3;
@@ -189,13 +193,17 @@ __global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / appe
         if (own) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) rope_sum(lo[i][e], hi[e], cs[2 * e], cs[2 * e + 1]);
+        } else if (is_axes(KIND)) {
+          if (!rope_angles_axes(a.rope, a.positions + tok0 + r, a.axes.stride, a.axes.of[l], l,
+                                cs) && a.status)
+            atomicOr(a.status, kStatusBadLength);
         } else {
           const int64_t at = a.positions ? (int64_t)a.positions[tok0 + r] : p0 + r;
           rope_angles(a.rope, at, l, cs);
           if (l == 0 && (at < 0 || at >= a.rope.max_pos) && a.status)
             atomicOr(a.status, kStatusBadLength);
         }
-        rope_turn(KIND == kTurnInterleaved, cs, u, v);
+        rope_turn(!is_half(KIND), cs, u, v);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / appe
       row_values(i, u, v);
       const uint2 cu = clean ? encode8<FMT, true>(u, inv) : encode8<FMT, false>(u, inv);
       const uint2 cv = clean ? encode8<FMT, true>(v, inv) : encode8<FMT, false>(v, inv);
-      if (KIND == kTurnHalf && ln.b != ln.a + 1) {
+      if (is_half(KIND) && ln.b != ln.a + 1) {
         *reinterpret_cast<uint2*>(out + r * kD + 8 * ln.a) = cu;
         *reinterpret_cast<uint2*>(out + r * kD + 8 * ln.b) = cv;
       } else {
@@ -367,6 +375,9 @@ cudaError_t append_kind(const AppendArgs& a, cudaStream_t st) {
 template <int FMT, int BLK>
 cudaError_t append_block(const AppendArgs& a, cudaStream_t st) {
   if (!a.rope.lo) return append_kind<FMT, BLK, kStraight>(a, st);
+  if (a.axes.n > 0)
+    return a.rope.interleaved ? append_kind<FMT, BLK, kAxesInterleaved>(a, st)
+                              : append_kind<FMT, BLK, kAxesHalf>(a, st);
   return a.rope.interleaved ? append_kind<FMT, BLK, kTurnInterleaved>(a, st)
                             : append_kind<FMT, BLK, kTurnHalf>(a, st);
 }

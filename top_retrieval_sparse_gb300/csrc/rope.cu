@@ -36,7 +36,7 @@ constexpr int kRopeBatch = 5;   // rows of eight lanes in flight
 // pairs, so no values change lanes.  A prompt of 32768 tokens, 32 + 8 heads: 113 us,
 // 5.9 TB/s (144 us with 16 lanes a row and shuffles).  It does not let the next kernel start
 // early: the key scan reads q and the keys before its dependency wait.
-template <int TOKENS, bool INTER>
+template <int TOKENS, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   constexpr int WAYS = kRopeThreads / 8 / TOKENS;
   pdl_wait();
@@ -52,7 +52,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   const int second = 8 * (ln.b - ln.a);
   float2 cs[8];
   if (ln.pair >= 0) {
-    rope_angles(a.rope, a.positions[t], threadIdx.x & 7, cs);
+    if (AXES)
+      rope_angles_axes(a.rope, a.positions + t, a.axes.stride, a.axes.of[threadIdx.x & 7],
+                       threadIdx.x & 7, cs);
+    else
+      rope_angles(a.rope, a.positions[t], threadIdx.x & 7, cs);
     if (a.inverse)
 #pragma unroll
       for (int e = 0; e < 8; ++e) cs[e].y = -cs[e].y;
@@ -88,13 +92,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   }
 }
 
-template <bool INTER>
+template <bool INTER, bool AXES>
 cudaError_t launch_layout(const RopeArgs& a, cudaStream_t st) {
   // Four tokens a CTA from two CTAs an SM on; below that latency counts.
   const dim3 th(kRopeThreads);
   if (a.T < 4 * 2 * 152)
-    return launch_dependent(rope_kernel<1, INTER>, dim3((unsigned)a.T), th, 0, st, a);
-  return launch_dependent(rope_kernel<4, INTER>, dim3((unsigned)((a.T + 3) / 4)), th, 0, st, a);
+    return launch_dependent(rope_kernel<1, INTER, AXES>, dim3((unsigned)a.T), th, 0, st, a);
+  return launch_dependent(rope_kernel<4, INTER, AXES>, dim3((unsigned)((a.T + 3) / 4)), th, 0, st,
+                          a);
 }
 
 }  // namespace
@@ -108,7 +113,10 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
-  return a.rope.interleaved ? launch_layout<true>(a, st) : launch_layout<false>(a, st);
+  if (a.axes.n > 0)
+    return a.rope.interleaved ? launch_layout<true, true>(a, st) : launch_layout<false, true>(a, st);
+  return a.rope.interleaved ? launch_layout<true, false>(a, st)
+                            : launch_layout<false, false>(a, st);
 }
 
 }  // namespace tsa

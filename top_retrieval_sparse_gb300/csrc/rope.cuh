@@ -37,6 +37,32 @@ __device__ __forceinline__ void rope_angles(const RopeView& r, int64_t t, int l,
   for (int e = 0; e < 4; ++e) rope_sum(lo[n8 * e], hi[n8 * e], cs[2 * e], cs[2 * e + 1]);
 }
 
+// The same with a position for each axis of the eight pairs (`of`: their axes, two bits
+// each).  Pieces of 8 bytes, since neighbours may turn by different positions; false: a
+// position is out of range (its pairs are NaN).
+__device__ __forceinline__ bool rope_angles_axes(const RopeView& r, const int32_t* positions,
+                                                 int64_t stride, uint32_t of, int l,
+                                                 float2 (&cs)[8]) {
+  const int n8 = r.pairs >> 3;
+  bool good = true;
+  int32_t t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = positions[((of >> (2 * e)) & 3u) * stride];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if ((uint32_t)t[e] >= (uint64_t)r.max_pos) {
+      cs[e] = make_float2(nanf(""), nanf(""));
+      good = false;
+      continue;
+    }
+    const int place = 2 * (n8 * (e >> 1) + l) + (e & 1);
+    const float2 a = r.lo[(int64_t)(t[e] & (kRopeLow - 1)) * r.pairs + place];
+    const float2 b = r.hi[(int64_t)(t[e] >> kRopeLowBits) * r.pairs + place];
+    cs[e] = make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+  }
+  return good;
+}
+
 // A row is turned by eight lanes, 16 elements each as two pieces of 8 (lane l's
 // pieces `a` and `b`, numbered in the row), such that a lane holds both elements of its
 // eight pairs: the pieces of both halves in the half layout, neighbours in the
