@@ -664,6 +664,36 @@ TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* l
                                float scale, float* out, float* lse_out, void* workspace,
                                size_t ws_bytes, void* stream);
 
+/* shared_attn_decode / kv8_shared_attn_decode -- one step of a batch whose sequences share
+ * their first rows (samples of one prompt, requests under one system prompt, beams).
+ *
+ * Sequences [cu_group[n], cu_group[n+1]) are group n (cu_group: int32 [N+1], device, rising
+ * within [0, B]); sequences before the first and behind the last group share nothing.
+ * shared: int32 [N] (device): the group's sequences all begin with the same shared[n] rows,
+ * and these are read once for the group, from the cache of its first sequence; sequence b
+ * then reads its own rows [shared[n], lens[b]).  (After pages_fork the page tables name the
+ * shared pages in every sequence; here only the first one's entries for them are looked up.)
+ *   q: bf16 [B][Hq][128]; lens: int32 [B] (device), 0: an empty place, its out 0, lse -inf;
+ *   out: [B][Hq][128] = softmax(scale q.k) . v over both, fp32, or bf16 with out_bf16 != 0;
+ *   lse_out: fp32 [B][Hq] or NULL.
+ *   Visible rows must be finite; limits as kv8_attn_decode, and N <= 4096.
+ *   workspace: tsa_shared_attn_workspace_size() bytes, 256-byte aligned, zero-filled before
+ *   its first use; calls of either entry point and of whatever sizes may share one.
+ * Device-detected errors (on the workspace): a lens[b] or shared[n] outside [0, l_cap] is
+ * clamped and flagged; 0 < lens[b] < shared[n] is flagged and gives NaN; offsets that do not
+ * rise are flagged and give NaN everywhere; pages as kv8_attn_decode (a bad page of the
+ * shared rows: NaN for all of the group). */
+TSA_API size_t tsa_shared_attn_workspace_size(int B, int N, int Hq, int Hkv, int d);
+TSA_API int shared_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int B,
+                               const int32_t* cu_group, const int32_t* shared, int N, int Hq,
+                               int Hkv, int d, float scale, void* out, int out_bf16,
+                               float* lse_out, void* workspace, size_t ws_bytes, void* stream);
+TSA_API int kv8_shared_attn_decode(const void* q, const tsa_kv8* cache, const int32_t* lens,
+                                   int B, const int32_t* cu_group, const int32_t* shared, int N,
+                                   int Hq, int Hkv, int d, float scale, void* out, int out_bf16,
+                                   float* lse_out, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
 /* window_attn_prefill -- the same for many new tokens per sequence, over a
  * bf16 cache that holds them already (prompts, chunks of prompts).
  *

@@ -27,7 +27,9 @@ __all__ = [
     "set_trace", "read_trace", "kernel_launches", "sparse_attn_decode_noalloc",
     "noalloc_scratch_bytes", "RopeTable", "rope", "KV8", "kv8_append", "kv8_read",
     "attn_decode_workspace", "kv8_attn_decode", "window_attn_decode",
-    "window_attn_prefill_workspace", "window_attn_prefill",
+    "window_attn_prefill_workspace", "window_attn_prefill", "shared_attn_decode",
+    "shared_attn_decode_workspace", "Pages", "pages_alloc", "pages_free", "pages_fork",
+    "pages_compact", "pages_copy",
 ]
 
 TSA_OK = 0
@@ -56,6 +58,20 @@ class _RopeSpec(C.Structure):
 class _RopeStruct(C.Structure):
     _fields_ = [("table", C.c_void_p), ("max_pos", C.c_int64), ("rot_dim", C.c_int32),
                 ("layout", C.c_int32)]
+
+
+class _RopeAxes(C.Structure):
+    _fields_ = [("n", C.c_int32), ("order", C.c_int32), ("rates", C.c_int32),
+                ("pairs", C.c_int32 * 4)]
+
+
+class _PagesStruct(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("refs", C.c_void_p), ("B", C.c_int32),
+                ("max_pages", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32)]
+
+
+class _PageBuf(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("bytes", C.c_int64)]
 
 
 class _RowsStruct(C.Structure):
@@ -136,6 +152,20 @@ def lib():
             L.rope_apply.argtypes = [P, P, i32, P, P, i32, i64, i32, P, P, i32, P]
             L.kv8_append.argtypes = [P, P, P, P, i64, i32, P, i32, i32, i32, P, P, P]
             L.kv8_read.argtypes = [P, P, P, P, i64, i32, P, i32, i32, i32, P]
+            L.tsa_rope_table_axes.argtypes = [P, P, P, sz, P, P]
+            L.rope_apply_axes.argtypes = [P, P, i32, P, P, i32, i64, i32, P, i64, P, P, i32, P]
+            L.kv8_append_axes.argtypes = [P, P, P, P, i64, i32, P, i32, i32, i32, P, P, P, i64, P]
+            L.tsa_pages_workspace_size.argtypes = [i32, i32, i32]
+            L.tsa_pages_workspace_size.restype = sz
+            for fn in (L.pages_alloc, L.pages_free):
+                fn.argtypes = [P, P, P, P, sz, P]
+            L.pages_fork.argtypes = [P, P, P, P, i32, P, P, P, sz, P]
+            L.pages_compact.argtypes = [P, P, P, P, P, sz, P]
+            L.pages_copy.argtypes = [P, i32, i32, P, P, P, i32, P, P]
+            L.tsa_shared_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+            L.tsa_shared_attn_workspace_size.restype = sz
+            for fn in (L.shared_attn_decode, L.kv8_shared_attn_decode):
+                fn.argtypes = [P, P, P, i32, P, P, i32, i32, i32, i32, f32, P, i32, P, P, sz, P]
             L.tsa_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32]
             L.tsa_attn_decode_workspace_size.restype = sz
             for fn in (L.kv8_attn_decode, L.window_attn_decode):
@@ -555,6 +585,8 @@ class ReTopK:
 # --------------------------------------------- cache-side operators
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}
 _ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_ROPE_ORDER = {"blocks": 0, "turns": 1}
+_ROPE_RATES = {"joint": 0, "own": 1}
 _KV8_FORMAT = {"int8": 0, "e4m3": 1}
 
 
@@ -656,16 +688,32 @@ class RopeTable:
     layout: "half" (pairs i, i + rot_dim/2) or "interleaved" (2i, 2i + 1);
     scaling: "none", "linear", "ntk", "by_parts" or "yarn" (see include/tsa.h)
     with `factor` and `orig_len`; low, high and amplitude default to the kind's.
+
+    sections: pairs of every axis (two to four numbers that add up to rot_dim / 2, or
+    one) where tokens have positions on several axes; order: "blocks" (axis after
+    axis) or "turns" (dealt in turn); rates: "joint" (of the whole table) or "own" (of
+    each axis by itself).  See tsa_rope_axes in include/tsa.h.
     """
 
     def __init__(self, rot_dim: int, max_pos: int, theta: float = 10000.0, layout: str = "half",
                  scaling: Optional[str] = None, factor: float = 1.0, orig_len: int = 0,
                  low: float = 0.0, high: float = 0.0, amplitude: float = 0.0, device="cuda",
-                 stream=None):
+                 stream=None, sections=None, order: str = "blocks", rates: str = "joint"):
         if layout not in _ROPE_LAYOUT:
             raise ValueError(f"layout {layout!r}: one of {sorted(_ROPE_LAYOUT)}")
         if (scaling or "none") not in _ROPE_SCALING:
             raise ValueError(f"scaling {scaling!r}: one of {sorted(_ROPE_SCALING)}")
+        for what, val, known in (("order", order, _ROPE_ORDER), ("rates", rates, _ROPE_RATES)):
+            if val not in known:
+                raise ValueError(f"{what} {val!r}: one of {sorted(known)}")
+        self.sections = None if sections is None else tuple(int(x) for x in sections)
+        self._axes = None
+        if self.sections is not None:
+            if not 1 <= len(self.sections) <= 4:
+                raise ValueError(f"sections {self.sections}: one to four axes")
+            pairs = (C.c_int32 * 4)(*[_count(x, "sections") for x in self.sections])
+            self._axes = C.byref(_RopeAxes(len(self.sections), _ROPE_ORDER[order],
+                                           _ROPE_RATES[rates], pairs))
         n = int(lib().tsa_rope_table_size(int(rot_dim), int(max_pos)))
         if n == 0:
             raise TsaError(-1, f"invalid rotation sizes (rot_dim {rot_dim}, max_pos {max_pos})")
@@ -679,14 +727,39 @@ class RopeTable:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.table = _new(stream, dev, (n,), torch.uint8)
         self.device = self.table.device
-        _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table, C.byref(spec),
-                _ptr(self.table), n, self._ref)
+        if self._axes is None:
+            _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table, C.byref(spec),
+                    _ptr(self.table), n, self._ref)
+        else:
+            _run_on(_gpu((self.table, "table")), stream, lib().tsa_rope_table_axes, C.byref(spec),
+                    self._axes, _ptr(self.table), n, self._ref)
+
+
+def _axis_positions(positions: torch.Tensor, table: RopeTable, T: int) -> int:
+    """Whether positions are [axes][T] (then their stride), or [T] (then -1)."""
+    if positions.dim() == 1:
+        _want(positions, torch.int32, "positions")
+        if positions.shape != (T,):
+            raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
+        return -1
+    if positions.dtype != torch.int32:
+        raise TypeError(f"positions must be {torch.int32}, got {positions.dtype}")
+    if table is None or table.sections is None:
+        raise ValueError("positions of several axes need a RopeTable with sections")
+    A = len(table.sections)
+    if positions.shape != (A, T):
+        raise ValueError(f"positions must be int32 [{A}][{T}] (or [{T}]), got "
+                         f"{tuple(positions.shape)}")
+    if T > 1 and positions.stride(1) != 1:
+        raise ValueError("positions must have contiguous rows")
+    return positions.stride(0)
 
 
 def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
          k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
          k_out: Optional[torch.Tensor] = None, inverse: bool = False, stream=None):
-    """Rotates q bf16 [T][Hq][128] (and k [T][Hkv][128]) by positions int32 [T].
+    """Rotates q bf16 [T][Hq][128] (and k [T][Hkv][128]) by positions int32 [T], or
+    [axes][T] with a table of several axes.
 
     Rows may be strided (a slice of a fused projection); q_out=q rotates in
     place.  Returns (q_out, k_out)."""
@@ -695,10 +768,8 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
             k is not None and k.device != dev or q_out is not None or k_out is not None:
         _gpu((q, "q"), (positions, "positions"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"),
              (table.table, "table"))
-    _want(positions, torch.int32, "positions")
     T, Hq, d = q.shape
-    if positions.shape != (T,):
-        raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
+    stride = _axis_positions(positions, table, T)
     if q_out is None:
         q_out = _new(stream, dev, (T, Hq, d), torch.bfloat16)
     elif q_out.shape != q.shape:
@@ -712,8 +783,13 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable,
         Hkv, ks, kos = k.shape[1], _rows(k, "k"), _rows(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _run_on(dev, stream, lib().rope_apply, _rows(q, "q"), _rows(q_out, "q_out"),
-            Hq, ks, kos, Hkv, T, d, _ptr(positions), table._ref, 1 if inverse else 0)
+    if stride < 0:
+        _run_on(dev, stream, lib().rope_apply, _rows(q, "q"), _rows(q_out, "q_out"),
+                Hq, ks, kos, Hkv, T, d, _ptr(positions), table._ref, 1 if inverse else 0)
+    else:
+        _run_on(dev, stream, lib().rope_apply_axes, _rows(q, "q"), _rows(q_out, "q_out"),
+                Hq, ks, kos, Hkv, T, d, _ptr(positions), stride, table._ref, table._axes,
+                1 if inverse else 0)
     return q_out, k_out
 
 
@@ -799,22 +875,24 @@ def kv8_append(cache: KV8, k_new: torch.Tensor, v_new: torch.Tensor, lens: torch
                stream=None) -> KV8:
     """Writes new tokens' rows (bf16 [T][Hkv][128], strided allowed) at the
     last positions before lens[b], quantised, the keys rotated if `rope` is
-    given (at positions int32 [T], or their own).  Ragged with cu_new int32
-    [B+1] and max_new, else T / B tokens a sequence."""
+    given (at positions int32 [T], [axes][T] with a table of several axes, or their
+    own).  Ragged with cu_new int32 [B+1] and max_new, else T / B tokens a sequence."""
     B = _cache_batch(cache, lens)
     dev = _gpu((cache.k, "cache"), (k_new, "k_new"), (v_new, "v_new"), (lens, "lens"),
                (cu_new, "cu_new"), (positions, "positions"), (rope.table if rope else None, "rope"))
     T = k_new.shape[0]
     if k_new.shape != (T, cache.Hkv, cache.d) or v_new.shape != k_new.shape:
         raise ValueError(f"k_new and v_new must be [T][{cache.Hkv}][{cache.d}]")
-    if positions is not None:
-        _want(positions, torch.int32, "positions")
-        if positions.shape != (T,):
-            raise ValueError(f"positions must be int32 [{T}], got {tuple(positions.shape)}")
+    stride = -1 if positions is None else _axis_positions(positions, rope, T)
     n = _offsets(cu_new, T, max_new, B, "max_new")
-    _run_on(dev, stream, lib().kv8_append, cache._ref, _rows(k_new, "k_new"),
-            _rows(v_new, "v_new"), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
-            rope._ref if rope else None, _ptr(positions))
+    if stride < 0:
+        _run_on(dev, stream, lib().kv8_append, cache._ref, _rows(k_new, "k_new"),
+                _rows(v_new, "v_new"), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
+                rope._ref if rope else None, _ptr(positions))
+    else:
+        _run_on(dev, stream, lib().kv8_append_axes, cache._ref, _rows(k_new, "k_new"),
+                _rows(v_new, "v_new"), _ptr(cu_new), T, n, _ptr(lens), B, cache.Hkv, cache.d,
+                rope._ref, rope._axes, _ptr(positions), stride)
     return cache
 
 
@@ -951,3 +1029,182 @@ def window_attn_prefill(q: torch.Tensor, kv: KV, lens: torch.Tensor, n_init: int
             _ptr(cu_q), T, n, _ptr(lens), B, Hq, kv.Hkv, d, int(n_init), nr, float(scale),
             _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.nbytes)
     return out, lse_out
+
+
+def shared_attn_decode_workspace(B: int, N: int, Hq: int, Hkv: int, d: int = 128,
+                                 device="cuda") -> torch.Tensor:
+    """A zeroed workspace of shared_attn_decode for N groups."""
+    n = int(lib().tsa_shared_attn_workspace_size(B, N, Hq, Hkv, d))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def shared_attn_decode(q: torch.Tensor, cache, lens: torch.Tensor, cu_group: torch.Tensor,
+                       shared: torch.Tensor, scale: Optional[float] = None,
+                       out: Optional[torch.Tensor] = None,
+                       lse_out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """One decode step of a batch in groups that share their first rows: sequences
+    [cu_group[n], cu_group[n+1]) (int32 [N+1]) begin with the same shared[n] rows (int32
+    [N]), which are read once a group.  q: bf16 [B][Hq][128]; cache: a KV or a KV8.
+    Returns (out [B][Hq][128], fp32 unless a bf16 one is passed, lse_out)."""
+    B = _cache_batch(cache, lens)
+    _want(q, torch.bfloat16, "q")
+    Bq, Hq, d = q.shape
+    if Bq != B:
+        raise ValueError(f"q has {Bq} sequences, lens {B}")
+    _want(cu_group, torch.int32, "cu_group")
+    _want(shared, torch.int32, "shared")
+    N = shared.numel()
+    if shared.dim() != 1 or cu_group.shape != (N + 1,):
+        raise ValueError("cu_group must be int32 [N + 1], shared int32 [N]")
+    dev = _gpu((q, "q"), (cache.k, "cache"), (lens, "lens"), (cu_group, "cu_group"),
+               (shared, "shared"), (out, "out"), (lse_out, "lse_out"), (workspace, "workspace"))
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = _new(stream, dev, (B, Hq, d), torch.float32)
+    elif out.shape != q.shape or out.dtype not in (torch.float32, torch.bfloat16) or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous fp32 or bf16 tensor of q's shape")
+    if lse_out is not None:
+        _want(lse_out, torch.float32, "lse_out")
+        if lse_out.shape != (B, Hq):
+            raise ValueError(f"lse_out must be fp32 [{B}][{Hq}]")
+    if workspace is None:
+        n = int(lib().tsa_shared_attn_workspace_size(B, N, Hq, cache.Hkv, d))
+        workspace = _new(stream, dev, (max(n, 256),), torch.uint8, zero=True)
+    fn, ref = (lib().kv8_shared_attn_decode, cache._ref) if isinstance(cache, KV8) else \
+        (lib().shared_attn_decode, C.byref(cache.struct))
+    _run_on(dev, stream, fn, _ptr(q), ref, _ptr(lens), B, _ptr(cu_group), _ptr(shared), N, Hq,
+            cache.Hkv, d, float(scale), _ptr(out), 1 if out.dtype == torch.bfloat16 else 0,
+            _ptr(lse_out), _ptr(workspace), workspace.nbytes)
+    return out, lse_out
+
+
+class Pages:
+    """Which pages of a pool the sequences have (tsa_pages in include/tsa.h).
+
+    table: int32 [B][max_pages], the page table of the layers' caches (entries without a
+    page are -1); refs: int32 [n_pages], how many entries name a page (0: free).  Calls on
+    one Pages must be ordered on a stream; workspace_status(pages.workspace) tells what
+    they flagged."""
+
+    def __init__(self, table: torch.Tensor, refs: torch.Tensor, page_size: int):
+        _want(table, torch.int32, "table")
+        _want(refs, torch.int32, "refs")
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError("table must be int32 [B][max_pages], refs int32 [n_pages]")
+        self.device = _gpu((table, "table"), (refs, "refs"))
+        self.table, self.refs, self.page_size = table, refs, int(page_size)
+        self.B, self.max_pages = table.shape
+        self.n_pages = refs.numel()
+        n = int(lib().tsa_pages_workspace_size(self.B, self.max_pages, self.n_pages))
+        self.workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+        self.struct = _PagesStruct(table.data_ptr(), refs.data_ptr(), self.B, self.max_pages,
+                                   self.n_pages, self.page_size)
+        self._ref = C.byref(self.struct)
+
+    @classmethod
+    def empty(cls, B: int, max_pages: int, n_pages: int, page_size: int,
+              device="cuda") -> "Pages":
+        """All pages free, no sequence with any."""
+        return cls(torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device), page_size)
+
+    def _run(self, fn, stream, *args):
+        _run_on(self.device, stream, fn, self._ref, *args, self.workspace.data_ptr(),
+                self.workspace.nbytes)
+
+    def _range(self, lo, hi):
+        for t, name in ((lo, "lo"), (hi, "hi")):
+            _want(t, torch.int32, name)
+            if t.shape != (self.B,):
+                raise ValueError(f"{name} must be int32 [{self.B}], got {tuple(t.shape)}")
+        _gpu((self.table, "pages"), (lo, "lo"), (hi, "hi"))
+        return lo.data_ptr(), hi.data_ptr()
+
+
+def pages_alloc(pages: Pages, lo: torch.Tensor, hi: torch.Tensor, stream=None) -> Pages:
+    """Gives sequence b a free page (the lowest ones) for every entry that holds a
+    position of [lo[b], hi[b]) and has none."""
+    pages._run(lib().pages_alloc, stream, *pages._range(lo, hi))
+    return pages
+
+
+def pages_free(pages: Pages, lo: torch.Tensor, hi: torch.Tensor, stream=None) -> Pages:
+    """Takes from sequence b the pages that lie in positions [lo[b], hi[b]) altogether."""
+    pages._run(lib().pages_free, stream, *pages._range(lo, hi))
+    return pages
+
+
+def pages_fork(pages: Pages, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor,
+               src: Optional[torch.Tensor] = None, dst: Optional[torch.Tensor] = None,
+               stream=None):
+    """Sequence children[i] becomes the first lens[i] positions of parents[i]: whole
+    pages are shared, a partial last one gets a page of its own.  Returns (src, dst),
+    int32 [n], the pages that pages_copy has to copy (-1: none)."""
+    n = parents.numel()
+    for t, name in ((parents, "parents"), (children, "children"), (lens, "lens"), (src, "src"),
+                    (dst, "dst")):
+        if t is not None:
+            _want(t, torch.int32, name)
+            if t.shape != (n,):
+                raise ValueError(f"{name} must be int32 [{n}], got {tuple(t.shape)}")
+    dev = _gpu((pages.table, "pages"), (parents, "parents"), (children, "children"),
+               (lens, "lens"), (src, "src"), (dst, "dst"))
+    src = _new(stream, dev, (n,), torch.int32) if src is None else src
+    dst = _new(stream, dev, (n,), torch.int32) if dst is None else dst
+    pages._run(lib().pages_fork, stream, _ptr(parents), _ptr(children), _ptr(lens), n, _ptr(src),
+               _ptr(dst))
+    return src, dst
+
+
+def pages_compact(pages: Pages, src: Optional[torch.Tensor] = None,
+                  dst: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Moves the pages in use to the front of the pool (tables and counts; the rows are
+    moved by pages_copy).  Returns (src, dst, count): int32 [n_pages // 2] twice, padded
+    with -1, and int32 [1]."""
+    n = pages.n_pages // 2
+    for t, name, size in ((src, "src", n), (dst, "dst", n), (count, "count", 1)):
+        if t is not None:
+            _want(t, torch.int32, name)
+            if t.shape != (size,):
+                raise ValueError(f"{name} must be int32 [{size}], got {tuple(t.shape)}")
+    dev = _gpu((pages.table, "pages"), (src, "src"), (dst, "dst"), (count, "count"))
+    src = _new(stream, dev, (n,), torch.int32) if src is None else src
+    dst = _new(stream, dev, (n,), torch.int32) if dst is None else dst
+    count = _new(stream, dev, (1,), torch.int32) if count is None else count
+    pages._run(lib().pages_compact, stream, _ptr(src), _ptr(dst), _ptr(count))
+    return src, dst, count
+
+
+def pages_copy(caches, src: torch.Tensor, dst: torch.Tensor,
+               count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copies page src[i] over page dst[i] (int32 [n], -1: none) in every cache given (a
+    paged KV or KV8, or a list of them, of one pool size); count: int32 [1], how many
+    pairs count."""
+    caches = list(caches) if isinstance(caches, (list, tuple)) else [caches]
+    n = src.numel()
+    for t, name, shape in ((src, "src", (n,)), (dst, "dst", (n,)), (count, "count", (1,))):
+        if t is not None:
+            _want(t, torch.int32, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be int32 {list(shape)}, got {tuple(t.shape)}")
+    if not caches:
+        return
+    bufs = []
+    for c in caches:
+        if c.page_table is None:
+            raise ValueError("pages_copy needs paged caches")
+        if c.k.shape[0] != caches[0].k.shape[0]:
+            raise ValueError("the caches' pools must have the same number of pages")
+        bufs += [c.k, c.v] + ([c.k_scale, c.v_scale] if isinstance(c, KV8) else [])
+    dev = _gpu((src, "src"), (dst, "dst"), (count, "count"), *((b, "a cache") for b in bufs))
+    n_pages = bufs[0].shape[0]
+    if n_pages == 0:
+        return
+    arr = (_PageBuf * len(bufs))(*[(b.data_ptr(), b.nbytes // n_pages) for b in bufs])
+    status = next((c.status for c in caches if getattr(c, "status", None) is not None), None)
+    _run_on(dev, stream, lib().pages_copy, arr, len(bufs), n_pages, _ptr(src), _ptr(dst),
+            _ptr(count), n, _ptr(status))

@@ -275,6 +275,16 @@ size_t prefill_bytes(const PrefillCut& c) {
   return prefill_sums(c) + (c.folds ? (size_t)kFoldPlaces * 2 * 128 * kD * sizeof(float) : 0);
 }
 
+// CTAs of a decode step: as many as fit at once, fewer where even the longest sequences
+// would not fill the smallest shares (8 slabs of 16 rows).
+int decode_grid(int64_t units, int64_t rows, int fmt) {
+  const int64_t slabs = units * ((rows + 15) / 16 + 1);
+  int64_t grid = num_sms() * attn_decode_ctas(fmt);
+  if (grid > kDecodeShares) grid = kDecodeShares;
+  if (grid > (slabs + 7) / 8) grid = (slabs + 7) / 8;
+  return (int)grid;
+}
+
 // Both decode entry points after their cache's checks.
 int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, int B, int Hq,
                int Hkv, int64_t n_init, int64_t n_recent, float scale, float* out,
@@ -307,16 +317,102 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   a.status = reinterpret_cast<int*>(ws);
   a.partial = reinterpret_cast<float*>(ws + kDecodePartial);
   a.arrived = reinterpret_cast<uint32_t*>(ws + kDecodeArrived);
-  // CTAs: as many as fit at once, fewer where even the longest sequences
-  // would not fill the smallest shares (8 slabs of 16 rows).
   const int64_t cap = c.l_cap;
   const int64_t seen = (n_init < cap ? n_init : cap) + (n_recent < cap ? n_recent : cap) + 32;
-  const int64_t slabs = (int64_t)B * Hkv * (((seen < cap ? seen : cap) + 15) / 16 + 1);
-  int64_t grid = num_sms() * attn_decode_ctas(fmt);
-  if (grid > kDecodeShares) grid = kDecodeShares;
-  if (grid > (slabs + 7) / 8) grid = (slabs + 7) / 8;
-  return launched(launch_attn_decode(a, fmt, (int)grid, static_cast<cudaStream_t>(stream)),
+  const int grid = decode_grid((int64_t)B * Hkv, seen < cap ? seen : cap, fmt);
+  return launched(launch_attn_decode(a, fmt, grid, static_cast<cudaStream_t>(stream)),
                   "attention launch");
+}
+
+// Workspace of a step with shared rows.  Nothing but the status word outlasts a call, so
+// that calls of whatever sizes may share it.
+struct SharedLayout {
+  size_t partial, arrived, rows, own, sh, total;
+};
+SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
+  SharedLayout l{};
+  (void)N;
+  const size_t row = round_up((size_t)B * Hq * (kD + 1) * sizeof(float));
+  l.partial = kDecodePartial;
+  l.arrived = kDecodeArrived;
+  l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));
+  l.own = l.rows + 5 * round_up((size_t)B * sizeof(int32_t));
+  l.sh = l.own + row;
+  l.total = l.sh + row;
+  return l;
+}
+
+// Both entry points of a step with shared rows after their cache's checks.
+int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, int B,
+               const int32_t* cu, const int32_t* shared, int N, int Hq, int Hkv, float scale,
+               void* out, int out16, float* lse_out, void* workspace, size_t ws_bytes,
+               void* stream) {
+  int rc = check_window(0, 0, scale);
+  if (rc) return rc;
+  if (N < 0 || N > 4096) return fail(TSA_ERR_INVALID_ARG, "N = %d: must be in [0, 4096]", N);
+  if (B == 0) return report_ok();
+  if (!q || !out || !lens) return fail(TSA_ERR_INVALID_ARG, "q, out and lens must be non-NULL");
+  if (!cu || (N > 0 && !shared))
+    return fail(TSA_ERR_INVALID_ARG, "cu_group and shared must be non-NULL");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(TSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const SharedLayout l = shared_layout(B, N, Hq, Hkv);
+  if ((rc = check_workspace(workspace, ws_bytes, l.total))) return rc;
+  const int64_t pool = c.page_table ? (fmt == kFmtBf16 ? 0 : (int64_t)c.n_pages << c.page_shift)
+                                    : (int64_t)B * c.l_cap;
+  if (pool > (int64_t)0xffffffff / Hkv)
+    return fail(TSA_ERR_INVALID_ARG, "the cache has 2^32 rows or more");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedArgs s{};
+  s.q = static_cast<const uint16_t*>(q);
+  s.c = c;
+  s.lens = lens;
+  s.cu = cu;
+  s.shared = shared;
+  s.B = B;
+  s.N = N;
+  s.Hq = Hq;
+  s.scale_log2 = (float)((double)scale * kLog2e);
+  s.out = out;
+  s.out16 = out16;
+  s.lse = lse_out;
+  s.status = reinterpret_cast<int*>(ws);
+  const size_t ints = round_up((size_t)B * sizeof(int32_t)), rows = (size_t)B * Hq;
+  s.group = reinterpret_cast<int32_t*>(ws + l.rows);
+  s.start = reinterpret_cast<int32_t*>(ws + l.rows + ints);
+  s.leader = reinterpret_cast<int32_t*>(ws + l.rows + 2 * ints);
+  s.zero = reinterpret_cast<int32_t*>(ws + l.rows + 3 * ints);
+  s.self = reinterpret_cast<int32_t*>(ws + l.rows + 4 * ints);
+  s.own_out = reinterpret_cast<float*>(ws + l.own);
+  s.own_lse = s.own_out + rows * kD;
+  s.sh_out = reinterpret_cast<float*>(ws + l.sh);
+  s.sh_lse = s.sh_out + rows * kD;
+  s.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
+  DecodeArgs a{};
+  a.q = s.q;
+  a.c = c;
+  a.B = B;
+  a.Hq = Hq;
+  a.scale_log2 = s.scale_log2;
+  a.status = s.status;
+  a.partial = reinterpret_cast<float*>(ws + l.partial);
+  a.arrived = s.arrived;
+  const int grid = decode_grid((int64_t)B * Hkv, c.l_cap, fmt);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = launched(launch_shared_prep(s, st), "groups launch"))) return rc;
+  a.lens = s.start;  // rows [0, start) of the leader's cache
+  a.start = s.zero;
+  a.from = s.leader;
+  a.out = s.sh_out;
+  a.lse = s.sh_lse;
+  if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;
+  a.lens = lens;
+  a.start = s.start;
+  a.from = s.self;
+  a.out = s.own_out;
+  a.lse = s.own_lse;
+  if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;
+  return launched(launch_shared_join(s, st), "join launch");
 }
 
 // The rates w_i of a rotation of `rot` elements.
@@ -585,6 +681,38 @@ int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int
   if ((rc = check_cache(kv, Hkv, c))) return rc;
   return decode_run(q, c, kFmtBf16, lens, B, Hq, Hkv, n_init, n_recent, scale, out, lse_out,
                     workspace, ws_bytes, stream);
+}
+
+size_t tsa_shared_attn_workspace_size(int B, int N, int Hq, int Hkv, int d) {
+  if (B <= 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d != kD) return 0;
+  return shared_layout(B, N, Hq, Hkv).total;
+}
+
+int shared_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int B,
+                       const int32_t* cu_group, const int32_t* shared, int N, int Hq, int Hkv,
+                       int d, float scale, void* out, int out_bf16, float* lse_out,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  CacheView c;
+  int rc = check_batch(B, Hkv, d);
+  if (rc) return rc;
+  if ((rc = check_groups(B, Hq, Hkv))) return rc;
+  if ((rc = check_cache(kv, Hkv, c))) return rc;
+  return shared_run(q, c, kFmtBf16, lens, B, cu_group, shared, N, Hq, Hkv, scale, out,
+                    out_bf16 != 0, lse_out, workspace, ws_bytes, stream);
+}
+
+int kv8_shared_attn_decode(const void* q, const tsa_kv8* cache, const int32_t* lens, int B,
+                           const int32_t* cu_group, const int32_t* shared, int N, int Hq,
+                           int Hkv, int d, float scale, void* out, int out_bf16, float* lse_out,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  CacheView c;
+  int rc = check_batch(B, Hkv, d);
+  if (rc) return rc;
+  if ((rc = check_groups(B, Hq, Hkv))) return rc;
+  if ((rc = check_kv8(cache, Hkv, c))) return rc;
+  return shared_run(q, c, cache->format == TSA_KV8_INT8 ? kFmtInt8 : kFmtE4m3, lens, B, cu_group,
+                    shared, N, Hq, Hkv, scale, out, out_bf16 != 0, lse_out, workspace, ws_bytes,
+                    stream);
 }
 
 size_t window_attn_prefill_workspace_size(int B, int Hq, int Hkv, int d, int max_q, int64_t l_cap,

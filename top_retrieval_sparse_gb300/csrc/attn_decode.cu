@@ -158,12 +158,18 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct Visible {
   int L, n0, lo, s0, sw, n;
 };
+template <bool SHARED>
 __device__ __forceinline__ Visible visible(const DecodeArgs& a, int b) {
   Visible v;
   const int len = a.lens[b], cap = (int)a.c.l_cap;
   v.L = len < 0 ? 0 : (len > cap ? cap : len);
-  v.n0 = a.n_init < v.L ? (int)a.n_init : v.L;
-  v.lo = a.n_recent < v.L ? v.L - (int)a.n_recent : 0;
+  if (SHARED) {
+    v.n0 = 0;
+    v.lo = a.start[b];
+  } else {
+    v.n0 = a.n_init < v.L ? (int)a.n_init : v.L;
+    v.lo = a.n_recent < v.L ? v.L - (int)a.n_recent : 0;
+  }
   v.s0 = (int)(((uint32_t)v.n0 + 15) >> 4);
   v.sw = v.lo >> 4 > v.s0 ? v.lo >> 4 : v.s0;
   const int se = (int)(((uint32_t)v.L + 15) >> 4);
@@ -201,7 +207,7 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, in
 __host__ __device__ constexpr int slabs_of(int fmt) { return fmt == kFmtE4m3 ? 2 : 1; }
 __host__ __device__ constexpr int ctas_of(int fmt) { return fmt == kFmtInt8 ? 4 : 3; }
 
-template <int FMT>
+template <int FMT, bool SHARED>
 __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kernel(DecodeArgs a) {
   constexpr bool B16 = FMT == kFmtBf16;
   constexpr int NS = slabs_of(FMT);      // slabs a warp works on at once
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     const int b = b0 + me;
     int64_t n = 0;
     if (b < a.B) {
-      const Visible v = visible(a, b);
+      const Visible v = visible<SHARED>(a, b);
       n = (int64_t)v.n * Hkv;
       if (blockIdx.x == 0 && v.L != a.lens[b]) atomicOr(a.status, kStatusBadLength);
       if (n == 0 && b % gridDim.x == blockIdx.x)  // nothing visible
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   bool first = true;
   while (at < end) {
     while (prefix[b + 1] <= at) ++b;
-    const Visible vis = visible(a, b);
+    const Visible vis = visible<SHARED>(a, b);
     const int g = (int)quotient(at - prefix[b], vis.n);
     // the unit in the list, and the slabs of it that are this share's
     const int64_t u0 = prefix[b] + (int64_t)g * vis.n, u1 = u0 + vis.n;
@@ -338,8 +344,10 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     uint32_t row[NS], seen[NS], seen_now[NS];
     float ks[NS], vs[NS], ks_now[NS], vs_now[NS];
     int32_t page[NS] = {};
-    const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
-    const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
+    const int cb = SHARED ? a.from[b] : b;  // whose cache
+    const int32_t* pages =
+        a.c.page_table ? a.c.page_table + (int64_t)cb * a.c.max_pages : nullptr;
+    const uint32_t unit_row = (uint32_t)(((int64_t)cb * Hkv + g) * a.c.l_cap);
     const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
     const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
 
@@ -693,9 +701,12 @@ int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st) {
   const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
   const dim3 g(grid), th(kDecodeThreads);
-  const auto kernel = fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8>
-                      : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3>
-                                        : attn_decode_kernel<kFmtBf16>;
+  const auto kernel = a.start ? (fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8, true>
+                                 : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3, true>
+                                                   : attn_decode_kernel<kFmtBf16, true>)
+                              : (fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8, false>
+                                 : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3, false>
+                                                   : attn_decode_kernel<kFmtBf16, false>);
   if (smem > 24 * 1024) {  // with the static arrays: past the default limit
     const cudaError_t e = cudaFuncSetAttribute(
         (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
