@@ -8,6 +8,7 @@
 
 #include "api_util.h"
 #include "cache_ops.h"
+#include "shared_attn.h"
 
 using namespace tsa;
 
@@ -327,18 +328,22 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
 // Workspace of a step with shared rows.  Nothing but the status word outlasts a call, so
 // that calls of whatever sizes may share it.
 struct SharedLayout {
-  size_t partial, arrived, rows, own, sh, total;
+  size_t partial, arrived, rows, groups, own, sh, parts, total;
 };
 SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   SharedLayout l{};
-  (void)N;
   const size_t row = round_up((size_t)B * Hq * (kD + 1) * sizeof(float));
+  // at most: every share's first segment, and the units' (two halves, rounded up to 8)
+  const int64_t units = 2 * ((int64_t)B * Hq + (int64_t)8 * Hkv * (N < B ? N : B));
   l.partial = kDecodePartial;
   l.arrived = kDecodeArrived;
   l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));
-  l.own = l.rows + 5 * round_up((size_t)B * sizeof(int32_t));
+  l.groups = l.rows + 4 * round_up((size_t)B * sizeof(int32_t));
+  l.own = l.groups + kAlign + round_up((size_t)N * sizeof(SharedGroup));
   l.sh = l.own + row;
-  l.total = l.sh + row;
+  l.parts = l.sh + row;
+  l.total = l.parts +
+            round_up((size_t)(kSharedShares * kShareRows + units) * (kD + 2) * sizeof(float));
   return l;
 }
 
@@ -360,8 +365,8 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   if ((rc = check_workspace(workspace, ws_bytes, l.total))) return rc;
   const int64_t pool = c.page_table ? (fmt == kFmtBf16 ? 0 : (int64_t)c.n_pages << c.page_shift)
                                     : (int64_t)B * c.l_cap;
-  if (pool > (int64_t)0xffffffff / Hkv)
-    return fail(TSA_ERR_INVALID_ARG, "the cache has 2^32 rows or more");
+  if (pool > (int64_t)0x7fffffff / Hkv)
+    return fail(TSA_ERR_INVALID_ARG, "the cache has 2^31 rows or more");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SharedArgs s{};
   s.q = static_cast<const uint16_t*>(q);
@@ -372,7 +377,10 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   s.B = B;
   s.N = N;
   s.Hq = Hq;
+  s.G = Hq / Hkv;
+  s.inv_g = (65536 + s.G - 1) / s.G;
   s.scale_log2 = (float)((double)scale * kLog2e);
+  s.box = c.page_table && (1 << c.page_shift) < 128 ? 1 << c.page_shift : 128;
   s.out = out;
   s.out16 = out16;
   s.lse = lse_out;
@@ -380,14 +388,18 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   const size_t ints = round_up((size_t)B * sizeof(int32_t)), rows = (size_t)B * Hq;
   s.group = reinterpret_cast<int32_t*>(ws + l.rows);
   s.start = reinterpret_cast<int32_t*>(ws + l.rows + ints);
-  s.leader = reinterpret_cast<int32_t*>(ws + l.rows + 2 * ints);
-  s.zero = reinterpret_cast<int32_t*>(ws + l.rows + 3 * ints);
-  s.self = reinterpret_cast<int32_t*>(ws + l.rows + 4 * ints);
+  s.total = reinterpret_cast<SharedTotal*>(ws + l.groups);
+  s.groups = reinterpret_cast<SharedGroup*>(ws + l.groups + kAlign);
   s.own_out = reinterpret_cast<float*>(ws + l.own);
   s.own_lse = s.own_out + rows * kD;
-  s.sh_out = reinterpret_cast<float*>(ws + l.sh);
-  s.sh_lse = s.sh_out + rows * kD;
+  s.parts = reinterpret_cast<float*>(ws + l.parts);
   s.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
+  if (fmt != kFmtBf16) {
+    s.leader = reinterpret_cast<int32_t*>(ws + l.rows + 2 * ints);
+    s.zero = reinterpret_cast<int32_t*>(ws + l.rows + 3 * ints);
+    s.sh_out = reinterpret_cast<float*>(ws + l.sh);
+    s.sh_lse = s.sh_out + rows * kD;
+  }
   DecodeArgs a{};
   a.q = s.q;
   a.c = c;
@@ -399,16 +411,25 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   a.arrived = s.arrived;
   const int grid = decode_grid((int64_t)B * Hkv, c.l_cap, fmt);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap kmap, vmap;
+  if (fmt == kFmtBf16 && N > 0) {
+    const int64_t all = c.page_table ? 0x7fffffff : (int64_t)B * Hkv * c.l_cap;
+    if ((rc = row_map(c.k, all, s.box, &kmap)) || (rc = row_map(c.v, all, s.box, &vmap))) return rc;
+  }
   if ((rc = launched(launch_shared_prep(s, st), "groups launch"))) return rc;
-  a.lens = s.start;  // rows [0, start) of the leader's cache
-  a.start = s.zero;
-  a.from = s.leader;
-  a.out = s.sh_out;
-  a.lse = s.sh_lse;
-  if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;
+  if (fmt != kFmtBf16) {
+    a.lens = s.start;  // rows [0, start) of the leader's cache
+    a.start = s.zero;
+    a.from = s.leader;
+    a.out = s.sh_out;
+    a.lse = s.sh_lse;
+    if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;
+  } else if (N > 0) {
+    if ((rc = launched(launch_shared_prefix(kmap, vmap, s, st), "attention launch"))) return rc;
+  }
   a.lens = lens;
   a.start = s.start;
-  a.from = s.self;
+  a.from = nullptr;
   a.out = s.own_out;
   a.lse = s.own_lse;
   if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;

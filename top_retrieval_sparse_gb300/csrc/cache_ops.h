@@ -144,41 +144,12 @@ struct DecodeArgs {
   float* partial;          // [2 * kDecodeShares][kDecodeSlot]
   uint32_t* arrived;       // [B * Hkv], zero between calls
   // Of a batch that shares rows (else nullptr): sequence b sees rows [start[b], lens[b]) of
-  // the cache of sequence from[b].
+  // its cache, or of sequence from[b]'s.
   const int32_t* start;
   const int32_t* from;
 };
 int attn_decode_ctas(int fmt);  // resident CTAs of an SM
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st);
-
-// Decode of groups that share rows (shared_attn.cu).
-struct SharedArgs {
-  const uint16_t* q;       // bf16 [B][Hq][128]
-  CacheView c;
-  const int32_t* lens;
-  const int32_t* cu;       // [N + 1] sequences before every group
-  const int32_t* shared;   // [N]
-  int B, N, Hq;
-  float scale_log2;
-  void* out;               // [B][Hq][128], fp32 or bf16
-  int out16;
-  float* lse;              // [B][Hq] or nullptr
-  int* status;
-  // in the workspace
-  int32_t* group;          // [B]: a sequence's group, -1: none, kNoGroups: bad offsets
-  int32_t* start;          // [B]: its rows before this one are the group's
-  int32_t* leader;         // [B]: the sequence whose cache has them
-  int32_t* zero;           // [B] zeros
-  int32_t* self;           // [B] 0, 1, ...
-  float* own_out;          // [B][Hq][128]: over its own rows
-  float* own_lse;          // [B][Hq]
-  float* sh_out;
-  float* sh_lse;
-  uint32_t* arrived;       // counters of the decode kernel
-};
-constexpr int kNoGroups = -2;
-cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st);
-cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
 
 // Many tokens per sequence (window_prefill.cu); the maps are the bf16 pool's
 // rows of 128 elements, in boxes of 64 elements by `box` rows.

@@ -1,0 +1,169 @@
+// shared_attn.h -- the step over shared rows: argument block, the list of its work and where
+// its partials lie (host <-> device contract inside the library; not part of the C ABI).
+#pragma once
+
+#include "cache_ops.h"
+
+namespace tsa {
+
+constexpr int kUnitRows = 256;      // query rows of a unit: two tiles of the tensor core
+constexpr int kSharedShares = 152;  // CTAs of the prefix kernel: one an SM
+// Cost of a key tile with two query tiles and with one (the products bound the former, the
+// rows' bytes the latter).
+constexpr int kCostBoth = 4, kCostAlone = 3;
+constexpr int kNoGroups = -2;
+
+// A group, as the first kernel finds it.
+struct SharedGroup {
+  int64_t cost0;  // of the groups before it
+  int64_t row0;   // first row of its partials
+  int32_t b0;     // first sequence
+  int32_t rows;   // queries of a KV head: sequences * G
+  int32_t P;      // shared rows
+  int32_t pad;
+};
+struct SharedTotal {
+  int64_t cost;
+  int32_t shares;  // of the list that take part
+};
+
+struct SharedArgs {
+  const uint16_t* q;       // bf16 [B][Hq][128]
+  CacheView c;
+  const int32_t* lens;
+  const int32_t* cu;       // [N + 1] sequences before every group
+  const int32_t* shared;   // [N]
+  int B, N, Hq, G;
+  int inv_g;               // ceil(2^16 / G): r / G = r * inv_g >> 16 for small r
+  float scale_log2;
+  int box;                 // rows of a copy: 128, or a smaller page
+  void* out;               // [B][Hq][128], fp32 or bf16
+  int out16;
+  float* lse;              // [B][Hq] or nullptr
+  int* status;
+  // in the workspace
+  int32_t* group;          // [B]: a sequence's group, -1: none, kNoGroups: bad offsets
+  int32_t* start;          // [B]: its rows before this one are the group's
+  SharedGroup* groups;     // [N]
+  SharedTotal* total;
+  float* own_out;          // [B][Hq][128]: over its own rows
+  float* own_lse;          // [B][Hq]
+  uint32_t* arrived;       // counters of the decode kernel
+  float* parts;            // partials: of each share's first segment, then of the units
+  int32_t* leader;         // 8-bit caches: the sequence whose cache has the shared rows
+  int32_t* zero;
+  float* sh_out;
+  float* sh_lse;
+};
+cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st);
+cudaError_t launch_shared_prefix(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 const SharedArgs& a, cudaStream_t st);
+cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
+
+// Rows of partials (of kD + 2 floats) that a group of `rows` queries can need, and a share.
+constexpr int64_t kShareRows = kUnitRows;
+__host__ __device__ inline int tile_rows(int rows) {  // of a unit's half
+  return rows > 128 ? 128 : (rows + 7) / 8 * 8;
+}
+__host__ __device__ inline int64_t group_rows(int rows, int Hkv) {
+  if (rows == 0) return 0;
+  const int full = (rows - 1) / kUnitRows;
+  return (int64_t)Hkv * (full * kUnitRows + 2 * tile_rows(rows - full * kUnitRows));
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int64_t share_start(const SharedTotal& t, int share) {
+  return (t.cost * share + t.shares - 1) / t.shares;
+}
+
+// A unit: queries [256 t, ...) of KV head g of a group.
+struct SharedUnit {
+  int t, g, rows, tiles, w;  // w: cost of a key tile
+  int rs;                    // rows of a half of its partials
+  int64_t cost0, row0;
+  __device__ bool both() const { return w == kCostBoth; }
+};
+__device__ __forceinline__ SharedUnit unit_of(const SharedGroup& s, int Hkv, int t, int g) {
+  SharedUnit u;
+  u.t = t;
+  u.g = g;
+  u.rows = s.rows - t * kUnitRows < kUnitRows ? s.rows - t * kUnitRows : kUnitRows;
+  u.tiles = (s.P + 127) / 128;
+  u.w = u.rows > 128 ? kCostBoth : kCostAlone;
+  u.rs = tile_rows(u.rows);
+  u.cost0 = s.cost0 + (int64_t)u.tiles * ((int64_t)t * Hkv * kCostBoth + g * u.w);
+  u.row0 = s.row0 + (int64_t)t * Hkv * kUnitRows + (int64_t)g * 2 * u.rs;
+  return u;
+}
+// Floats from a half of a segment's partials to the next: O as [32][rs] pieces of four
+// columns, then maxima and sums.
+__device__ __forceinline__ int64_t half_floats(int rs) { return (int64_t)rs * (kD + 2); }
+__device__ __forceinline__ float* segment_parts(const SharedArgs& a, const SharedUnit& u, int share,
+                                                int j0) {
+  const int64_t row = j0 > 0 ? share * kShareRows : kSharedShares * kShareRows + u.row0;
+  return a.parts + row * (kD + 2);
+}
+
+// A share's segments, in order.
+struct SharedWalk {
+  const SharedArgs& a;
+  int64_t at, end;     // costs
+  int n;               // group
+  SharedGroup s;
+  SharedUnit u;
+  int j0, j1;          // key tiles of the segment
+  __device__ SharedWalk(const SharedArgs& args, int share) : a(args) {
+    const SharedTotal t = *a.total;
+    at = end = 0;
+    n = -1;
+    if (share >= t.shares) return;
+    at = share_start(t, share);
+    end = share_start(t, share + 1);
+    if (at >= end) return;
+    int lo = 0;
+    for (int hi = a.N; hi - lo > 1;) {  // the last group that starts at or before `at`
+      const int mid = (lo + hi) >> 1;
+      if (a.groups[mid].cost0 <= at) lo = mid; else hi = mid;
+    }
+    n = lo;
+    s = a.groups[n];
+  }
+  // The next segment; false: none.
+  __device__ bool next() {
+    if (at >= end) return false;
+    const int Hkv = a.c.Hkv;
+    for (;;) {
+      const int64_t tiles = (s.P + 127) / 128, off = at - s.cost0;
+      const int last = (s.rows - 1) / kUnitRows;
+      const int64_t column = tiles * Hkv * kCostBoth;  // all but the last are full
+      if (s.rows > 0 && tiles > 0) {
+        int64_t t = off / column;
+        if (t > last) t = last;
+        const int64_t in = off - t * column;
+        const int w = s.rows - (int)t * kUnitRows > 128 ? kCostBoth : kCostAlone;
+        const int64_t g = in / (tiles * w);
+        if (g < Hkv) {
+          u = unit_of(s, Hkv, (int)t, (int)g);
+          j0 = (int)((at - u.cost0 + w - 1) / w);
+          if (j0 < u.tiles) {
+            const int64_t n1 = (end - u.cost0 + w - 1) / w;
+            j1 = n1 < u.tiles ? (int)n1 : u.tiles;
+            at = u.cost0 + (int64_t)u.tiles * w;
+            return j1 > j0 ? true : (at = end, false);
+          }
+          at = u.cost0 + (int64_t)u.tiles * w;  // (begins behind the last tile's start)
+          if (at >= end) return false;
+          continue;
+        }
+      }
+      if (++n >= a.N) {
+        at = end;
+        return false;
+      }
+      s = a.groups[n];
+    }
+  }
+};
+#endif
+
+}  // namespace tsa
