@@ -12,7 +12,7 @@ namespace tsa {
 
 namespace {
 
-constexpr int kPrepThreads = 1024;
+constexpr int kPrepThreads = 256;
 constexpr int kMostGroups = 4096;
 
 // Exclusive prefix over the block's threads, and the whole sum.
@@ -46,8 +46,9 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
   const int tid = threadIdx.x;
   const int B = a.B, N = a.N, Hkv = a.c.Hkv;
   if (blockIdx.x > 0) {
-    const int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + tid;
-    if (i < (int64_t)B * Hkv) a.arrived[i] = 0u;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + tid; i < (int64_t)B * Hkv;
+         i += (int64_t)(gridDim.x - 1) * kPrepThreads)
+      a.arrived[i] = 0u;
     return;
   }
   for (int n = tid; n <= N; n += kPrepThreads) cu_s[n] = a.cu[n];
@@ -126,94 +127,149 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
   }
 }
 
-// Four columns of a row (sequence, query head) a thread: the partials of the segments of its
-// unit in the order of the list, then the own rows'.
-__global__ void __launch_bounds__(256) shared_join_kernel(SharedArgs a) {
+constexpr int kJoinThreads = 256;
+constexpr int kMostParts = 2 * kSharedShares;
+
+// A (sequence, KV head) a CTA.  First a warp a query head: the maxima and sums of the row's
+// partials, lanes over them, and each one's weight.  Then four columns of a row a thread
+// (neighbouring threads the query heads of one KV head, whose partials are neighbours), the
+// loads of eight partials in flight; with few query heads several threads share the partials.
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a) {
+  __shared__ float weight_s[kMaxGroup][kMostParts];
+  __shared__ int place_s[kMaxGroup][kMostParts];   // of the partial's columns, in pieces of 16 bytes
+  __shared__ int count_s[kMaxGroup], rs_s[kMaxGroup];
+  __shared__ float own_s[kMaxGroup], inv_s[kMaxGroup];
+  __shared__ float4 sum_s[kJoinThreads];
   pdl_wait();
   if (!a.out16) pdl_trigger();  // (bf16 outputs may be queries of a key scan)
-  const int b = blockIdx.x, Hkv = a.c.Hkv, G = a.G;
-  const int item = blockIdx.y * 256 + threadIdx.x;
-  if (item >= a.Hq * 32) return;
-  // neighbouring threads: a KV head's query heads, whose partials are neighbours
-  const int h = item % G, c = item / G % 32, g = item / (32 * G);
-  const int64_t row = (int64_t)b * a.Hq + g * G + h;
+  const int b = blockIdx.x, g = blockIdx.y, Hkv = a.c.Hkv, G = a.G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = a.group[b], L = a.lens[b];
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool nan = n == kNoGroups;
-  auto add = [&](float pm, float pl, const float4* from) {
-    if (pl == 0.f) return;  // (has seen nothing and left no sums)
-    const float top = fmaxf(m, pm), f = m == -INFINITY ? 0.f : exp2f(m - top), e = exp2f(pm - top);
-    const float4 x = *from;
-    o = make_float4(fmaf(o.x, f, x.x * e), fmaf(o.y, f, x.y * e), fmaf(o.z, f, x.z * e),
-                    fmaf(o.w, f, x.w * e));
-    l = fmaf(l, f, pl * e);
-    m = top;
-  };
-  if (n >= 0 && L > 0) {
-    const int P = a.shared[n];
-    nan |= L < P;
-    if (L >= P && P > 0 && a.leader) {
-      const float lse = a.sh_lse[row];
-      add(lse * 1.4426950408889634f, lse == -INFINITY ? 0.f : (lse != lse ? lse : 1.f),
-          reinterpret_cast<const float4*>(a.sh_out + row * kD) + c);
-    } else if (L >= P && P > 0) {
-      const SharedGroup s = a.groups[n];
-      const SharedTotal t = *a.total;
-      const int r0 = (b - s.b0) * G + h, column = r0 / kUnitRows, r = r0 - column * kUnitRows;
-      const SharedUnit u = unit_of(s, Hkv, column, g);
-      const bool both = u.both();
-      const int64_t half = half_floats(u.rs);
-      const int s0 = (int)(u.cost0 * t.shares / t.cost);
-      for (int share = s0, j0 = 0; j0 < u.tiles; ++share) {
-        const float* p = segment_parts(a, u, share, j0);
-        if (both) {
-          p += (r >> 7) * half;
-          const float* stats = p + (int64_t)u.rs * kD + (r & 127);
-          add(stats[0], stats[u.rs],
-              reinterpret_cast<const float4*>(p) + (int64_t)c * u.rs + (r & 127));
-        } else {
-#pragma unroll
-          for (int x = 0; x < 2; ++x, p += half) {
-            const float* stats = p + (int64_t)u.rs * kD + r;
-            add(stats[0], stats[u.rs], reinterpret_cast<const float4*>(p) + (int64_t)c * u.rs + r);
+  const int64_t row0 = (int64_t)b * a.Hq + g * G;
+  if (warp < G) {
+    const int h = warp;
+    const float own_lse = a.own_lse[row0 + h];
+    float m = -INFINITY, l = 0.f;
+    int parts = 0, rs = 0;
+    bool nan = n == kNoGroups;
+    const int P = n >= 0 ? a.shared[n] : 0;
+    if (P > 0 && L > 0) {
+      nan |= L < P;
+      if (!nan && a.leader) {
+        parts = 1;
+        rs = 1;
+        if (lane == 0) {
+          const float lse = a.sh_lse[row0 + h];
+          m = lse * 1.4426950408889634f;
+          l = lse == -INFINITY ? 0.f : (lse != lse ? lse : 1.f);
+          place_s[h][0] = (int)((row0 + h) * (kD / 4));
+          weight_s[h][0] = m;
+        }
+      } else if (!nan) {
+        const SharedGroup s = a.groups[n];
+        const SharedTotal t = *a.total;
+        const int r0 = (b - s.b0) * G + h, column = r0 / kUnitRows, r = r0 - column * kUnitRows;
+        const SharedUnit u = unit_of(s, Hkv, column, g);
+        const bool both = u.both();
+        const int at = both ? r & 127 : r;
+        const int half = (int)(half_floats(u.rs) / 4);
+        const int s0 = (int)(u.cost0 * t.shares / t.cost);
+        const int s1 = (int)((u.cost0 + (int64_t)(u.tiles - 1) * u.w) * t.shares / t.cost);
+        parts = (s1 - s0 + 1) * (both ? 1 : 2);
+        rs = u.rs;
+        float l_all = 0.f;
+        for (int e = lane; e < parts; e += 32) {
+          const int share = s0 + (both ? e : e >> 1);
+          const int place = (int)((segment_parts(a, u, share, share > s0) - a.parts) / 4) +
+                            (both ? r >> 7 : e & 1) * half;
+          const float* stats = a.parts + (int64_t)place * 4 + u.rs * kD + at;
+          const float pm = stats[0], pl = stats[u.rs];
+          place_s[h][e] = place + at;
+          // (one that has seen nothing has left no sums)
+          weight_s[h][e] = pl == 0.f ? -INFINITY : pm;
+          const float top = fmaxf(m, pl == 0.f ? -INFINITY : pm);
+          if (pl != 0.f) {
+            l_all = (m == -INFINITY ? 0.f : l_all * exp2f(m - top)) + pl * exp2f(pm - top);
+            m = top;
           }
         }
-        const int64_t next = share_start(t, share + 1) - u.cost0;
-        j0 = (int)((next + u.w - 1) / u.w);
+        l = l_all;
       }
     }
+    // of all lanes, and of the own rows
+    float top = warp_max(m);
+    const float own_m = own_lse == -INFINITY ? -INFINITY : own_lse * 1.4426950408889634f;
+    if (own_lse == own_lse) top = fmaxf(top, own_m);
+    float all = warp_sum(m == -INFINITY ? 0.f : l * exp2f(m - top));
+    const float own = own_lse == -INFINITY ? 0.f : exp2f(own_m - top);  // (NaN stays)
+    all += own;
+    nan |= all != all;
+    __syncwarp();
+    for (int e = lane; e < parts; e += 32)
+      weight_s[h][e] = weight_s[h][e] == -INFINITY ? 0.f : exp2f(weight_s[h][e] - top);
+    if (lane == 0) {
+      count_s[h] = nan ? 0 : parts;
+      rs_s[h] = rs;
+      own_s[h] = own;
+      inv_s[h] = nan ? nanf("") : (all > 0.f ? 1.f / all : 0.f);
+      if (a.lse)
+        a.lse[row0 + h] = nan ? nanf("")
+                              : (all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY);
+    }
   }
-  {
-    const float lse = a.own_lse[row];
-    add(lse * 1.4426950408889634f, lse == -INFINITY ? 0.f : (lse != lse ? lse : 1.f),
-        reinterpret_cast<const float4*>(a.own_out + row * kD) + c);
+  __syncthreads();
+  const int per = 32 * G, ways = kJoinThreads / per;  // threads of all columns, and of each
+  const int h = threadIdx.x % G, c = threadIdx.x / G & 31, way = threadIdx.x / per;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (way < ways) {
+    const float4* parts = reinterpret_cast<const float4*>(a.leader ? a.sh_out : a.parts);
+    const int count = count_s[h], rs = rs_s[h];
+#pragma unroll 8
+    for (int e = way; e < count; e += ways) {
+      const float w = weight_s[h][e];
+      if (w > 0.f) {
+        const float4 x = __ldcg(parts + place_s[h][e] + (int64_t)c * rs);
+        o.x = fmaf(x.x, w, o.x); o.y = fmaf(x.y, w, o.y);
+        o.z = fmaf(x.z, w, o.z); o.w = fmaf(x.w, w, o.w);
+      }
+    }
+    if (way == 0 && own_s[h] > 0.f) {
+      const float w = own_s[h];
+      const float4 x = reinterpret_cast<const float4*>(a.own_out + (row0 + h) * kD)[c];
+      o.x = fmaf(x.x, w, o.x); o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z); o.w = fmaf(x.w, w, o.w);
+    }
   }
-  nan |= l != l;
-  const float inv = nan ? nanf("") : (l > 0.f ? 1.f / l : 0.f);
-  if (nan) o = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (ways > 1) {
+    sum_s[threadIdx.x] = o;
+    __syncthreads();
+    for (int i = 1; i < ways && way == 0; ++i) {
+      const float4 x = sum_s[threadIdx.x + i * per];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+  }
+  if (way > 0) return;
+  const float inv = inv_s[h];
+  if (inv != inv) o = make_float4(1.f, 1.f, 1.f, 1.f);
   o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
   if (a.out16) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kD)[c] =
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (row0 + h) * kD)[c] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   } else {
-    reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kD)[c] = o;
+    reinterpret_cast<float4*>(static_cast<float*>(a.out) + (row0 + h) * kD)[c] = o;
   }
-  if (a.lse && c == 0)
-    a.lse[row] = nan ? inv : (l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY);
 }
 
 }  // namespace
 
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st) {
-  const int64_t counters = (int64_t)a.B * a.c.Hkv;
-  const dim3 grid((unsigned)(1 + (counters + kPrepThreads - 1) / kPrepThreads));
+  const int64_t counters = ((int64_t)a.B * a.c.Hkv + kPrepThreads - 1) / kPrepThreads;
+  const dim3 grid((unsigned)(1 + (counters < 64 ? counters : 64)));
   return launch_dependent(shared_prep_kernel, grid, dim3(kPrepThreads), 0, st, a);
 }
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st) {
-  const dim3 grid(a.B, (a.Hq * 32 + 255) / 256);
-  return launch_dependent(shared_join_kernel, grid, dim3(256), 0, st, a);
+  return launch_dependent(shared_join_kernel, dim3(a.B, a.c.Hkv), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace tsa
