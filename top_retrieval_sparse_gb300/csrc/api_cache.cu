@@ -200,8 +200,9 @@ int check_window(int64_t n_init, int64_t n_recent, float scale) {
 }
 
 // The tensor map of a bf16 pool's rows: boxes of 64 elements by `box` rows with
-// the 128-byte swizzle (encoded on the host; nothing is launched).
-int row_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
+// the 128-byte swizzle; of a pool of codes: boxes of whole rows as they are (encoded on
+// the host; nothing is launched).
+int row_map(const void* base, int64_t rows, int box, CUtensorMap* map, bool codes = false) {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static std::atomic<void*> fn{nullptr};
   void* f = fn.load(std::memory_order_acquire);
@@ -214,11 +215,12 @@ int row_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
     fn.store(f, std::memory_order_release);
   }
   const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {kRowBytes};
-  const cuuint32_t extent[2] = {64, (cuuint32_t)box}, step[2] = {1, 1};
+  const cuuint64_t strides[1] = {(cuuint64_t)(codes ? kD : kRowBytes)};
+  const cuuint32_t extent[2] = {(cuuint32_t)(codes ? kD : 64), (cuuint32_t)box}, step[2] = {1, 1};
   const CUresult r = reinterpret_cast<Encode>(f)(
-      map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, extent,
-      step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+      const_cast<void*>(base), dims, strides, extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TSA_ERR_CUDA, "tensor map: driver error %d", (int)r);
   return TSA_OK;
@@ -328,7 +330,7 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
 // Workspace of a step with shared rows.  Nothing but the status word outlasts a call, so
 // that calls of whatever sizes may share it.
 struct SharedLayout {
-  size_t partial, arrived, rows, groups, own, sh, parts, total;
+  size_t partial, arrived, rows, groups, own, parts, total;
 };
 SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   SharedLayout l{};
@@ -338,10 +340,9 @@ SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   l.partial = kDecodePartial;
   l.arrived = kDecodeArrived;
   l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));
-  l.groups = l.rows + 4 * round_up((size_t)B * sizeof(int32_t));
+  l.groups = l.rows + 2 * round_up((size_t)B * sizeof(int32_t));
   l.own = l.groups + kAlign + round_up((size_t)N * sizeof(SharedGroup));
-  l.sh = l.own + row;
-  l.parts = l.sh + row;
+  l.parts = l.own + row;
   l.total = l.parts +
             round_up((size_t)(kSharedShares * kShareRows + units) * (kD + 2) * sizeof(float));
   return l;
@@ -394,12 +395,6 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   s.own_lse = s.own_out + rows * kD;
   s.parts = reinterpret_cast<float*>(ws + l.parts);
   s.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
-  if (fmt != kFmtBf16) {
-    s.leader = reinterpret_cast<int32_t*>(ws + l.rows + 2 * ints);
-    s.zero = reinterpret_cast<int32_t*>(ws + l.rows + 3 * ints);
-    s.sh_out = reinterpret_cast<float*>(ws + l.sh);
-    s.sh_lse = s.sh_out + rows * kD;
-  }
   DecodeArgs a{};
   a.q = s.q;
   a.c = c;
@@ -412,24 +407,19 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   const int grid = decode_grid((int64_t)B * Hkv, c.l_cap, fmt);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap kmap, vmap;
-  if (fmt == kFmtBf16 && N > 0) {
-    const int64_t all = c.page_table ? 0x7fffffff : (int64_t)B * Hkv * c.l_cap;
-    if ((rc = row_map(c.k, all, s.box, &kmap)) || (rc = row_map(c.v, all, s.box, &vmap))) return rc;
+  const bool codes = fmt != kFmtBf16;
+  if (N > 0) {
+    const int64_t all = c.page_table ? (codes ? pool * Hkv : 0x7fffffff) : (int64_t)B * Hkv * c.l_cap;
+    if ((rc = row_map(c.k, all, s.box, &kmap, codes)) ||
+        (rc = row_map(c.v, all, s.box, &vmap, codes)))
+      return rc;
   }
   if ((rc = launched(launch_shared_prep(s, st), "groups launch"))) return rc;
-  if (fmt != kFmtBf16) {
-    a.lens = s.start;  // rows [0, start) of the leader's cache
-    a.start = s.zero;
-    a.from = s.leader;
-    a.out = s.sh_out;
-    a.lse = s.sh_lse;
-    if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;
-  } else if (N > 0) {
-    if ((rc = launched(launch_shared_prefix(kmap, vmap, s, st), "attention launch"))) return rc;
-  }
+  if (N > 0 &&
+      (rc = launched(launch_shared_prefix(kmap, vmap, s, fmt, st), "attention launch")))
+    return rc;
   a.lens = lens;
   a.start = s.start;
-  a.from = nullptr;
   a.out = s.own_out;
   a.lse = s.own_lse;
   if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;

@@ -344,10 +344,8 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     uint32_t row[NS], seen[NS], seen_now[NS];
     float ks[NS], vs[NS], ks_now[NS], vs_now[NS];
     int32_t page[NS] = {};
-    const int cb = SHARED && a.from ? a.from[b] : b;  // whose cache
-    const int32_t* pages =
-        a.c.page_table ? a.c.page_table + (int64_t)cb * a.c.max_pages : nullptr;
-    const uint32_t unit_row = (uint32_t)(((int64_t)cb * Hkv + g) * a.c.l_cap);
+    const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
+    const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
     const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
     const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
 

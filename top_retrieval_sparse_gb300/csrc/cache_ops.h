@@ -143,10 +143,8 @@ struct DecodeArgs {
   int* status;
   float* partial;          // [2 * kDecodeShares][kDecodeSlot]
   uint32_t* arrived;       // [B * Hkv], zero between calls
-  // Of a batch that shares rows (else nullptr): sequence b sees rows [start[b], lens[b]) of
-  // its cache, or of sequence from[b]'s.
+  // Of a batch that shares rows (else nullptr): sequence b sees rows [start[b], lens[b]).
   const int32_t* start;
-  const int32_t* from;
 };
 int attn_decode_ctas(int fmt);  // resident CTAs of an SM
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st);

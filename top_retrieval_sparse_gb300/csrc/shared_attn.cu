@@ -120,10 +120,6 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
     }
     a.group[b] = n;
     a.start[b] = start;
-    if (a.leader) {
-      a.leader[b] = n >= 0 ? cu_s[n] : b;
-      a.zero[b] = 0;
-    }
   }
 }
 
@@ -155,17 +151,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a)
     const int P = n >= 0 ? a.shared[n] : 0;
     if (P > 0 && L > 0) {
       nan |= L < P;
-      if (!nan && a.leader) {
-        parts = 1;
-        rs = 1;
-        if (lane == 0) {
-          const float lse = a.sh_lse[row0 + h];
-          m = lse * 1.4426950408889634f;
-          l = lse == -INFINITY ? 0.f : (lse != lse ? lse : 1.f);
-          place_s[h][0] = (int)((row0 + h) * (kD / 4));
-          weight_s[h][0] = m;
-        }
-      } else if (!nan) {
+if (!nan) {
         const SharedGroup s = a.groups[n];
         const SharedTotal t = *a.total;
         const int r0 = (b - s.b0) * G + h, column = r0 / kUnitRows, r = r0 - column * kUnitRows;
@@ -212,9 +198,16 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a)
       rs_s[h] = rs;
       own_s[h] = own;
       inv_s[h] = nan ? nanf("") : (all > 0.f ? 1.f / all : 0.f);
-      if (a.lse)
+      if (a.lse) {
+        // (8-bit: the sum may carry an inverse scale of up to 2^60, so the exponents are
+        // added first)
+        const uint32_t u = __float_as_uint(all);
+        const float e = (float)((int)(u >> 23) - 127);
+        const float f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
         a.lse[row0 + h] = nan ? nanf("")
-                              : (all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY);
+                              : (all > 0.f ? ((top + e) + log2f(f)) * 0.6931471805599453f
+                                           : -INFINITY);
+      }
     }
   }
   __syncthreads();
@@ -222,7 +215,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a)
   const int h = threadIdx.x % G, c = threadIdx.x / G & 31, way = threadIdx.x / per;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (way < ways) {
-    const float4* parts = reinterpret_cast<const float4*>(a.leader ? a.sh_out : a.parts);
+    const float4* parts = reinterpret_cast<const float4*>(a.parts);
     const int count = count_s[h], rs = rs_s[h];
 #pragma unroll 8
     for (int e = way; e < count; e += ways) {

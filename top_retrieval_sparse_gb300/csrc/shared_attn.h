@@ -50,14 +50,10 @@ struct SharedArgs {
   float* own_lse;          // [B][Hq]
   uint32_t* arrived;       // counters of the decode kernel
   float* parts;            // partials: of each share's first segment, then of the units
-  int32_t* leader;         // 8-bit caches: the sequence whose cache has the shared rows
-  int32_t* zero;
-  float* sh_out;
-  float* sh_lse;
 };
 cudaError_t launch_shared_prep(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_shared_prefix(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                 const SharedArgs& a, cudaStream_t st);
+                                 const SharedArgs& a, int fmt, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
 
 // Rows of partials (of kD + 2 floats) that a group of `rows` queries can need, and a share.

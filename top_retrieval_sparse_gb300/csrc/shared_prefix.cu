@@ -25,6 +25,8 @@
 // when its three readers have given it back: both matrix threads, or one and the zeroing
 // warp for the other, and the zeroing warp.  It passes every slot in order, so nobody falls
 // behind by two laps and a barrier's parity is never taken for another lap's.
+#include <cuda_fp16.h>
+
 #include "shared_attn.h"
 #include "tcgen.cuh"
 
@@ -32,10 +34,24 @@ namespace tsa {
 
 namespace {
 
-constexpr int kSlots = 5;
-constexpr int kSharedThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 2 * 216 + 72 = 3 * 168 a scheduler
-constexpr int kSharedSmem = (2 + kSlots) * kSlotBytes + 1024;
+// Slots of the ring of operands, and, for 8-bit caches, of the ring of codes before it.
+template <int FMT>
+constexpr int kSlots = FMT == kFmtBf16 ? 5 : 3;
+constexpr int kRawSlots = 4, kRawBytes = kTile * kD;
+template <int FMT>
+constexpr int kSharedThreads = FMT == kFmtBf16 ? 384 : 512;
+// Registers a scheduler: 2 * 216 + 72 = 3 * 168, or 2 * 200 + 2 * 56 = 4 * 128.
+template <int FMT>
+constexpr int kSoftmaxRegs = FMT == kFmtBf16 ? 216 : 200;
+template <int FMT>
+constexpr int kOtherRegs = FMT == kFmtBf16 ? 72 : 56;
+template <int FMT>
+constexpr int kSharedSmem = (2 + kSlots<FMT>) * kSlotBytes +
+                            (FMT == kFmtBf16 ? 0 : kRawSlots * kRawBytes) + 1024;
+constexpr float kLeastScale = 1.f / (1ll << 60);  // the smallest that the cache's writer gives
+constexpr float kLeastFactor = 1e-37f;  // of a logit: keys of scale 0 (never written) are masked too
+// fp16 weights: 2^7 for the one that raised the maximum, up to 2^15 under it later.
+constexpr float kRaised = 7.f, kSlack = 15.f;
 // Weights may grow to 2^16 under an old maximum before O is rescaled: bf16 and fp32 keep
 // their precision at any size.
 constexpr float kRescale = 16.f, kMost = 65536.f;
@@ -45,21 +61,66 @@ constexpr float kRescale = 16.f, kMost = 65536.f;
 template <int PARTS>
 constexpr int kFoldEvery = PARTS == 2 ? 32 : 128;
 
+template <int FMT>
 struct SharedBars {
-  uint64_t q[2], s[2], p[2][2], o[2], full[kSlots], empty[kSlots], clean[kSlots], drain[2],
-      turn[2];
+  uint64_t q[2], s[2], p[2][2], o[2], full[kSlots<FMT>], empty[kSlots<FMT>], clean[kSlots<FMT>],
+      drain[2], turn[2], raw_full[kRawSlots], raw_empty[kRawSlots], scale[kRawSlots];
 };
 
-// Slot i of the ring's endless row, and the parity of its barriers there.
-__device__ __forceinline__ int slot_of(uint32_t i) { return i % kSlots; }
-__device__ __forceinline__ uint32_t lap_of(uint32_t i) { return i / kSlots & 1u; }
+// Slot i of the rings' endless rows, and the parity of its barriers there.
+template <int FMT>
+__device__ __forceinline__ int slot_of(uint32_t i) { return i % kSlots<FMT>; }
+template <int FMT>
+__device__ __forceinline__ uint32_t lap_of(uint32_t i) { return i / kSlots<FMT> & 1u; }
+__device__ __forceinline__ int raw_slot(uint32_t i) { return i % kRawSlots; }
+__device__ __forceinline__ uint32_t raw_lap(uint32_t i) { return i / kRawSlots & 1u; }
 
-template <int PARTS>
-__global__ void __launch_bounds__(kSharedThreads, 1)
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two weights in the products' type, and their values.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return FMT == kFmtBf16 ? bf16x2(lo, hi) : f16x2(lo, hi);
+}
+template <int FMT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (FMT == kFmtBf16) return make_float2(bf_lo(w), bf_hi(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Four codes as fp16, exactly.
+template <int FMT>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == kFmtInt8) {
+    lo = codes_lo_f16x2(w);
+    hi = codes_hi_f16x2(w);
+  } else {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+// Logarithm of a value scale: exact for powers of two.
+__device__ __forceinline__ float lg2_scale(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (float)((int)(u >> 23) - 127) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+
+template <int FMT, int PARTS>
+__global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, SharedArgs a) {
+  constexpr bool Q8 = FMT != kFmtBf16;
+  constexpr int SLOTS = kSlots<FMT>;
+  constexpr uint32_t kTypes = (1u << 7) | (1u << 10);  // operands in bf16, else fp16
+  constexpr uint32_t kQk = Q8 ? kIdesc & ~kTypes : kIdesc, kPv = Q8 ? kIdescV & ~kTypes : kIdescV;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ SharedBars bar;
+  __shared__ SharedBars<FMT> bar;
+  // 8-bit: of a tile's blocks of 16 rows: the keys' scale, the logarithm of the values' scale
+  // and its inverse.
+  __shared__ float4 scale_s[Q8 ? kRawSlots : 1][8];
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
   __shared__ volatile int bad_s[8];          // number of a segment that met a bad page
@@ -76,10 +137,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       mbar_init(&bar.drain[i], 1);
       mbar_init(&bar.turn[i], 1);
     }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bar.full[i], 1);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&bar.full[i], Q8 ? 4 : 1);
       mbar_init(&bar.empty[i], 3);
       mbar_init(&bar.clean[i], 1);
+    }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&bar.raw_full[i], 1);
+      mbar_init(&bar.raw_empty[i], 4);
+      mbar_init(&bar.scale[i], 1);
     }
     fence_mbar_init();
     abort_s = 0;
@@ -103,9 +169,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   };
   SharedWalk walk(a, blockIdx.x);
 
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<FMT>));
     const int x = (warp >> 2) - 1;           // stream A or B
     const int r = tid & 127;                 // row of the stream's tile
     const int r_warp = (warp & 3) * 32, r_half = lane >> 4, piece = lane & 15;
@@ -114,6 +180,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t o_at = s_at + 2 * kTile;
     const float sc = a.scale_log2 < 0.f ? -a.scale_log2 : (a.scale_log2 == 0.f ? 1.f : a.scale_log2);
     uint32_t tiles = 0, segs = 0;            // of this stream, so far
+    uint32_t seg_tile = 0;                   // tiles of the segments before this one
     bool ok = true;
     for (int number = 1; walk.next(); ++number) {
       const SharedUnit& u = walk.u;
@@ -127,6 +194,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       float* mine = segment_parts(a, u, blockIdx.x, walk.j0) + x * half_floats(rs);
       float4* sums = reinterpret_cast<float4*>(mine) + r;  // columns 4 i .. at sums[i * rs]
       float m = -INFINITY, l = 0.f;
+      float row_sc = sc;                     // 8-bit: with the inverse of the queries' shift
       if (n > 0 && ok) {
         // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7).
         // A half-warp a row, so that a row's 256 bytes are one request.
@@ -142,6 +210,29 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               const int sq = ((in0 + rr) * a.inv_g) >> 16, h = in0 + rr - sq * a.G;
               w[i] = *reinterpret_cast<const uint4*>(
                   a.q + ((int64_t)(walk.s.b0 + seq0 + sq) * a.Hq + u.g * a.G + h) * kD + 8 * piece);
+            }
+          }
+          if constexpr (Q8) {
+            // fp16, each row's exponents shifted so that its largest element is in
+            // [2^14, 2^15)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t* x = &w[i].x;
+              float amax = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                amax = fmaxf(amax, fmaxf(fabsf(bf_lo(x[e])), fabsf(bf_hi(x[e]))));
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1)
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+              int e2 = 141 - (int)(__float_as_uint(amax) >> 23);  // 14 - floor(log2 amax)
+              e2 = amax == 0.f ? 0 : (e2 > 126 ? 126 : (e2 < -113 ? -113 : e2));
+              const float up = __uint_as_float((uint32_t)(e2 + 127) << 23);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = f16x2(bf_lo(x[e]) * up, bf_hi(x[e]) * up);
+              // (this thread's own row is number lane: round lane / 2, half lane % 2)
+              const int of = __shfl_sync(0xffffffffu, e2, (lane & 1) * 16);
+              if (lane >> 1 == i) row_sc = sc * __uint_as_float((uint32_t)(127 - of) << 23);
             }
           }
 #pragma unroll
@@ -174,7 +265,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
         };
         auto put = [&]() {
-          const float f = !more || under == m ? 1.f : ex2((under - m) * sc);
+          const float f = !more || under == m ? 1.f : ex2(Q8 ? under - m : (under - m) * sc);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float o[32];
@@ -191,9 +282,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         for (int j0 = 0; j0 < n && ok; j0 += kFoldEvery<PARTS>) {
           const int j1 = j0 + kFoldEvery<PARTS> < n ? j0 + kFoldEvery<PARTS> : n;
           for (int j = j0; j < j1; ++j) {
-            const int k0 = (walk.j0 + (both ? j : 2 * j + x)) * kTile;
+            const int tile = both ? j : 2 * j + x, k0 = (walk.j0 + tile) * kTile;
             const uint32_t parity = (tiles + j) & 1;
             ok = wait(&bar.s[x], parity);
+            if (__builtin_expect(!ok, 0)) break;
+            if (Q8) ok = wait(&bar.scale[raw_slot(seg_tile + tile)], raw_lap(seg_tile + tile));
             if (__builtin_expect(!ok, 0)) break;
             if (!warp_live) {  // nobody reads these rows' weights
               mbar_arrive(&bar.p[x][0]);
@@ -204,7 +297,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             // (S is there, so O's products before it are done)
             if (__builtin_expect(j == j0 && j > 0, 0)) put();
             float s[128];
-            load_cols(s_at, s);
+            if constexpr (Q8) {  // (one load of 128 would need more registers than at launch)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                load_cols(s_at + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
+            } else {
+              load_cols(s_at, s);
+            }
             if (__builtin_expect(k0 + kTile > P, 0)) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -214,76 +313,121 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                   if (!(on & (1u << i))) s[32 * c + i] = -INFINITY;
               }
             }
+            // 8-bit: y = log2 of a weight with its row's value scale, block by block of 16
+            const float4* blocks = scale_s[Q8 ? (seg_tile + tile) % kRawSlots : 0];
             // Weights of half a tile (64 keys) under the maximum `top`; their sum.
             auto weights = [&](int half, float top) {
-              const float off = top == -INFINITY ? 0.f : -top * sc;
+              const float off = top == -INFINITY ? 0.f : (Q8 ? -top : -top * sc);
               float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              float sum = 0.f;
 #pragma unroll
               for (int c = 2 * half; c < 2 * half + 2; ++c) {
                 uint32_t w[16], w2[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
+                  float f = sc, o = off;
+                  if constexpr (Q8) {
+                    const float4 k = blocks[2 * c + i / 8];
+                    f = fmaxf(row_sc * k.x, kLeastFactor);
+                    o = off + k.y;
+                    if (i % 8 == 0) add[0] = add[1] = make_float2(0.f, 0.f);
+                  }
                   float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]),
-                                  make_float2(sc, sc), make_float2(off, off));
+                                  make_float2(f, f), make_float2(o, o));
                   e.x = ex2(e.x);
                   e.y = ex2(e.y);
                   add[i & 1] = add2(add[i & 1], e);
-                  w[i] = bf16x2(e.x, e.y);
+                  if constexpr (Q8) {
+                    if (i % 8 == 7)
+                      sum = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y),
+                                 blocks[2 * c + i / 8].z, sum);
+                  }
+                  w[i] = pack2<FMT>(e.x, e.y);
                   if (PARTS == 2) {
-                    const float2 h = make_float2(bf_lo(w[i]), bf_hi(w[i]));
-                    const float2 d = fma2(h, make_float2(-1.f, -1.f), e);
-                    w2[i] = bf16x2(d.x, d.y);
+                    const float2 d = fma2(unpack2<FMT>(w[i]), make_float2(-1.f, -1.f), e);
+                    w2[i] = pack2<FMT>(d.x, d.y);
                   }
                 }
                 store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, w);
                 if (PARTS == 2) store_cols(s_at + 32 * c + 16, w2);
               }
-              return (add[0].x + add[0].y) + (add[1].x + add[1].y);
+              return Q8 ? sum : (add[0].x + add[0].y) + (add[1].x + add[1].y);
             };
             auto publish = [&](int half) {  // their products may begin
               wait_stores();
               fence_before();
               mbar_arrive(&bar.p[x][half]);
             };
-            // The maximum is off the path from S to the weights.  They are taken under the
-            // maximum so far as long as they stay below 2^kRescale: the first half's sum
-            // tells for itself, the second half's logits are looked at.  Where they do not
-            // (first tiles, rarely later) the maximum is found, O and the sum are rescaled
-            // and the weights taken again.
             float l0 = 0.f;
-            bool good = m != -INFINITY || !live;
-            if (__builtin_expect(__all_sync(0xffffffffu, good), 1)) {
-              float tops[4] = {s[64], s[65], s[66], s[67]};
+            if constexpr (Q8) {
+              // fp16's range is short: every logit is looked at before the weights are taken.
+              float top = -INFINITY;
 #pragma unroll
-              for (int i = 68; i < 124; i += 8)
+              for (int i = 0; i < 8; ++i) {
+                float t = s[16 * i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
-              const float t = max3(fmaxf(tops[0], s[124]), fmaxf(tops[1], s[125]),
-                                   max3(tops[2], s[126], fmaxf(tops[3], s[127])));
-              l0 = weights(0, m);
-              good = (l0 <= kMost && (t - m) * sc <= kRescale) || !live;
-            }
-            if (__builtin_expect(!__all_sync(0xffffffffu, good), 0)) {
-              float tops[4] = {m, m, m, m};
+                for (int e = 1; e < 15; e += 2) t = max3(t, s[16 * i + e], s[16 * i + e + 1]);
+                t = fmaxf(t, s[16 * i + 15]);
+                top = fmaxf(top, t == -INFINITY ? t : fmaf(t, fmaxf(row_sc * blocks[i].x, kLeastFactor),
+                                                           blocks[i].y));
+              }
+              if (__builtin_expect(__any_sync(0xffffffffu, !(top <= m + kSlack)), 0)) {
+                const float to = fmaxf(m, top - kRaised);
+                const float f = m == to ? 1.f : ex2(m - to);
+                m = to;
+                l *= f;
+                if (j > j0) {
 #pragma unroll
-              for (int i = 0; i < 128; i += 8)
+                  for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    load_cols(o_at + 32 * c, o);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
-              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-              const float f = m == top ? 1.f : ex2((m - top) * sc);
-              m = top;
-              l *= f;
-              if (j > j0) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  float o[32];
-                  load_cols(o_at + 32 * c, o);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] *= f;
-                  store_cols(o_at + 32 * c, o);
+                    for (int i = 0; i < 32; ++i) o[i] *= f;
+                    store_cols(o_at + 32 * c, o);
+                  }
                 }
               }
               l0 = weights(0, m);
+            } else {
+              // The maximum is off the path from S to the weights.  They are taken under the
+              // maximum so far as long as they stay below 2^kRescale: the first half's sum
+              // tells for itself, the second half's logits are looked at.  Where they do not
+              // (first tiles, rarely later) the maximum is found, O and the sum are rescaled
+              // and the weights taken again.
+              bool good = m != -INFINITY || !live;
+              if (__builtin_expect(__all_sync(0xffffffffu, good), 1)) {
+                float tops[4] = {s[64], s[65], s[66], s[67]};
+#pragma unroll
+                for (int i = 68; i < 124; i += 8)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
+                const float t = max3(fmaxf(tops[0], s[124]), fmaxf(tops[1], s[125]),
+                                     max3(tops[2], s[126], fmaxf(tops[3], s[127])));
+                l0 = weights(0, m);
+                good = (l0 <= kMost && (t - m) * sc <= kRescale) || !live;
+              }
+              if (__builtin_expect(!__all_sync(0xffffffffu, good), 0)) {
+                float tops[4] = {m, m, m, m};
+#pragma unroll
+                for (int i = 0; i < 128; i += 8)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                const float f = m == top ? 1.f : ex2((m - top) * sc);
+                m = top;
+                l *= f;
+                if (j > j0) {
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    load_cols(o_at + 32 * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= f;
+                    store_cols(o_at + 32 * c, o);
+                  }
+                }
+                l0 = weights(0, m);
+              }
             }
             publish(0);
             l += l0 + weights(1, m);
@@ -305,12 +449,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       }
       if (live) {
         float* stats = mine + (size_t)rs * kD;
-        stats[r] = m * sc;
+        stats[r] = Q8 ? m : m * sc;
         stats[rs + r] = l;
       }
+      seg_tile += all;
     }
   } else {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<FMT>));
    if (warp == 0 || warp == 3) {
     // ------------------------------------------------ matrix instructions
     // One thread for each stream.  With both on the same tiles by turns: O_A(j), S_A(j+1),
@@ -326,7 +471,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          mma_ss(s_at, qd + at, kx + at, kIdesc, k > 0);
+          mma_ss(s_at, qd + at, kx + at, kQk, k > 0);
         }
         commit_mma(&bar.s[x]);
         commit_mma(&bar.empty[slot]);
@@ -341,20 +486,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         if (n > 0) {
           const uint32_t i = 2 * number(0);
           ok = wait_for(&bar.q[x], segs & 1, &abort_s) &&
-               wait_for(&bar.full[slot_of(i)], lap_of(i), &abort_s);
+               wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (both && x == 1) ok = ok && wait_for(&bar.turn[1], turns & 1, &abort_s);
           if (ok) {
             fence_after();
-            qk(slot_of(i));
+            qk(slot_of<FMT>(i));
           }
           if (both) mbar_arrive(&bar.turn[x ^ 1]);
         }
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t tile = number(j), i = 2 * tile + 1;  // V's slot
-          ok = wait_for(&bar.full[slot_of(i)], lap_of(i), &abort_s);
-          if (ok && (walk.j0 + (int)(tile - passed) + 1) * kTile > walk.s.P)
-            ok = wait_for(&bar.clean[slot_of(tile)], lap_of(tile), &abort_s);
-          const uint64_t vx = vd + slot_of(i) * (kSlotBytes >> 4);
+          ok = wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
+          if (!Q8 && ok && (walk.j0 + (int)(tile - passed) + 1) * kTile > walk.s.P)
+            ok = wait_for(&bar.clean[slot_of<FMT>(tile)], lap_of<FMT>(tile), &abort_s);
+          const uint64_t vx = vd + slot_of<FMT>(i) * (kSlotBytes >> 4);
           const bool more = j % kFoldEvery<PARTS> > 0;
           const uint32_t parity = (tiles + j) & 1;
 #pragma unroll
@@ -369,21 +514,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 const uint64_t vk = vx + ((k * 16 * 128) >> 4);
                 if (PARTS == 2) {
                   const uint32_t w = s_at + 32 * (k >> 1) + 8 * (k & 1);
-                  mma_ts(o_at, w, vk, kIdescV, more || k > 0);
-                  mma_ts(o_at, w + 16, vk, kIdescV, true);
+                  mma_ts(o_at, w, vk, kPv, more || k > 0);
+                  mma_ts(o_at, w + 16, vk, kPv, true);
                 } else {
-                  mma_ts(o_at, s_at + 8 * k, vk, kIdescV, more || k > 0);
+                  mma_ts(o_at, s_at + 8 * k, vk, kPv, more || k > 0);
                 }
               }
             }
           }
           if (!ok) break;
-          commit_mma(&bar.empty[slot_of(i)]);
+          commit_mma(&bar.empty[slot_of<FMT>(i)]);
           if (j + 1 < n) {
             const uint32_t k = 2 * number(j + 1);
-            ok = wait_for(&bar.full[slot_of(k)], lap_of(k), &abort_s);
+            ok = wait_for(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
             if (!ok) break;
-            qk(slot_of(k));
+            qk(slot_of<FMT>(k));
           } else {
             commit_mma(&bar.o[x]);
           }
@@ -408,7 +553,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     // -------------------------------------------------------------- copies
     const int box = a.box;                   // rows of a box: 128, or a smaller page
     const int per = kTile / box;             // boxes of a tile
-    const int i_box = lane >> 1, half = lane & 1;
+    // (bf16: two halves of 64 columns)
+    const int i_box = Q8 ? lane : lane >> 1, half = Q8 ? 0 : lane & 1;
+    const uint32_t raw = ring + SLOTS * kSlotBytes;
     uint32_t it = 0;
     bool ok = true;
     for (int number = 1; ok && walk.next(); ++number) {
@@ -437,21 +584,29 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         next = find(j + 1);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box * 128;
         for (int w = 0; w < 2 && ok; ++w) {
-          const int sl = slot_of(it);
-          if (it >= kSlots) ok = wait(&bar.empty[sl], lap_of(it) ^ 1);
+          const int sl = Q8 ? raw_slot(it) : slot_of<FMT>(it);
+          uint64_t* landed = Q8 ? &bar.raw_full[sl] : &bar.full[sl];
+          if (it >= (Q8 ? kRawSlots : SLOTS))
+            ok = Q8 ? wait(&bar.raw_empty[sl], raw_lap(it) ^ 1)
+                    : wait(&bar.empty[sl], lap_of<FMT>(it) ^ 1);
           if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&bar.full[sl], bytes);
+          if (lane == 0) mbar_expect_tx(landed, bytes);
           __syncwarp();
           if (row >= 0)
-            copy_box(ring + sl * kSlotBytes + half * kHalf + i_box * box * 128, w ? &vmap : &kmap,
-                     64 * half, (int)row, &bar.full[sl]);
+            copy_box(Q8 ? raw + sl * kRawBytes + i_box * box * kD
+                        : ring + sl * kSlotBytes + half * kHalf + i_box * box * 128,
+                     w ? &vmap : &kmap, 64 * half, (int)row, landed);
           ++it;
         }
       }
     }
     if (!ok)  // let the copies in flight land
-      for (uint32_t i = it > kSlots ? it - kSlots : 0; i < it; ++i)
-        mbar_wait(&bar.full[slot_of(i)], lap_of(i));
+      for (uint32_t n = Q8 ? kRawSlots : SLOTS, i = it > n ? it - n : 0; i < it; ++i) {
+        if (Q8)
+          mbar_wait(&bar.raw_full[raw_slot(i)], raw_lap(i));
+        else
+          mbar_wait(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i));
+      }
    } else if (warp == 2) {
     // ---------------------------------------- rows of V behind the shared ones
     uint32_t tile = 0;
@@ -461,20 +616,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       for (int j = walk.j0; j < walk.j1 && ok; ++j, ++tile) {
         // every slot is given back for this warp, and for the stream that passes it by
         auto give = [&](uint32_t i) {
-          mbar_arrive(&bar.empty[slot_of(i)]);
-          if (!both) mbar_arrive(&bar.empty[slot_of(i)]);
+          mbar_arrive(&bar.empty[slot_of<FMT>(i)]);
+          if (!both) mbar_arrive(&bar.empty[slot_of<FMT>(i)]);
         };
         const uint32_t i = 2 * tile;
         if (lane == 0) {
-          ok = wait_for(&bar.full[slot_of(i)], lap_of(i), &abort_s);
+          ok = wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (ok) give(i);
-          ok = ok && wait_for(&bar.full[slot_of(i + 1)], lap_of(i + 1), &abort_s);
+          ok = ok && wait_for(&bar.full[slot_of<FMT>(i + 1)], lap_of<FMT>(i + 1), &abort_s);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int left = walk.s.P - j * kTile;
-        if (left < kTile) {
-          const uint32_t at = ring + slot_of(i + 1) * kSlotBytes + (lane >> 4) * kHalf +
+        if (!Q8 && left < kTile) {
+          const uint32_t at = ring + slot_of<FMT>(i + 1) * kSlotBytes + (lane >> 4) * kHalf +
                               (lane & 15) * 8;
           for (int r = left; r < kTile; ++r)
             asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(at + r * 128), "r"(0)
@@ -483,8 +638,90 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           __syncwarp();
         }
         if (lane == 0) {
-          mbar_arrive(&bar.clean[slot_of(tile)]);
+          if (!Q8) mbar_arrive(&bar.clean[slot_of<FMT>(tile)]);
           give(i + 1);
+        }
+      }
+    }
+   } else if (Q8 && warp >= 12) {
+    // ------------------------------------------- codes to operands, scales
+    // 16 codes a lane and turn: 16 bytes of a row become two pieces of its half of the
+    // operand.  Lanes of the second half store their pieces in the other order, so that
+    // eight lanes together touch all banks.
+    const uint32_t raw = ring + SLOTS * kSlotBytes;
+    const int mine = tid - 384;
+    uint32_t tile = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const int b = walk.s.b0, g = walk.u.g, P = walk.s.P;
+      const int32_t* pages =
+          a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
+      // Lanes 0-7: the keys' scales of key tile j's eight blocks of 16 rows, 8-15 the values'.
+      auto scale_of = [&](int j) {
+        const int r0 = j * kTile + 16 * (lane & 7);
+        if (warp != 12 || lane >= 16 || j >= walk.j1 || r0 >= P) return 1.f;
+        int64_t row = ((int64_t)b * a.c.Hkv + g) * a.c.l_cap + r0;
+        if (pages) {
+          const int32_t page = pages[r0 >> a.c.page_shift];
+          if ((uint32_t)page >= a.c.n_pages) return 1.f;  // (flagged by the copies)
+          row = (((int64_t)page * a.c.Hkv + g) << a.c.page_shift) +
+                (r0 & ((1 << a.c.page_shift) - 1));
+        }
+        return (lane < 8 ? a.c.ks : a.c.vs)[row >> a.c.block_shift];
+      };
+      float next = scale_of(walk.j0);
+      for (int j = walk.j0; j < walk.j1 && ok; ++j, ++tile) {
+        if (warp == 12) {
+          // (a value scale of 0, never written, counts as the least)
+          const float vs = fmaxf(__shfl_down_sync(0xffffffffu, next, 8), kLeastScale);
+          if (lane < 8)
+            scale_s[raw_slot(tile)][lane] = make_float4(next, lg2_scale(vs), 1.f / vs, 0.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.scale[raw_slot(tile)]);
+          next = scale_of(j + 1);
+        }
+        const int left = P - j * kTile;
+        for (int w = 0; w < 2 && ok; ++w) {
+          const uint32_t i = 2 * tile + w;
+          ok = wait(&bar.raw_full[raw_slot(i)], raw_lap(i));
+          if (ok && i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
+          if (!ok) break;
+          const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
+#pragma unroll 4
+          for (int n = 0; n < 8; ++n) {
+            const int at = n * 128 + mine, row = at >> 3, ch = at & 7;
+            uint4 c, x, y;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                         : "r"(from + at * 16)
+                         : "memory");
+            widen<FMT>(c.x, x.x, x.y);
+            widen<FMT>(c.y, x.z, x.w);
+            widen<FMT>(c.z, y.x, y.y);
+            widen<FMT>(c.w, y.z, y.w);
+            if (row >= left) x = y = make_uint4(0u, 0u, 0u, 0u);  // behind the shared rows
+            const int swap = ch >> 2, p = 2 * (ch & 3);
+            if (swap) {
+              const uint4 z = x;
+              x = y;
+              y = z;
+            }
+            const uint32_t half = to + swap * kHalf + row * 128;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             half + (((p + swap) ^ (row & 7)) << 4)),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             half + (((p + 1 - swap) ^ (row & 7)) << 4)),
+                         "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                         : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar.full[slot_of<FMT>(i)]);
+            mbar_arrive(&bar.raw_empty[raw_slot(i)]);
+          }
         }
       }
     }
@@ -498,16 +735,24 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   }
 }
 
+template <int FMT>
+cudaError_t launch_fmt(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a,
+                       cudaStream_t st) {
+  const auto kernel = a.out16 ? shared_prefix_kernel<FMT, 1> : shared_prefix_kernel<FMT, 2>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedSmem<FMT>);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3(kSharedShares), dim3(kSharedThreads<FMT>), kSharedSmem<FMT>,
+                          st, kmap, vmap, a);
+}
+
 }  // namespace
 
 cudaError_t launch_shared_prefix(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                 const SharedArgs& a, cudaStream_t st) {
-  const auto kernel = a.out16 ? shared_prefix_kernel<1> : shared_prefix_kernel<2>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedSmem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3(kSharedShares), dim3(kSharedThreads), kSharedSmem, st, kmap,
-                          vmap, a);
+                                 const SharedArgs& a, int fmt, cudaStream_t st) {
+  if (fmt == kFmtInt8) return launch_fmt<kFmtInt8>(kmap, vmap, a, st);
+  if (fmt == kFmtE4m3) return launch_fmt<kFmtE4m3>(kmap, vmap, a, st);
+  return launch_fmt<kFmtBf16>(kmap, vmap, a, st);
 }
 
 }  // namespace tsa
