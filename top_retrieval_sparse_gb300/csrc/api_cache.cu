@@ -330,7 +330,7 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
 // Workspace of a step with shared rows.  Nothing but the status word outlasts a call, so
 // that calls of whatever sizes may share it.
 struct SharedLayout {
-  size_t partial, arrived, rows, groups, own, parts, total;
+  size_t partial, arrived, rows, total_at, groups, segments, own, parts, total;
 };
 SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   SharedLayout l{};
@@ -340,8 +340,12 @@ SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   l.partial = kDecodePartial;
   l.arrived = kDecodeArrived;
   l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));
-  l.groups = l.rows + 2 * round_up((size_t)B * sizeof(int32_t));
-  l.own = l.groups + kAlign + round_up((size_t)N * sizeof(SharedGroup));
+  l.total_at = l.rows + 2 * round_up((size_t)B * sizeof(int32_t));
+  l.groups = l.total_at + round_up(sizeof(SharedTotal));
+  l.segments = l.groups + round_up((size_t)N * sizeof(SharedGroup));
+  // (a unit has 256 queries, or is its group and head's last)
+  const size_t list = kSharedShares + (size_t)B * Hq / kUnitRows + (size_t)Hkv * (N < B ? N : B);
+  l.own = l.segments + round_up(list * sizeof(SharedSegment));
   l.parts = l.own + row;
   l.total = l.parts +
             round_up((size_t)(kSharedShares * kShareRows + units) * (kD + 2) * sizeof(float));
@@ -389,8 +393,9 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   const size_t ints = round_up((size_t)B * sizeof(int32_t)), rows = (size_t)B * Hq;
   s.group = reinterpret_cast<int32_t*>(ws + l.rows);
   s.start = reinterpret_cast<int32_t*>(ws + l.rows + ints);
-  s.total = reinterpret_cast<SharedTotal*>(ws + l.groups);
-  s.groups = reinterpret_cast<SharedGroup*>(ws + l.groups + kAlign);
+  s.total = reinterpret_cast<SharedTotal*>(ws + l.total_at);
+  s.groups = reinterpret_cast<SharedGroup*>(ws + l.groups);
+  s.segments = reinterpret_cast<SharedSegment*>(ws + l.segments);
   s.own_out = reinterpret_cast<float*>(ws + l.own);
   s.own_lse = s.own_out + rows * kD;
   s.parts = reinterpret_cast<float*>(ws + l.parts);

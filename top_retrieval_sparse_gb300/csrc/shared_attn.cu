@@ -36,6 +36,61 @@ __device__ int64_t block_prefix(int64_t x, int64_t* scratch, int64_t& total) {
   return before + y - x;
 }
 
+// The segments of a share, in order: costs [at, end) of the list.
+__device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share) {
+  const int Hkv = a.c.Hkv;
+  int count = 0;
+  if (share < t.shares && t.cost > 0) {
+    int64_t at = share_start(t, share);
+    const int64_t end = share_start(t, share + 1);
+    int n = 0;
+    for (int hi = a.N; hi - n > 1;) {  // the last group that starts at or before `at`
+      const int mid = (n + hi) >> 1;
+      if (a.groups[mid].cost0 <= at) n = mid; else hi = mid;
+    }
+    SharedGroup s = a.groups[n];
+    while (at < end) {
+      const int64_t tiles = (s.P + 127) / 128, column = tiles * Hkv * kCostBoth;
+      int64_t g = Hkv;
+      SharedUnit u;
+      if (s.rows > 0) {
+        const int last = (s.rows - 1) / kUnitRows;  // all columns but this one are full
+        int64_t k = (at - s.cost0) / column;
+        if (k > last) k = last;
+        const int w = s.rows - (int)k * kUnitRows > 128 ? kCostBoth : kCostAlone;
+        g = (at - s.cost0 - k * column) / (tiles * w);
+        if (g < Hkv) u = unit_of(s, Hkv, (int)k, (int)g);
+      }
+      if (g >= Hkv) {
+        if (++n >= a.N) break;
+        s = a.groups[n];
+        continue;
+      }
+      SharedSegment x;
+      x.j0 = (int)((at - u.cost0 + u.w - 1) / u.w);
+      const int64_t j1 = (end - u.cost0 + u.w - 1) / u.w;
+      x.j1 = j1 < u.tiles ? (int)j1 : u.tiles;
+      at = u.cost0 + (int64_t)u.tiles * u.w;
+      if (x.j0 >= x.j1) continue;  // (begins behind the last tile's start)
+      const int row = u.t * kUnitRows;
+      x.b0 = s.b0;
+      x.P = s.P;
+      x.seq0 = s.b0 + row / a.G;
+      x.in0 = row % a.G;
+      x.g = u.g;
+      x.rows = u.rows;
+      x.rs = u.rs;
+      x.both = u.both();
+      x.part = segment_part(u, share, x.j0 == 0);
+      const int number = share + s.unit0 + u.t * Hkv + u.g;
+      if (count == 0) a.total->first[share] = number;
+      a.segments[number] = x;
+      ++count;
+    }
+  }
+  a.total->count[share] = count;
+}
+
 // The groups' work in a list, and who shares what with whom (the first CTA); the decode
 // kernel's counters cleared (the others).
 __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a) {
@@ -59,12 +114,12 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
     bad |= cu_s[n] < 0 || cu_s[n] > cu_s[n + 1] || cu_s[n + 1] > B;
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(a.status, kStatusBadLength);
-  int64_t cost = 0, rows = 0;
+  int64_t cost = 0, rows = 0, units = 0;
   int columns = 0, groups = 0;  // of groups with work
   for (int n0 = 0; n0 < N; n0 += kPrepThreads) {
     const int n = n0 + tid;
     SharedGroup s{};
-    int64_t c = 0, r = 0, total;
+    int64_t c = 0, r = 0, k = 0, total;
     bool some = false;
     if (n < N && !bad) {
       const int P = a.shared[n];
@@ -78,6 +133,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
         c = (int64_t)((s.P + 127) / 128) * Hkv * ((int64_t)last * kCostBoth + w);
         r = group_rows(s.rows, Hkv);
         columns += last + 1;
+        k = (int64_t)(last + 1) * Hkv;
         some = true;
       }
     }
@@ -85,6 +141,8 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
     cost += total;
     s.row0 = rows + block_prefix(r, scan_s, total);
     rows += total;
+    s.unit0 = (int)(units + block_prefix(k, scan_s, total));
+    units += total;
     if (n < N) a.groups[n] = s;
     groups += __syncthreads_count(some);
   }
@@ -96,12 +154,18 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
   }
   if (groups != 1 && tid == 0) scan_s[0] = kSharedShares;
   __syncthreads();
-  if (tid == 0) {
+  SharedTotal total;
+  total.cost = cost;
+  {
     int64_t shares = scan_s[0];
     if (shares > cost / kCostBoth) shares = cost / kCostBoth;
-    a.total->cost = cost;
-    a.total->shares = shares < 1 ? 1 : (int)shares;
+    total.shares = shares < 1 ? 1 : (int)shares;
   }
+  if (tid == 0) {
+    a.total->cost = total.cost;
+    a.total->shares = total.shares;
+  }
+  for (int share = tid; share < kSharedShares; share += kPrepThreads) list_share(a, total, share);
   for (int b = tid; b < B; b += kPrepThreads) {
     int n = -1, start = 0;
     if (bad) {
@@ -166,8 +230,7 @@ if (!nan) {
         float l_all = 0.f;
         for (int e = lane; e < parts; e += 32) {
           const int share = s0 + (both ? e : e >> 1);
-          const int place = (int)((segment_parts(a, u, share, share > s0) - a.parts) / 4) +
-                            (both ? r >> 7 : e & 1) * half;
+          const int place = (int)segment_part(u, share, share == s0) + (both ? r >> 7 : e & 1) * half;
           const float* stats = a.parts + (int64_t)place * 4 + u.rs * kD + at;
           const float pm = stats[0], pl = stats[u.rs];
           place_s[h][e] = place + at;

@@ -20,11 +20,22 @@ struct SharedGroup {
   int32_t b0;     // first sequence
   int32_t rows;   // queries of a KV head: sequences * G
   int32_t P;      // shared rows
-  int32_t pad;
+  int32_t unit0;  // units of the groups before it
 };
 struct SharedTotal {
   int64_t cost;
   int32_t shares;  // of the list that take part
+  // each share's segments: the number of the first, how many
+  int32_t first[kSharedShares], count[kSharedShares];
+};
+// What a share has of a unit.
+struct __align__(16) SharedSegment {
+  int32_t b0, P;         // the group's first sequence, its rows
+  int32_t seq0, in0;     // sequence and query head of the unit's first query
+  int32_t g, rows, rs;   // KV head, queries, rows of a half of the partials
+  int32_t both;          // two query tiles
+  int32_t j0, j1;        // key tiles
+  int64_t part;          // its partials: float4's from a.parts
 };
 
 struct SharedArgs {
@@ -46,6 +57,7 @@ struct SharedArgs {
   int32_t* start;          // [B]: its rows before this one are the group's
   SharedGroup* groups;     // [N]
   SharedTotal* total;
+  SharedSegment* segments; // share after share; number: the share's, plus that of the unit
   float* own_out;          // [B][Hq][128]: over its own rows
   float* own_lse;          // [B][Hq]
   uint32_t* arrived;       // counters of the decode kernel
@@ -94,72 +106,13 @@ __device__ __forceinline__ SharedUnit unit_of(const SharedGroup& s, int Hkv, int
 // Floats from a half of a segment's partials to the next: O as [32][rs] pieces of four
 // columns, then maxima and sums.
 __device__ __forceinline__ int64_t half_floats(int rs) { return (int64_t)rs * (kD + 2); }
-__device__ __forceinline__ float* segment_parts(const SharedArgs& a, const SharedUnit& u, int share,
-                                                int j0) {
-  const int64_t row = j0 > 0 ? share * kShareRows : kSharedShares * kShareRows + u.row0;
-  return a.parts + row * (kD + 2);
+// Where a segment's partials begin (a share has at most one that is not its unit's first), in
+// pieces of 16 bytes.
+__device__ __forceinline__ int64_t segment_part(const SharedUnit& u, int share, bool first) {
+  const int64_t row = first ? kSharedShares * kShareRows + u.row0 : share * kShareRows;
+  return row * (kD + 2) / 4;
 }
 
-// A share's segments, in order.
-struct SharedWalk {
-  const SharedArgs& a;
-  int64_t at, end;     // costs
-  int n;               // group
-  SharedGroup s;
-  SharedUnit u;
-  int j0, j1;          // key tiles of the segment
-  __device__ SharedWalk(const SharedArgs& args, int share) : a(args) {
-    const SharedTotal t = *a.total;
-    at = end = 0;
-    n = -1;
-    if (share >= t.shares) return;
-    at = share_start(t, share);
-    end = share_start(t, share + 1);
-    if (at >= end) return;
-    int lo = 0;
-    for (int hi = a.N; hi - lo > 1;) {  // the last group that starts at or before `at`
-      const int mid = (lo + hi) >> 1;
-      if (a.groups[mid].cost0 <= at) lo = mid; else hi = mid;
-    }
-    n = lo;
-    s = a.groups[n];
-  }
-  // The next segment; false: none.
-  __device__ bool next() {
-    if (at >= end) return false;
-    const int Hkv = a.c.Hkv;
-    for (;;) {
-      const int64_t tiles = (s.P + 127) / 128, off = at - s.cost0;
-      const int last = (s.rows - 1) / kUnitRows;
-      const int64_t column = tiles * Hkv * kCostBoth;  // all but the last are full
-      if (s.rows > 0 && tiles > 0) {
-        int64_t t = off / column;
-        if (t > last) t = last;
-        const int64_t in = off - t * column;
-        const int w = s.rows - (int)t * kUnitRows > 128 ? kCostBoth : kCostAlone;
-        const int64_t g = in / (tiles * w);
-        if (g < Hkv) {
-          u = unit_of(s, Hkv, (int)t, (int)g);
-          j0 = (int)((at - u.cost0 + w - 1) / w);
-          if (j0 < u.tiles) {
-            const int64_t n1 = (end - u.cost0 + w - 1) / w;
-            j1 = n1 < u.tiles ? (int)n1 : u.tiles;
-            at = u.cost0 + (int64_t)u.tiles * w;
-            return j1 > j0 ? true : (at = end, false);
-          }
-          at = u.cost0 + (int64_t)u.tiles * w;  // (begins behind the last tile's start)
-          if (at >= end) return false;
-          continue;
-        }
-      }
-      if (++n >= a.N) {
-        at = end;
-        return false;
-      }
-      s = a.groups[n];
-    }
-  }
-};
 #endif
 
 }  // namespace tsa

@@ -40,11 +40,8 @@ constexpr int kSlots = FMT == kFmtBf16 ? 5 : 3;
 constexpr int kRawSlots = 4, kRawBytes = kTile * kD;
 template <int FMT>
 constexpr int kSharedThreads = FMT == kFmtBf16 ? 384 : 512;
-// Registers a scheduler: 2 * 216 + 72 = 3 * 168, or 2 * 200 + 2 * 56 = 4 * 128.
-template <int FMT>
-constexpr int kSoftmaxRegs = FMT == kFmtBf16 ? 216 : 200;
-template <int FMT>
-constexpr int kOtherRegs = FMT == kFmtBf16 ? 72 : 56;
+// Registers a scheduler (bf16): 2 * 216 + 72 = 3 * 168.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 template <int FMT>
 constexpr int kSharedSmem = (2 + kSlots<FMT>) * kSlotBytes +
                             (FMT == kFmtBf16 ? 0 : kRawSlots * kRawBytes) + 1024;
@@ -167,11 +164,12 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
   auto wait = [&](uint64_t* x, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_for(x, parity, &abort_s)) != 0;
   };
-  SharedWalk walk(a, blockIdx.x);
+  const int n_seg = a.total->count[blockIdx.x];
+  const SharedSegment* segments = a.segments + (n_seg > 0 ? a.total->first[blockIdx.x] : 0);
 
   if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<FMT>));
+    if (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = (warp >> 2) - 1;           // stream A or B
     const int r = tid & 127;                 // row of the stream's tile
     const int r_warp = (warp & 3) * 32, r_half = lane >> 4, piece = lane & 15;
@@ -182,16 +180,16 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     uint32_t tiles = 0, segs = 0;            // of this stream, so far
     uint32_t seg_tile = 0;                   // tiles of the segments before this one
     bool ok = true;
-    for (int number = 1; walk.next(); ++number) {
-      const SharedUnit& u = walk.u;
-      const bool both = u.both();
+    for (int number = 0; number < n_seg; ++number) {
+      const SharedSegment& u = segments[number];
+      const bool both = u.both;
       const int first = both ? x * kTile : 0;            // the stream's first row of the unit
       const bool live = first + r < u.rows;
       const bool warp_live = first + r_warp < u.rows;
-      const int all = walk.j1 - walk.j0;
+      const int all = u.j1 - u.j0, tile0 = u.j0;
       const int n = both ? all : (all - x + 1) / 2;      // tiles of this stream
-      const int P = walk.s.P, rs = u.rs;
-      float* mine = segment_parts(a, u, blockIdx.x, walk.j0) + x * half_floats(rs);
+      const int P = u.P, rs = u.rs;
+      float* mine = a.parts + 4 * u.part + x * half_floats(rs);
       float4* sums = reinterpret_cast<float4*>(mine) + r;  // columns 4 i .. at sums[i * rs]
       float m = -INFINITY, l = 0.f;
       float row_sc = sc;                     // 8-bit: with the inverse of the queries' shift
@@ -200,16 +198,16 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         // A half-warp a row, so that a row's 256 bytes are one request.
         {
           const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-          const int seq0 = u.t * kUnitRows / a.G, in0 = u.t * kUnitRows - seq0 * a.G;
+          const int seq0 = u.seq0, in0 = u.in0, rows = u.rows, head0 = u.g * a.G;
           uint4 w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int rr = first + r_warp + 2 * i + r_half;
             w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < u.rows && a.scale_log2 != 0.f) {
+            if (rr < rows && a.scale_log2 != 0.f) {
               const int sq = ((in0 + rr) * a.inv_g) >> 16, h = in0 + rr - sq * a.G;
               w[i] = *reinterpret_cast<const uint4*>(
-                  a.q + ((int64_t)(walk.s.b0 + seq0 + sq) * a.Hq + u.g * a.G + h) * kD + 8 * piece);
+                  a.q + ((int64_t)(seq0 + sq) * a.Hq + head0 + h) * kD + 8 * piece);
             }
           }
           if constexpr (Q8) {
@@ -282,7 +280,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         for (int j0 = 0; j0 < n && ok; j0 += kFoldEvery<PARTS>) {
           const int j1 = j0 + kFoldEvery<PARTS> < n ? j0 + kFoldEvery<PARTS> : n;
           for (int j = j0; j < j1; ++j) {
-            const int tile = both ? j : 2 * j + x, k0 = (walk.j0 + tile) * kTile;
+            const int tile = both ? j : 2 * j + x, k0 = (tile0 + tile) * kTile;
             const uint32_t parity = (tiles + j) & 1;
             ok = wait(&bar.s[x], parity);
             if (__builtin_expect(!ok, 0)) break;
@@ -296,25 +294,25 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             fence_after();
             // (S is there, so O's products before it are done)
             if (__builtin_expect(j == j0 && j > 0, 0)) put();
-            float s[128];
-            if constexpr (Q8) {  // (one load of 128 would need more registers than at launch)
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                load_cols(s_at + 32 * c, reinterpret_cast<float(&)[32]>(s[32 * c]));
-            } else {
-              load_cols(s_at, s);
-            }
-            if (__builtin_expect(k0 + kTile > P, 0)) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
+            // 8-bit: y = log2 of a weight with its row's value scale, block by block of 16; the
+            // columns are read twice, 32 at a time, for want of registers.
+            const float4* blocks = scale_s[Q8 ? (seg_tile + tile) % kRawSlots : 0];
+            float s[Q8 ? 32 : 128];
+            auto columns = [&](int c) {  // 32 c ..., masked
+              float(&y)[32] = reinterpret_cast<float(&)[32]>(s[Q8 ? 0 : 32 * c]);
+              if (Q8) load_cols(s_at + 32 * c, y);
+              if (__builtin_expect(k0 + kTile > P, 0)) {
                 const uint32_t on = below(P - k0 - 32 * c);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (!(on & (1u << i))) s[32 * c + i] = -INFINITY;
+                  if (!(on & (1u << i))) y[i] = -INFINITY;
               }
+            };
+            if constexpr (!Q8) {
+              load_cols(s_at, s);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) columns(c);
             }
-            // 8-bit: y = log2 of a weight with its row's value scale, block by block of 16
-            const float4* blocks = scale_s[Q8 ? (seg_tile + tile) % kRawSlots : 0];
             // Weights of half a tile (64 keys) under the maximum `top`; their sum.
             auto weights = [&](int half, float top) {
               const float off = top == -INFINITY ? 0.f : (Q8 ? -top : -top * sc);
@@ -322,6 +320,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               float sum = 0.f;
 #pragma unroll
               for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                if (Q8) columns(c);
+                const float* y = s + (Q8 ? 0 : 32 * c);
                 uint32_t w[16], w2[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
                     o = off + k.y;
                     if (i % 8 == 0) add[0] = add[1] = make_float2(0.f, 0.f);
                   }
-                  float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]),
-                                  make_float2(f, f), make_float2(o, o));
+                  float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), make_float2(f, f),
+                                  make_float2(o, o));
                   e.x = ex2(e.x);
                   e.y = ex2(e.y);
                   add[i & 1] = add2(add[i & 1], e);
@@ -363,13 +363,18 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               // fp16's range is short: every logit is looked at before the weights are taken.
               float top = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float t = s[16 * i];
+              for (int c = 0; c < 4; ++c) {
+                columns(c);
 #pragma unroll
-                for (int e = 1; e < 15; e += 2) t = max3(t, s[16 * i + e], s[16 * i + e + 1]);
-                t = fmaxf(t, s[16 * i + 15]);
-                top = fmaxf(top, t == -INFINITY ? t : fmaf(t, fmaxf(row_sc * blocks[i].x, kLeastFactor),
-                                                           blocks[i].y));
+                for (int i = 0; i < 2; ++i) {
+                  float t = s[16 * i];
+#pragma unroll
+                  for (int e = 1; e < 15; e += 2) t = max3(t, s[16 * i + e], s[16 * i + e + 1]);
+                  t = fmaxf(t, s[16 * i + 15]);
+                  const float4 k = blocks[2 * c + i];
+                  const float f = fmaxf(row_sc * k.x, kLeastFactor);
+                  top = fmaxf(top, t == -INFINITY ? t : fmaf(t, f, k.y));
+                }
               }
               if (__builtin_expect(__any_sync(0xffffffffu, !(top <= m + kSlack)), 0)) {
                 const float to = fmaxf(m, top - kRaised);
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         tiles += n;
         ++segs;
       }
-      if (!ok || bad_s[number & 7] == number) {
+      if (!ok || bad_s[number & 7] == number + 1) {
         l = nanf("");
         m = 0.f;
       }
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
       seg_tile += all;
     }
   } else {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<FMT>));
+   if (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
    if (warp == 0 || warp == 3) {
     // ------------------------------------------------ matrix instructions
     // One thread for each stream.  With both on the same tiles by turns: O_A(j), S_A(j+1),
@@ -479,9 +484,10 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
       // so far: tiles and segments of this stream, turns, tiles of the segments
       uint32_t tiles = 0, segs = 0, turns = 0, passed = 0;
       bool ok = true;
-      while (ok && walk.next()) {
-        const bool both = walk.u.both();
-        const int all = walk.j1 - walk.j0, n = both ? all : (all - x + 1) / 2;
+      for (int seg = 0; ok && seg < n_seg; ++seg) {
+        const bool both = segments[seg].both;
+        const int j0 = segments[seg].j0, P = segments[seg].P;
+        const int all = segments[seg].j1 - j0, n = both ? all : (all - x + 1) / 2;
         auto number = [&](int j) { return passed + (both ? j : 2 * j + x); };
         if (n > 0) {
           const uint32_t i = 2 * number(0);
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t tile = number(j), i = 2 * tile + 1;  // V's slot
           ok = wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
-          if (!Q8 && ok && (walk.j0 + (int)(tile - passed) + 1) * kTile > walk.s.P)
+          if (!Q8 && ok && (j0 + (int)(tile - passed) + 1) * kTile > P)
             ok = wait_for(&bar.clean[slot_of<FMT>(tile)], lap_of<FMT>(tile), &abort_s);
           const uint64_t vx = vd + slot_of<FMT>(i) * (kSlotBytes >> 4);
           const bool more = j % kFoldEvery<PARTS> > 0;
@@ -558,28 +564,29 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     const uint32_t raw = ring + SLOTS * kSlotBytes;
     uint32_t it = 0;
     bool ok = true;
-    for (int number = 1; ok && walk.next(); ++number) {
-      const int b = walk.s.b0, g = walk.u.g, P = walk.s.P;
+    for (int number = 0; ok && number < n_seg; ++number) {
+      const int b = segments[number].b0, g = segments[number].g, P = segments[number].P;
+      const int j0 = segments[number].j0, j1 = segments[number].j1;
       const int32_t* pages =
           a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
       // Lane's box of key tile j: its first row in the pool, or -1 where nothing of it
       // is seen.
       auto find = [&](int j) -> int64_t {
-        if (j >= walk.j1 || i_box >= per) return -1;
+        if (j >= j1 || i_box >= per) return -1;
         const int r0 = j * kTile + i_box * box;
         if (r0 >= P) return -1;
         if (!pages) return ((int64_t)b * a.c.Hkv + g) * a.c.l_cap + r0;
         const int32_t page = pages[r0 >> a.c.page_shift];
         if ((uint32_t)page >= a.c.n_pages) {
-          bad_s[number & 7] = number;
+          bad_s[number & 7] = number + 1;
           atomicOr(a.status, kStatusBadLength);
           return -1;
         }
         return (((int64_t)page * a.c.Hkv + g) << a.c.page_shift) +
                (r0 & ((1 << a.c.page_shift) - 1));
       };
-      int64_t next = find(walk.j0);
-      for (int j = walk.j0; j < walk.j1 && ok; ++j) {
+      int64_t next = find(j0);
+      for (int j = j0; j < j1 && ok; ++j) {
         const int64_t row = next;
         next = find(j + 1);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box * 128;
@@ -611,9 +618,10 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     // ---------------------------------------- rows of V behind the shared ones
     uint32_t tile = 0;
     bool ok = true;
-    while (ok && walk.next()) {
-      const bool both = walk.u.both();
-      for (int j = walk.j0; j < walk.j1 && ok; ++j, ++tile) {
+    for (int seg = 0; ok && seg < n_seg; ++seg) {
+      const bool both = segments[seg].both;
+      const int P = segments[seg].P, j1 = segments[seg].j1;
+      for (int j = segments[seg].j0; j < j1 && ok; ++j, ++tile) {
         // every slot is given back for this warp, and for the stream that passes it by
         auto give = [&](uint32_t i) {
           mbar_arrive(&bar.empty[slot_of<FMT>(i)]);
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int left = walk.s.P - j * kTile;
+        const int left = P - j * kTile;
         if (!Q8 && left < kTile) {
           const uint32_t at = ring + slot_of<FMT>(i + 1) * kSlotBytes + (lane >> 4) * kHalf +
                               (lane & 15) * 8;
@@ -652,14 +660,15 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     const int mine = tid - 384;
     uint32_t tile = 0;
     bool ok = true;
-    while (ok && walk.next()) {
-      const int b = walk.s.b0, g = walk.u.g, P = walk.s.P;
+    for (int seg = 0; ok && seg < n_seg; ++seg) {
+      const int b = segments[seg].b0, g = segments[seg].g, P = segments[seg].P;
+      const int j0 = segments[seg].j0, j1 = segments[seg].j1;
       const int32_t* pages =
           a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
       // Lanes 0-7: the keys' scales of key tile j's eight blocks of 16 rows, 8-15 the values'.
       auto scale_of = [&](int j) {
         const int r0 = j * kTile + 16 * (lane & 7);
-        if (warp != 12 || lane >= 16 || j >= walk.j1 || r0 >= P) return 1.f;
+        if (warp != 12 || lane >= 16 || j >= j1 || r0 >= P) return 1.f;
         int64_t row = ((int64_t)b * a.c.Hkv + g) * a.c.l_cap + r0;
         if (pages) {
           const int32_t page = pages[r0 >> a.c.page_shift];
@@ -669,8 +678,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         }
         return (lane < 8 ? a.c.ks : a.c.vs)[row >> a.c.block_shift];
       };
-      float next = scale_of(walk.j0);
-      for (int j = walk.j0; j < walk.j1 && ok; ++j, ++tile) {
+      float next = scale_of(j0);
+      for (int j = j0; j < j1 && ok; ++j, ++tile) {
         if (warp == 12) {
           // (a value scale of 0, never written, counts as the least)
           const float vs = fmaxf(__shfl_down_sync(0xffffffffu, next, 8), kLeastScale);
@@ -687,34 +696,36 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           if (ok && i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
           if (!ok) break;
           const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
-#pragma unroll 4
-          for (int n = 0; n < 8; ++n) {
-            const int at = n * 128 + mine, row = at >> 3, ch = at & 7;
-            uint4 c, x, y;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
-                         : "r"(from + at * 16)
-                         : "memory");
-            widen<FMT>(c.x, x.x, x.y);
-            widen<FMT>(c.y, x.z, x.w);
-            widen<FMT>(c.z, y.x, y.y);
-            widen<FMT>(c.w, y.z, y.w);
-            if (row >= left) x = y = make_uint4(0u, 0u, 0u, 0u);  // behind the shared rows
-            const int swap = ch >> 2, p = 2 * (ch & 3);
-            if (swap) {
-              const uint4 z = x;
-              x = y;
-              y = z;
+#pragma unroll
+          for (int n0 = 0; n0 < 8; n0 += 4) {
+            uint4 c[4];                      // (all loads before the first store)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
+                           : "r"(from + ((n0 + n) * 128 + mine) * 16)
+                           : "memory");
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int row = ((n0 + n) * 128 + mine) >> 3, ch = mine & 7;
+              uint4 x, y;
+              widen<FMT>(c[n].x, x.x, x.y);
+              widen<FMT>(c[n].y, x.z, x.w);
+              widen<FMT>(c[n].z, y.x, y.y);
+              widen<FMT>(c[n].w, y.z, y.w);
+              if (row >= left) x = y = make_uint4(0u, 0u, 0u, 0u);  // behind the shared rows
+              const int swap = ch >> 2, p = 2 * (ch & 3);
+              const uint32_t half = to + swap * kHalf + row * 128;
+              const uint32_t at_x = half + ((p ^ (row & 7)) << 4);
+              const uint32_t at_y = half + (((p + 1) ^ (row & 7)) << 4);
+              const uint4 u = swap ? y : x, v = swap ? x : y;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(swap ? at_y : at_x),
+                           "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(swap ? at_x : at_y),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
             }
-            const uint32_t half = to + swap * kHalf + row * 128;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             half + (((p + swap) ^ (row & 7)) << 4)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             half + (((p + 1 - swap) ^ (row & 7)) << 4)),
-                         "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                         : "memory");
           }
           fence_proxy_async();
           __syncwarp();
