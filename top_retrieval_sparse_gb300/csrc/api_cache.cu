@@ -335,8 +335,10 @@ struct SharedLayout {
 SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   SharedLayout l{};
   const size_t row = round_up((size_t)B * Hq * (kD + 1) * sizeof(float));
-  // at most: every share's first segment, and the units' (two halves, rounded up to 8)
-  const int64_t units = 2 * ((int64_t)B * Hq + (int64_t)8 * Hkv * (N < B ? N : B));
+  // at most: every share's first segment, and the units' (two halves; units of up to 64
+  // queries, one of a group and head, have up to four copies of each row)
+  const int64_t groups = N < B ? N : B, all = (int64_t)B * Hq, few = groups * Hkv * 64;
+  const int64_t units = 2 * all + 6 * (all < few ? all : few) + 2 * groups * Hkv;
   l.partial = kDecodePartial;
   l.arrived = kDecodeArrived;
   l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));

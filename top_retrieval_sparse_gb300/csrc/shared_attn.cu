@@ -81,6 +81,7 @@ __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share)
       x.rows = u.rows;
       x.rs = u.rs;
       x.both = u.both();
+      x.copies = u.both() ? 1 : tile_copies(u.rows);
       x.part = segment_part(u, share, x.j0 == 0);
       const int number = share + s.unit0 + u.t * Hkv + u.g;
       if (count == 0) a.total->first[share] = number;
@@ -221,7 +222,6 @@ if (!nan) {
         const int r0 = (b - s.b0) * G + h, column = r0 / kUnitRows, r = r0 - column * kUnitRows;
         const SharedUnit u = unit_of(s, Hkv, column, g);
         const bool both = u.both();
-        const int at = both ? r & 127 : r;
         const int half = (int)(half_floats(u.rs) / 4);
         const int s0 = (int)(u.cost0 * t.shares / t.cost);
         const int s1 = (int)((u.cost0 + (int64_t)(u.tiles - 1) * u.w) * t.shares / t.cost);
@@ -229,7 +229,7 @@ if (!nan) {
         rs = u.rs;
         float l_all = 0.f;
         for (int e = lane; e < parts; e += 32) {
-          const int share = s0 + (both ? e : e >> 1);
+          const int share = s0 + (both ? e : e >> 1), at = both ? r & 127 : r;
           const int place = (int)segment_part(u, share, share == s0) + (both ? r >> 7 : e & 1) * half;
           const float* stats = a.parts + (int64_t)place * 4 + u.rs * kD + at;
           const float pm = stats[0], pl = stats[u.rs];

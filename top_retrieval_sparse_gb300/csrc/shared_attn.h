@@ -34,7 +34,8 @@ struct __align__(16) SharedSegment {
   int32_t seq0, in0;     // sequence and query head of the unit's first query
   int32_t g, rows, rs;   // KV head, queries, rows of a half of the partials
   int32_t both;          // two query tiles
-  int32_t j0, j1;        // key tiles
+  int32_t copies;        // of the queries in the one tile
+  int32_t j0, j1, pad;   // key tiles
   int64_t part;          // its partials: float4's from a.parts
 };
 
@@ -68,15 +69,19 @@ cudaError_t launch_shared_prefix(const CUtensorMap& kmap, const CUtensorMap& vma
                                  const SharedArgs& a, int fmt, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t st);
 
-// Rows of partials (of kD + 2 floats) that a group of `rows` queries can need, and a share.
+// Rows of partials (of kD + 2 floats) that a share can need, a half of a unit of so many
+// queries (while sums are folded the copies in its one tile have theirs), and a group's units.
 constexpr int64_t kShareRows = kUnitRows;
-__host__ __device__ inline int tile_rows(int rows) {  // of a unit's half
-  return rows > 128 ? 128 : (rows + 7) / 8 * 8;
+// Few queries are laid out 4 or 2 times in their tile of 128 rows, and each copy takes a part
+// of the key tile's columns, so that all warps have exponentials to take.
+__host__ __device__ inline int tile_copies(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
+__host__ __device__ inline int half_rows(int rows) {
+  return rows > 128 ? 128 : (rows * tile_copies(rows) + 1) / 2 * 2;
 }
 __host__ __device__ inline int64_t group_rows(int rows, int Hkv) {
   if (rows == 0) return 0;
   const int full = (rows - 1) / kUnitRows;
-  return (int64_t)Hkv * (full * kUnitRows + 2 * tile_rows(rows - full * kUnitRows));
+  return (int64_t)Hkv * (full * kUnitRows + 2 * half_rows(rows - full * kUnitRows));
 }
 
 #ifdef __CUDACC__
@@ -98,7 +103,7 @@ __device__ __forceinline__ SharedUnit unit_of(const SharedGroup& s, int Hkv, int
   u.rows = s.rows - t * kUnitRows < kUnitRows ? s.rows - t * kUnitRows : kUnitRows;
   u.tiles = (s.P + 127) / 128;
   u.w = u.rows > 128 ? kCostBoth : kCostAlone;
-  u.rs = tile_rows(u.rows);
+  u.rs = half_rows(u.rows);
   u.cost0 = s.cost0 + (int64_t)u.tiles * ((int64_t)t * Hkv * kCostBoth + g * u.w);
   u.row0 = s.row0 + (int64_t)t * Hkv * kUnitRows + (int64_t)g * 2 * u.rs;
   return u;

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
   // 8-bit: of a tile's blocks of 16 rows: the keys' scale, the logarithm of the values' scale
   // and its inverse.
   __shared__ float4 scale_s[Q8 ? kRawSlots : 1][8];
+  __shared__ float2 run_s[2][64];            // maxima and sums while copies are joined
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
   __shared__ volatile int bad_s[8];          // number of a segment that met a bad page
@@ -183,28 +184,36 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     for (int number = 0; number < n_seg; ++number) {
       const SharedSegment& u = segments[number];
       const bool both = u.both;
-      const int first = both ? x * kTile : 0;            // the stream's first row of the unit
-      const bool live = first + r < u.rows;
-      const bool warp_live = first + r_warp < u.rows;
+      // The unit's row in this thread's row of the tile.  Few queries are there in copies,
+      // each of which takes its part of every tile's columns.
+      const int copies = u.copies, lg = copies >> 1, span = kTile >> lg, copy = r >> (7 - lg);
+      const int first = both ? x * kTile : 0, unit_rows = u.rows;
+      const int row = first + (r & (span - 1));
+      const bool live = row < unit_rows;
+      const bool warp_live = first + (r_warp & (span - 1)) < unit_rows;
+      // bit c: columns 32 c ... are this copy's
+      const uint32_t mine_c = copies == 1 ? 15u : (copies == 2 ? 3u << 2 * copy : 1u << copy);
+      auto mine_is = [&](int c) { return (mine_c >> c & 1u) != 0u; };
       const int all = u.j1 - u.j0, tile0 = u.j0;
       const int n = both ? all : (all - x + 1) / 2;      // tiles of this stream
       const int P = u.P, rs = u.rs;
       float* mine = a.parts + 4 * u.part + x * half_floats(rs);
-      float4* sums = reinterpret_cast<float4*>(mine) + r;  // columns 4 i .. at sums[i * rs]
+      // columns 4 i .. of this thread's sum at sums[i * rs]
+      float4* sums = reinterpret_cast<float4*>(mine) + (both ? r : copy * unit_rows + row);
       float m = -INFINITY, l = 0.f;
       float row_sc = sc;                     // 8-bit: with the inverse of the queries' shift
-      if (n > 0 && ok) {
+      if (n > 0) {
         // Q, swizzled as the copies would: rows of 128 bytes, piece c at c ^ (row & 7).
         // A half-warp a row, so that a row's 256 bytes are one request.
         {
           const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-          const int seq0 = u.seq0, in0 = u.in0, rows = u.rows, head0 = u.g * a.G;
+          const int seq0 = u.seq0, in0 = u.in0, head0 = u.g * a.G;
           uint4 w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int rr = first + r_warp + 2 * i + r_half;
+            const int rr = first + ((r_warp + 2 * i + r_half) & (span - 1));
             w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < rows && a.scale_log2 != 0.f) {
+            if (rr < unit_rows && a.scale_log2 != 0.f) {
               const int sq = ((in0 + rr) * a.inv_g) >> 16, h = in0 + rr - sq * a.G;
               w[i] = *reinterpret_cast<const uint4*>(
                   a.q + ((int64_t)(seq0 + sq) * a.Hq + head0 + h) * kD + 8 * piece);
@@ -301,8 +310,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             auto columns = [&](int c) {  // 32 c ..., masked
               float(&y)[32] = reinterpret_cast<float(&)[32]>(s[Q8 ? 0 : 32 * c]);
               if (Q8) load_cols(s_at + 32 * c, y);
-              if (__builtin_expect(k0 + kTile > P, 0)) {
-                const uint32_t on = below(P - k0 - 32 * c);
+              if (__builtin_expect(k0 + kTile > P || copies > 1, 0)) {
+                const uint32_t on = mine_is(c) ? below(P - k0 - 32 * c) : 0u;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (!(on & (1u << i))) y[i] = -INFINITY;
@@ -320,6 +329,12 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               float sum = 0.f;
 #pragma unroll
               for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                if (copies > 1 && !mine_is(c)) {  // another copy's
+                  const uint32_t none[16] = {};
+                  store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, none);
+                  if (PARTS == 2) store_cols(s_at + 32 * c + 16, none);
+                  continue;
+                }
                 if (Q8) columns(c);
                 const float* y = s + (Q8 ? 0 : 32 * c);
                 uint32_t w[16], w2[16];
@@ -364,6 +379,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               float top = -INFINITY;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
+                if (copies > 1 && !mine_is(c)) continue;
                 columns(c);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -440,11 +456,57 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           }
         }
         if (ok) ok = wait(&bar.o[x], segs & 1);
-        if (ok && warp_live) {
-          fence_after();
-          put();
-          fence_before();
+        fence_after();
+        if (copies == 1) {
+          if (ok && warp_live) put();
+        } else {
+          // The copies by turns, each adding its rows to the sums so far (in the queries'
+          // tile, which the products have read); the last one writes them out.  Every warp
+          // of the stream passes all barriers, whatever has gone wrong.
+          float4* so_far = reinterpret_cast<float4*>(smem_raw + (q_mine - smem_u32(smem_raw))) + row;
+          float4* total = reinterpret_cast<float4*>(mine) + row;
+          if (!ok) l = nanf("");
+#pragma unroll 1
+          for (int k = 0; k < copies; ++k) {
+            if (k == copy && warp_live) {
+              const float2 was = k > 0 && live ? run_s[x][row] : make_float2(-INFINITY, 0.f);
+              const float top = fmaxf(m, was.x);
+              auto under_top = [&](float y) { return y == top ? 1.f : ex2(Q8 ? y - top : (y - top) * sc); };
+              const float f = under_top(m), f_was = under_top(was.x), f_more = under_top(under);
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float o[32] = {};
+                if (ok) load_cols(o_at + 32 * c, o);
+                if (live) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    float4 y = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f,
+                                           o[4 * i + 3] * f);
+                    if (more) {
+                      const float4 u = __ldcg(sums + (8 * c + i) * rs);
+                      y = make_float4(fmaf(u.x, f_more, y.x), fmaf(u.y, f_more, y.y),
+                                      fmaf(u.z, f_more, y.z), fmaf(u.w, f_more, y.w));
+                    }
+                    if (k > 0) {
+                      const float4 u = so_far[(8 * c + i) * span];
+                      y = make_float4(fmaf(u.x, f_was, y.x), fmaf(u.y, f_was, y.y),
+                                      fmaf(u.z, f_was, y.z), fmaf(u.w, f_was, y.w));
+                    }
+                    if (k < copies - 1)
+                      so_far[(8 * c + i) * span] = y;
+                    else
+                      __stcg(total + (8 * c + i) * rs, y);
+                  }
+                }
+              }
+              l = l * f + was.y * f_was;
+              m = top;
+              if (live) run_s[x][row] = make_float2(m, l);
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+          }
         }
+        fence_before();
         tiles += n;
         ++segs;
       }
@@ -452,10 +514,11 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         l = nanf("");
         m = 0.f;
       }
-      if (live) {
+      if (live && copy == copies - 1) {
         float* stats = mine + (size_t)rs * kD;
-        stats[r] = Q8 ? m : m * sc;
-        stats[rs + r] = l;
+        const int at = both ? r : row;
+        stats[at] = Q8 ? m : m * sc;
+        stats[rs + at] = l;
       }
       seg_tile += all;
     }
@@ -654,10 +717,12 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
    } else if (Q8 && warp >= 12) {
     // ------------------------------------------- codes to operands, scales
     // 16 codes a lane and turn: 16 bytes of a row become two pieces of its half of the
-    // operand.  Lanes of the second half store their pieces in the other order, so that
-    // eight lanes together touch all banks.
+    // operand.  Eight lanes take half of a row and the other half of the next one, so that
+    // together they touch all banks, in the codes as in the operand.
     const uint32_t raw = ring + SLOTS * kSlotBytes;
-    const int mine = tid - 384;
+    const int mine = tid - 384, row0 = mine >> 2;
+    const int ch = (mine & 3) | (row0 & 1) << 2;       // of a row's eight, at even turns
+    const uint32_t at0 = ((2 * (mine & 3)) ^ (row0 & 7)) << 4;  // the first piece's place
     uint32_t tile = 0;
     bool ok = true;
     for (int seg = 0; ok && seg < n_seg; ++seg) {
@@ -696,34 +761,33 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           if (ok && i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
           if (!ok) break;
           const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
+          // (all loads before the first store; rows 8 apart have the same swizzle)
 #pragma unroll
           for (int n0 = 0; n0 < 8; n0 += 4) {
-            uint4 c[4];                      // (all loads before the first store)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
-                           : "r"(from + ((n0 + n) * 128 + mine) * 16)
-                           : "memory");
+            uint4 c[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-              const int row = ((n0 + n) * 128 + mine) >> 3, ch = mine & 7;
-              uint4 x, y;
-              widen<FMT>(c[n].x, x.x, x.y);
-              widen<FMT>(c[n].y, x.z, x.w);
-              widen<FMT>(c[n].z, y.x, y.y);
-              widen<FMT>(c[n].w, y.z, y.w);
-              if (row >= left) x = y = make_uint4(0u, 0u, 0u, 0u);  // behind the shared rows
-              const int swap = ch >> 2, p = 2 * (ch & 3);
-              const uint32_t half = to + swap * kHalf + row * 128;
-              const uint32_t at_x = half + ((p ^ (row & 7)) << 4);
-              const uint32_t at_y = half + (((p + 1) ^ (row & 7)) << 4);
-              const uint4 u = swap ? y : x, v = swap ? x : y;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(swap ? at_y : at_x),
-                           "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+              const int piece = ch ^ ((n0 + n) & 1) << 2;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
+                           : "r"(from + (row0 + (n0 + n) / 2 * 32) * kD + piece * 16)
                            : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(swap ? at_x : at_y),
-                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int row = row0 + (n0 + n) / 2 * 32, piece = ch ^ ((n0 + n) & 1) << 2;
+              uint4 y, z;
+              widen<FMT>(c[n].x, y.x, y.y);
+              widen<FMT>(c[n].y, y.z, y.w);
+              widen<FMT>(c[n].z, z.x, z.y);
+              widen<FMT>(c[n].w, z.z, z.w);
+              if (left < kTile && row >= left) y = z = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t half = to + (piece >> 2) * kHalf + row * 128;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + at0),
+                           "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + (at0 ^ 16)),
+                           "r"(z.x), "r"(z.y), "r"(z.z), "r"(z.w)
                            : "memory");
             }
           }
