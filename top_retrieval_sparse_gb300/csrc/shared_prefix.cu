@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
   const uint32_t tmem = tmem_s;
   // The whole warp agrees, where what follows is a warp's work.
   auto wait = [&](uint64_t* x, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_for(x, parity, &abort_s)) != 0;
+    return __all_sync(0xffffffffu, wait_long(x, parity, &abort_s)) != 0;
   };
   const int n_seg = a.total->count[blockIdx.x];
   const SharedSegment* segments = a.segments + (n_seg > 0 ? a.total->first[blockIdx.x] : 0);
@@ -554,9 +554,9 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         auto number = [&](int j) { return passed + (both ? j : 2 * j + x); };
         if (n > 0) {
           const uint32_t i = 2 * number(0);
-          ok = wait_for(&bar.q[x], segs & 1, &abort_s) &&
-               wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
-          if (both && x == 1) ok = ok && wait_for(&bar.turn[1], turns & 1, &abort_s);
+          ok = wait_long(&bar.q[x], segs & 1, &abort_s) &&
+               wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
+          if (both && x == 1) ok = ok && wait_long(&bar.turn[1], turns & 1, &abort_s);
           if (ok) {
             fence_after();
             qk(slot_of<FMT>(i));
@@ -565,17 +565,17 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         }
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t tile = number(j), i = 2 * tile + 1;  // V's slot
-          ok = wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
+          ok = wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (!Q8 && ok && (j0 + (int)(tile - passed) + 1) * kTile > P)
-            ok = wait_for(&bar.clean[slot_of<FMT>(tile)], lap_of<FMT>(tile), &abort_s);
+            ok = wait_long(&bar.clean[slot_of<FMT>(tile)], lap_of<FMT>(tile), &abort_s);
           const uint64_t vx = vd + slot_of<FMT>(i) * (kSlotBytes >> 4);
           const bool more = j % kFoldEvery<PARTS> > 0;
           const uint32_t parity = (tiles + j) & 1;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            ok = ok && wait_for(&bar.p[x][half], parity, &abort_s);
+            ok = ok && wait_long(&bar.p[x][half], parity, &abort_s);
             if (half == 0 && both)
-              ok = ok && wait_for(&bar.turn[x], (turns + j + x) & 1, &abort_s);
+              ok = ok && wait_long(&bar.turn[x], (turns + j + x) & 1, &abort_s);
             if (ok) {
               fence_after();
 #pragma unroll
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           commit_mma(&bar.empty[slot_of<FMT>(i)]);
           if (j + 1 < n) {
             const uint32_t k = 2 * number(j + 1);
-            ok = wait_for(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
+            ok = wait_long(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
             if (!ok) break;
             qk(slot_of<FMT>(k));
           } else {
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           if (both) mbar_arrive(&bar.turn[x ^ 1]);
         }
         if (both) {  // (A sees B's last arrival, so that neither's count runs ahead)
-          if (x == 0) ok = ok && wait_for(&bar.turn[0], (turns + n) & 1, &abort_s);
+          if (x == 0) ok = ok && wait_long(&bar.turn[0], (turns + n) & 1, &abort_s);
           turns += n + 1;
         }
         tiles += n;
@@ -692,9 +692,9 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         };
         const uint32_t i = 2 * tile;
         if (lane == 0) {
-          ok = wait_for(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
+          ok = wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (ok) give(i);
-          ok = ok && wait_for(&bar.full[slot_of<FMT>(i + 1)], lap_of<FMT>(i + 1), &abort_s);
+          ok = ok && wait_long(&bar.full[slot_of<FMT>(i + 1)], lap_of<FMT>(i + 1), &abort_s);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;

@@ -203,4 +203,19 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 
+// The same for waits that are often long: its limit counts the SM's clocks (2^31, about a
+// second), which are read faster than the global timer.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  } while (!*abort && clock64() - t0 < 1ll << 31);
+  *abort = 1;
+  return false;
+}
+
 }  // namespace tsa
