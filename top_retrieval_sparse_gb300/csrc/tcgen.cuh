@@ -203,16 +203,22 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 
-// The same for waits that are often long: its limit counts the SM's clocks (2^31, about a
-// second), which are read faster than the global timer.
+// The same for waits that are often long: the thread is suspended for up to 20 us a try, so
+// that it takes no issue slots from those that work, and the limit counts the SM's clocks
+// (2^31, about a second), which are read faster than the global timer.
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
 #pragma unroll 1
   do {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
   } while (!*abort && clock64() - t0 < 1ll << 31);
   *abort = 1;
   return false;
