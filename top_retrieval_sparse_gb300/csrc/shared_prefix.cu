@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               const float off = top == -INFINITY ? 0.f : (Q8 ? -top : -top * sc);
               float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               float sum = 0.f;
-#pragma unroll
+#pragma unroll (Q8 ? 1 : 2)
               for (int c = 2 * half; c < 2 * half + 2; ++c) {
                 if (copies > 1 && !mine_is(c)) {  // another copy's
                   const uint32_t none[16] = {};
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             if constexpr (Q8) {
               // fp16's range is short: every logit is looked at before the weights are taken.
               float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 if (copies > 1 && !mine_is(c)) continue;
                 columns(c);
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
                 m = to;
                 l *= f;
                 if (j > j0) {
-#pragma unroll
+#pragma unroll 1
                   for (int c = 0; c < 4; ++c) {
                     float o[32];
                     load_cols(o_at + 32 * c, o);
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           if (!ok) break;
           const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
           // (all loads before the first store; rows 8 apart have the same swizzle)
-#pragma unroll
+#pragma unroll 1
           for (int n0 = 0; n0 < 8; n0 += 4) {
             uint4 c[4];
 #pragma unroll
