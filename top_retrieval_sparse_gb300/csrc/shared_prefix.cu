@@ -27,6 +27,8 @@
 // behind by two laps and a barrier's parity is never taken for another lap's.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "shared_attn.h"
 #include "tcgen.cuh"
 
@@ -286,6 +288,9 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           more = true;
           under = m;
         };
+        // (two forms, so that the usual one's code is in one piece)
+        auto tiles_of = [&](auto many) {
+        constexpr bool MANY = decltype(many)::value;  // copies > 1
         for (int j0 = 0; j0 < n && ok; j0 += kFoldEvery<PARTS>) {
           const int j1 = j0 + kFoldEvery<PARTS> < n ? j0 + kFoldEvery<PARTS> : n;
           for (int j = j0; j < j1; ++j) {
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             auto columns = [&](int c) {  // 32 c ..., masked
               float(&y)[32] = reinterpret_cast<float(&)[32]>(s[Q8 ? 0 : 32 * c]);
               if (Q8) load_cols(s_at + 32 * c, y);
-              if (__builtin_expect(k0 + kTile > P || copies > 1, 0)) {
-                const uint32_t on = mine_is(c) ? below(P - k0 - 32 * c) : 0u;
+              if (__builtin_expect(MANY || k0 + kTile > P, 0)) {
+                const uint32_t on = !MANY || mine_is(c) ? below(P - k0 - 32 * c) : 0u;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (!(on & (1u << i))) y[i] = -INFINITY;
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               float sum = 0.f;
 #pragma unroll (Q8 ? 1 : 2)
               for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                if (copies > 1 && !mine_is(c)) {  // another copy's
+                if (MANY && !mine_is(c)) {  // another copy's
                   const uint32_t none[16] = {};
                   store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, none);
                   if (PARTS == 2) store_cols(s_at + 32 * c + 16, none);
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
               float top = -INFINITY;
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
-                if (copies > 1 && !mine_is(c)) continue;
+                if (MANY && !mine_is(c)) continue;
                 columns(c);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -455,6 +460,11 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             publish(1);
           }
         }
+        };
+        if (copies > 1)
+          tiles_of(std::true_type{});
+        else
+          tiles_of(std::false_type{});
         if (ok) ok = wait(&bar.o[x], segs & 1);
         fence_after();
         if (copies == 1) {
