@@ -87,11 +87,20 @@ CASES = [  # Hq, Hkv, cap, page, lens, cu, shared
      [99 - 3 * (i % 30) for i in range(30)])]
 
 
+def roomy(B, Hkv, cap, page, row_bytes):
+    """A capacity past the 64 MiB up to which shared rows are read for every sequence."""
+    unit = max(page, 128)
+    need = (64 << 20) // (B * Hkv * row_bytes) + 1
+    return max(cap, -(-need // unit) * unit)
+
+
+@pytest.mark.parametrize("room", [False, True], ids=["small", "large"])
 @pytest.mark.parametrize("out16", [False, True], ids=["fp32", "bf16"])
 @pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
-def test_shared_attn_decode(tsa, case, out16):
+def test_shared_attn_decode(tsa, case, out16, room):
     Hq, Hkv, cap, page, lens, cu, shared = case
     B = len(lens)
+    cap = roomy(B, Hkv, cap, page, 512) if room else cap
     g = gen(cap + B)
     q = randn(g, B, Hq, D).bfloat16()
     kv, rows = bf16_cache(tsa, g, B, Hkv, cap, page)
@@ -114,14 +123,16 @@ def test_shared_attn_decode(tsa, case, out16):
         assert torch.equal(out, tsa.shared_attn_decode(*args)[0])
 
 
+@pytest.mark.parametrize("room", [False, True], ids=["small", "large"])
 @pytest.mark.parametrize("fmt,block", [("int8", 16), ("int8", 64), ("e4m3", 32), ("e4m3", 128)])
 @pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
-def test_kv8_shared_attn_decode(tsa, case, fmt, block):
+def test_kv8_shared_attn_decode(tsa, case, fmt, block, room):
     Hq, Hkv, cap, page, lens, cu, shared = case
     B = len(lens)
     if page and block > page:
         block = page
     cap = -(-cap // 128) * 128 if page == 0 else cap
+    cap = roomy(B, Hkv, cap, page, 256) if room else cap
     g = gen(cap + B + block)
     q = randn(g, B, Hq, D).bfloat16()
     cache, rows = quant_cache(tsa, g, B, Hkv, cap, block, fmt, page)
@@ -139,11 +150,12 @@ def test_kv8_shared_attn_decode(tsa, case, fmt, block):
     assert tsa.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("cap", [1024, 4096], ids=["small", "large"])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
-def test_other_scales(tsa, scale):
+def test_other_scales(tsa, scale, cap):
     """Logits of hundreds, of both signs, and none at all."""
     g = gen(11)
-    B, Hq, Hkv, cap = 20, 8, 2, 1024
+    B, Hq, Hkv = 20, 8, 2
     lens, cu, shared = [600 + 9 * i for i in range(20)], [0, 20], [555]
     q = randn(g, B, Hq, D).bfloat16()
     kv, rows = bf16_cache(tsa, g, B, Hkv, cap, 64)
@@ -153,13 +165,14 @@ def test_other_scales(tsa, scale):
           scale=scale)
 
 
-def test_a_maximum_that_rises_with_every_row(tsa):
+@pytest.mark.parametrize("cap", [2048, 16384], ids=["small", "large"])
+def test_a_maximum_that_rises_with_every_row(tsa, cap):
     """Keys whose logits grow by 1 every 8 rows: the weights' maximum is raised many times,
     and most weight lies in the last shared rows, or the own ones."""
     g = gen(12)
-    B, Hq, Hkv, cap = 9, 8, 1, 2048
+    B, Hq, Hkv = 9, 8, 1
     q = torch.ones((B, Hq, D), device=DEV).bfloat16()
-    k = (torch.arange(cap, device=DEV) / 8.0)[:, None].expand(cap, D) / D
+    k = (torch.arange(cap, device=DEV).clamp(max=2047) / 8.0)[:, None].expand(cap, D) / D
     k = k.expand(B, 1, cap, D).contiguous().bfloat16()
     v = randn(g, B, Hkv, cap, D).bfloat16()
     kv = tsa.kv_contiguous(k, v)
@@ -190,11 +203,12 @@ def test_values_of_one_sign_over_long_shared_rows(tsa, out16):
           only=[0, 1, 7, 16, 23])
 
 
-def test_invisible_rows_and_pages_do_not_matter(tsa):
+@pytest.mark.parametrize("cap", [512, 12288], ids=["small", "large"])
+def test_invisible_rows_and_pages_do_not_matter(tsa, cap):
     """NaN behind every length and in the members' unread copies of shared rows; page table
     entries of nothing visible are not looked up."""
     g = gen(14)
-    Hq, Hkv, cap, page = 8, 2, 512, 32
+    Hq, Hkv, page = 8, 2, 32
     lens, cu, shared = [200, 150, 130, 400, 300, 0], [0, 3, 5], [129, 299]
     B = len(lens)
     kv, rows = bf16_cache(tsa, g, B, Hkv, cap, page)
@@ -204,7 +218,7 @@ def test_invisible_rows_and_pages_do_not_matter(tsa):
     dirty = torch.ones(kv.k.shape[0], page, dtype=torch.bool, device=DEV)
     for b, (n, first) in enumerate(members(B, cu)):
         P = shared[n] if n >= 0 else 0
-        for i in range(cap):
+        for i in range(512):
             if (b == first and i < max(P, lens[b])) or (P <= i < lens[b]):
                 dirty[pt[b, i // page].long(), i % page] = False
     for t in (kv.k, kv.v):
@@ -221,7 +235,8 @@ def test_invisible_rows_and_pages_do_not_matter(tsa):
     assert torch.equal(got, want) and tsa.workspace_status(ws) == 0
 
 
-def test_bad_input_is_flagged(tsa):
+@pytest.mark.parametrize("cap", [256, 20480], ids=["small", "large"])
+def test_bad_input_is_flagged(tsa, cap):
     def status(ws):
         return int(tsa.lib().tsa_workspace_status(ws.data_ptr(), 1, None))
 
@@ -231,7 +246,7 @@ def test_bad_input_is_flagged(tsa):
         return torch.allclose(a, b, rtol=0, atol=1e-4)
 
     g = gen(15)
-    Hq, Hkv, cap, page = 4, 2, 256, 16
+    Hq, Hkv, page = 4, 2, 16
     lens, cu, shared = [200, 150, 90, 100], [0, 2, 4], [100, 80]
     kv, rows = bf16_cache(tsa, g, 4, Hkv, cap, page)
     q = randn(g, 4, Hq, D).bfloat16()
@@ -252,12 +267,12 @@ def test_bad_input_is_flagged(tsa):
     assert s != 0 and nan == [False, True, False, False] and same(out[2:], good[2:])
     s, nan, out = run(lens=[200, 0, 90, 100])             # an empty place is none of these
     assert s == 0 and not any(nan) and (out[1] == 0).all() and same(out[0], good[0])
-    s, nan, out = run(shared=[100, 257])                  # past the cache
+    s, nan, out = run(shared=[100, cap + 1])                  # past the cache
     assert s != 0 and nan == [False, False, True, True]
     s, nan, out = run(shared=[-1, 80])                    # clamped to 0
     assert s != 0 and not any(nan) and same(out[2:], good[2:])
-    s, nan, out = run(lens=[200, 150, 90, 300])           # clamped to the cache
-    assert s != 0 and not any(nan) and same(out[:3], good[:3])
+    s, nan, out = run(lens=[200, 150, 90, cap + 44])           # clamped to the cache
+    assert s != 0 and not nan[0] and not nan[1] and not nan[2] and same(out[:3], good[:3])
     for bad in ([0, 3, 2], [0, 2, 5], [-1, 2, 4], [4, 0, 4]):
         s, nan, out = run(cu=bad)
         assert s != 0 and all(nan)
@@ -282,12 +297,13 @@ def test_without_groups_it_is_the_plain_step(tsa):
         check(q, lambda b, h: (rows(kv.k, b, h), rows(kv.v, b, h)), lens, cu, shared, Hkv, out, lse)
 
 
-def test_the_largest_batch(tsa):
+@pytest.mark.parametrize("per", [2, 4], ids=["small", "large"])
+def test_the_largest_batch(tsa, per):
     """4096 sequences in 512 groups of one page each."""
     g = gen(17)
     B, Hq, Hkv, ps = 4096, 4, 1, 16
-    pt = torch.randperm(B * 2, generator=g, device=DEV).view(B, 2).int().contiguous()
-    k, v = (randn(g, B * 2, Hkv, ps, D).bfloat16() for _ in range(2))
+    pt = torch.randperm(B * per, generator=g, device=DEV).view(B, per).int().contiguous()
+    k, v = (randn(g, B * per, Hkv, ps, D).bfloat16() for _ in range(2))
     kv = tsa.kv_paged(k, v, pt)
     cu = list(range(0, B + 1, 8))
     shared = [n % 17 for n in range(512)]
@@ -295,15 +311,16 @@ def test_the_largest_batch(tsa):
     q = randn(g, B, Hq, D).bfloat16()
     lse = torch.empty((B, Hq), device=DEV)
     out, _ = tsa.shared_attn_decode(q, kv, i32(lens), i32(cu), i32(shared), lse_out=lse)
-    flat = [t[pt.long()].reshape(B, 2 * ps, D) for t in (k, v)]
+    flat = [t[pt.long()].reshape(B, per * ps, D) for t in (k, v)]
     check(q, lambda b, h: (flat[0][b], flat[1][b]), lens, cu, shared, Hkv, out, lse,
           only=set(range(0, B, 37)) | set(range(130)) | set(range(B - 20, B)))
 
 
-def test_streams_graphs_and_calls_of_all_sizes_share_a_workspace(tsa):
+@pytest.mark.parametrize("cap", [2048, 12288], ids=["small", "large"])
+def test_streams_graphs_and_calls_of_all_sizes_share_a_workspace(tsa, cap):
     g = gen(18)
-    Hq, Hkv, cap = 16, 4, 2048
-    kv, _ = bf16_cache(tsa, g, 40, Hkv, cap, 64)
+    Hq, Hkv = 16, 4
+    kv, _ = bf16_cache(tsa, g, 40, Hkv, cap, 64)     # (small: 3 sequences' rows)
     cache, _ = quant_cache(tsa, g, 40, Hkv, cap, 32, "int8", 64)
     q = randn(g, 40, Hq, D).bfloat16()
     small = (q[:3], kv, i32([1500, 1400, 1300]), i32([0, 3]), i32([1299]))

@@ -330,7 +330,7 @@ int decode_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
 // Workspace of a step with shared rows.  Nothing but the status word outlasts a call, so
 // that calls of whatever sizes may share it.
 struct SharedLayout {
-  size_t partial, arrived, rows, total_at, groups, segments, own, parts, total;
+  size_t partial, arrived, rows, total_at, groups, segments, spans, own, parts, total;
 };
 SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   SharedLayout l{};
@@ -342,17 +342,22 @@ SharedLayout shared_layout(int B, int N, int Hq, int Hkv) {
   l.partial = kDecodePartial;
   l.arrived = kDecodeArrived;
   l.rows = l.arrived + round_up((size_t)B * Hkv * sizeof(uint32_t));
-  l.total_at = l.rows + 2 * round_up((size_t)B * sizeof(int32_t));
+  l.total_at = l.rows + 3 * round_up((size_t)B * sizeof(int32_t));
   l.groups = l.total_at + round_up(sizeof(SharedTotal));
   l.segments = l.groups + round_up((size_t)N * sizeof(SharedGroup));
   // (a unit has 256 queries, or is its group and head's last)
   const size_t list = kSharedShares + (size_t)B * Hq / kUnitRows + (size_t)Hkv * (N < B ? N : B);
-  l.own = l.segments + round_up(list * sizeof(SharedSegment));
+  l.spans = l.segments + round_up(list * sizeof(SharedSegment));
+  l.own = l.spans + round_up(list * sizeof(int2));
   l.parts = l.own + row;
   l.total = l.parts +
             round_up((size_t)(kSharedShares * kShareRows + units) * (kD + 2) * sizeof(float));
   return l;
 }
+
+// Bytes of keys and values up to which reading the shared rows for every sequence costs less
+// than the three kernels that read them once.
+constexpr int64_t kSmallCache = (int64_t)64 << 20;
 
 // Both entry points of a step with shared rows after their cache's checks.
 int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, int B,
@@ -398,6 +403,7 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   s.total = reinterpret_cast<SharedTotal*>(ws + l.total_at);
   s.groups = reinterpret_cast<SharedGroup*>(ws + l.groups);
   s.segments = reinterpret_cast<SharedSegment*>(ws + l.segments);
+  s.spans = reinterpret_cast<int2*>(ws + l.spans);
   s.own_out = reinterpret_cast<float*>(ws + l.own);
   s.own_lse = s.own_out + rows * kD;
   s.parts = reinterpret_cast<float*>(ws + l.parts);
@@ -411,10 +417,23 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   a.status = s.status;
   a.partial = reinterpret_cast<float*>(ws + l.partial);
   a.arrived = s.arrived;
-  const int grid = decode_grid((int64_t)B * Hkv, c.l_cap, fmt);
+  const int grid = decode_grid((int64_t)B * Hkv, c.l_cap + 16, fmt);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap kmap, vmap;
   const bool codes = fmt != kFmtBf16;
+  a.lens = lens;
+  a.start = s.start;
+  // A small cache: every sequence reads the shared rows for itself, mostly from L2.
+  if ((int64_t)B * Hkv * c.l_cap * 2 * (codes ? kD : kRowBytes) <= kSmallCache) {
+    s.leader = reinterpret_cast<int32_t*>(ws + l.rows + 2 * ints);
+    a.leader = s.leader;
+    a.group = s.group;
+    a.out = static_cast<float*>(out);
+    a.out16 = out16;
+    a.lse = lse_out;
+    if ((rc = launched(launch_shared_prep(s, st), "groups launch"))) return rc;
+    return launched(launch_attn_decode(a, fmt, grid, st), "attention launch");
+  }
+  CUtensorMap kmap, vmap;
   if (N > 0) {
     const int64_t all = c.page_table ? (codes ? pool * Hkv : 0x7fffffff) : (int64_t)B * Hkv * c.l_cap;
     if ((rc = row_map(c.k, all, s.box, &kmap, codes)) ||
@@ -425,8 +444,6 @@ int shared_run(const void* q, const CacheView& c, int fmt, const int32_t* lens, 
   if (N > 0 &&
       (rc = launched(launch_shared_prefix(kmap, vmap, s, fmt, st), "attention launch")))
     return rc;
-  a.lens = lens;
-  a.start = s.start;
   a.out = s.own_out;
   a.lse = s.own_lse;
   if ((rc = launched(launch_attn_decode(a, fmt, grid, st), "attention launch"))) return rc;

@@ -163,15 +163,15 @@ __device__ __forceinline__ Visible visible(const DecodeArgs& a, int b) {
   Visible v;
   const int len = a.lens[b], cap = (int)a.c.l_cap;
   v.L = len < 0 ? 0 : (len > cap ? cap : len);
-  if (SHARED) {
-    v.n0 = 0;
+  if (SHARED) {  // the shared rows, then the own ones: two ranges, which may share a slab
     v.lo = a.start[b];
+    v.n0 = !a.leader ? 0 : (v.lo < v.L ? v.lo : v.L);
   } else {
     v.n0 = a.n_init < v.L ? (int)a.n_init : v.L;
     v.lo = a.n_recent < v.L ? v.L - (int)a.n_recent : 0;
   }
   v.s0 = (int)(((uint32_t)v.n0 + 15) >> 4);
-  v.sw = v.lo >> 4 > v.s0 ? v.lo >> 4 : v.s0;
+  v.sw = v.lo >> 4 > v.s0 || SHARED ? v.lo >> 4 : v.s0;
   const int se = (int)(((uint32_t)v.L + 15) >> 4);
   v.n = v.s0 + (v.lo < v.L && se > v.sw ? se - v.sw : 0);
   return v;
@@ -182,12 +182,18 @@ __device__ __forceinline__ float* slot_of(const DecodeArgs& a, int share, int wh
   return a.partial + (size_t)(2 * share + which) * kDecodeSlot;
 }
 
+template <bool SHARED>
 __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, int lane, float4 o,
                                         float m, float l) {
+  if (SHARED && a.group && a.group[b] == kNoGroups) l = nanf("");
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
   const int64_t at = (int64_t)b * a.Hq + head;
-  *reinterpret_cast<float4*>(a.out + at * kD + 4 * lane) =
-      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (SHARED && a.out16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * kD + 4 * lane) =
+        make_uint2(pack2<kFmtBf16>(o.x, o.y), pack2<kFmtBf16>(o.z, o.w));
+  else
+    *reinterpret_cast<float4*>(a.out + at * kD + 4 * lane) = o;
   if (a.lse && lane == 0) {
     // m carries a value scale and l its inverse (2^60 at most), so the exponents are
     // added first: log2(l) as one number would be off by up to 2^-18.
@@ -241,9 +247,15 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
       if (blockIdx.x == 0 && v.L != a.lens[b]) atomicOr(a.status, kStatusBadLength);
       if (n == 0 && b % gridDim.x == blockIdx.x)  // nothing visible
         for (int h = 0; h < a.Hq; ++h) {
+          const float none = SHARED && a.group && a.group[b] == kNoGroups ? nanf("") : 0.f;
           float* o = a.out + ((int64_t)b * a.Hq + h) * kD;
-          for (int j = 0; j < kD; ++j) o[j] = 0.f;
-          if (a.lse) a.lse[(int64_t)b * a.Hq + h] = -INFINITY;
+          if (SHARED && a.out16) {
+            uint16_t* o16 = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)b * a.Hq + h) * kD;
+            for (int j = 0; j < kD; ++j) o16[j] = none == 0.f ? 0 : 0x7fff;
+          } else {
+            for (int j = 0; j < kD; ++j) o[j] = none;
+          }
+          if (a.lse) a.lse[(int64_t)b * a.Hq + h] = none == 0.f ? -INFINITY : none;
         }
     }
     int64_t x = n;
@@ -346,6 +358,11 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     int32_t page[NS] = {};
     const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
     const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
+    // (the shared rows': in another sequence's cache)
+    const int lead = SHARED && a.leader ? a.leader[b] : b;
+    const int32_t* pages0 =
+        SHARED && a.c.page_table ? a.c.page_table + (int64_t)lead * a.c.max_pages : nullptr;
+    const uint32_t unit_row0 = (uint32_t)(((int64_t)lead * Hkv + g) * a.c.l_cap);
     const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
     const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
 
@@ -359,7 +376,8 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     auto want_pages = [&](int k) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        if (pages && k + s < k1) page[s] = pages[first_row(k + s) >> a.c.page_shift];
+        if (pages && k + s < k1)
+          page[s] = (SHARED && k + s < vis.s0 ? pages0 : pages)[first_row(k + s) >> a.c.page_shift];
     };
     auto find_rows = [&](int k) {
 #pragma unroll
@@ -370,10 +388,13 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
                                  k + s >= k1, 0)) {
           seen[s] = 0u;
           if (k + s < k1)
-            for (int j = 0; j < 16; ++j)
-              if ((j < vis.n0 - i || j >= vis.lo - i) && j < vis.L - i) seen[s] |= 1u << j;
+            for (int j = 0; j < 16; ++j) {
+              const bool sees = SHARED ? (k + s < vis.s0 ? j < vis.n0 - i : j >= vis.lo - i)
+                                       : j < vis.n0 - i || j >= vis.lo - i;
+              if (sees && j < vis.L - i) seen[s] |= 1u << j;
+            }
         }
-        row[s] = unit_row + (uint32_t)i;
+        row[s] = (SHARED && k + s < vis.s0 ? unit_row0 : unit_row) + (uint32_t)i;
         if (pages) {
           row[s] = (((uint32_t)page[s] * (uint32_t)Hkv + (uint32_t)g) << a.c.page_shift) +
                    ((uint32_t)i & ((1u << a.c.page_shift) - 1u));
@@ -635,7 +656,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
         o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
       }
       if (all) {
-        put_row(a, b, g * G + h, lane, o, m, l);
+        put_row<SHARED>(a, b, g * G + h, lane, o, m, l);
       } else {
         if (lane == 0) {
           slot[h] = m;
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
             }
           }
           l = warp_sum(l);
-          put_row(a, b, g * G + h, lane, o, m, l);
+          put_row<SHARED>(a, b, g * G + h, lane, o, m, l);
         }
         if (tid == 0) *ctr = 0u;  // ready for the next call
       }

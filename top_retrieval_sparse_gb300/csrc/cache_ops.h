@@ -128,6 +128,7 @@ struct ReadArgs {
 cudaError_t launch_kv8_read(const ReadArgs& a, cudaStream_t st);
 
 // One decode step (attn_decode.cu).
+constexpr int kNoGroups = -2;
 constexpr int kDecodeThreads = 128;
 constexpr int kDecodeShares = 4 * 152;                      // most CTAs of a call
 constexpr int kDecodeSlot = 2 * kMaxGroup + kMaxGroup * kD; // floats of a partial
@@ -143,8 +144,13 @@ struct DecodeArgs {
   int* status;
   float* partial;          // [2 * kDecodeShares][kDecodeSlot]
   uint32_t* arrived;       // [B * Hkv], zero between calls
-  // Of a batch that shares rows (else nullptr): sequence b sees rows [start[b], lens[b]).
+  // Of a batch that shares rows (else nullptr): sequence b sees rows [start[b], lens[b]) of its
+  // cache and, with `leader`, rows [0, start[b]) of sequence leader[b]'s; its output is NaN
+  // where group[b] is kNoGroups, and bf16 with out16.
   const int32_t* start;
+  const int32_t* leader;
+  const int32_t* group;
+  int out16;
 };
 int attn_decode_ctas(int fmt);  // resident CTAs of an SM
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st);

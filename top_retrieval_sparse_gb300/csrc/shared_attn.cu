@@ -85,6 +85,8 @@ __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share)
       x.part = segment_part(u, share, x.j0 == 0);
       const int number = share + s.unit0 + u.t * Hkv + u.g;
       if (count == 0) a.total->first[share] = number;
+      if (x.j0 == 0) a.spans[number - share].x = share;
+      if (x.j1 == u.tiles) a.spans[number - share].y = share;
       a.segments[number] = x;
       ++count;
     }
@@ -166,7 +168,8 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
     a.total->cost = total.cost;
     a.total->shares = total.shares;
   }
-  for (int share = tid; share < kSharedShares; share += kPrepThreads) list_share(a, total, share);
+  if (!a.leader)
+    for (int share = tid; share < kSharedShares; share += kPrepThreads) list_share(a, total, share);
   for (int b = tid; b < B; b += kPrepThreads) {
     int n = -1, start = 0;
     if (bad) {
@@ -180,11 +183,16 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
       n = lo;
       const int P = a.shared[n], L = a.lens[b];
       start = P < 0 ? 0 : (P > a.c.l_cap ? (int)a.c.l_cap : P);
-      if (L > 0 && L < start) atomicOr(a.status, kStatusBadLength);
-      if (L < start) start = 0;  // nothing of the group's (the join knows)
+      if (a.leader) a.leader[b] = cu_s[n];
+      if (L > 0 && L < P) {
+        atomicOr(a.status, kStatusBadLength);
+        n = kNoGroups;
+      }
+      if (L < start) start = 0;
     }
     a.group[b] = n;
     a.start[b] = start;
+    if (a.leader && n < 0) a.leader[b] = b;
   }
 }
 
@@ -213,19 +221,15 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a)
     float m = -INFINITY, l = 0.f;
     int parts = 0, rs = 0;
     bool nan = n == kNoGroups;
-    const int P = n >= 0 ? a.shared[n] : 0;
-    if (P > 0 && L > 0) {
-      nan |= L < P;
-if (!nan) {
-        const SharedGroup s = a.groups[n];
-        const SharedTotal t = *a.total;
+    if (n >= 0 && L > 0) {
+      const SharedGroup s = a.groups[n];
+      if (s.rows > 0) {
         const int r0 = (b - s.b0) * G + h, column = r0 / kUnitRows, r = r0 - column * kUnitRows;
+        const int2 shares = a.spans[s.unit0 + column * Hkv + g];
         const SharedUnit u = unit_of(s, Hkv, column, g);
         const bool both = u.both();
-        const int half = (int)(half_floats(u.rs) / 4);
-        const int s0 = (int)(u.cost0 * t.shares / t.cost);
-        const int s1 = (int)((u.cost0 + (int64_t)(u.tiles - 1) * u.w) * t.shares / t.cost);
-        parts = (s1 - s0 + 1) * (both ? 1 : 2);
+        const int half = (int)(half_floats(u.rs) / 4), s0 = shares.x;
+        parts = (shares.y - s0 + 1) * (both ? 1 : 2);
         rs = u.rs;
         float l_all = 0.f;
         for (int e = lane; e < parts; e += 32) {

@@ -11,7 +11,6 @@ constexpr int kSharedShares = 152;  // CTAs of the prefix kernel: one an SM
 // Cost of a key tile with two query tiles and with one (the products bound the former, the
 // rows' bytes the latter).
 constexpr int kCostBoth = 4, kCostAlone = 3;
-constexpr int kNoGroups = -2;
 
 // A group, as the first kernel finds it.
 struct SharedGroup {
@@ -54,11 +53,13 @@ struct SharedArgs {
   float* lse;              // [B][Hq] or nullptr
   int* status;
   // in the workspace
-  int32_t* group;          // [B]: a sequence's group, -1: none, kNoGroups: bad offsets
+  int32_t* group;          // [B]: a sequence's group, -1: none, kNoGroups: its output is NaN
   int32_t* start;          // [B]: its rows before this one are the group's
+  int32_t* leader;         // [B]: the sequence whose cache has them (small caches, else nullptr)
   SharedGroup* groups;     // [N]
   SharedTotal* total;
   SharedSegment* segments; // share after share; number: the share's, plus that of the unit
+  int2* spans;             // [units]: a unit's first and last share
   float* own_out;          // [B][Hq][128]: over its own rows
   float* own_lse;          // [B][Hq]
   uint32_t* arrived;       // counters of the decode kernel
