@@ -154,24 +154,28 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// Which rows a call sees: sinks and window, or, where sequences share their first rows, the
+// own ones behind them, or both.
+enum { kWindow = 0, kOwn = 1, kBoth = 2 };
+
 // The visible rows of one sequence as a list of slabs: [0, s0), then from sw.
 struct Visible {
   int L, n0, lo, s0, sw, n;
 };
-template <bool SHARED>
+template <int ROWS>
 __device__ __forceinline__ Visible visible(const DecodeArgs& a, int b) {
   Visible v;
   const int len = a.lens[b], cap = (int)a.c.l_cap;
   v.L = len < 0 ? 0 : (len > cap ? cap : len);
-  if (SHARED) {  // the shared rows, then the own ones: two ranges, which may share a slab
+  if (ROWS != kWindow) {  // (both: two ranges, which may share a slab)
     v.lo = a.start[b];
-    v.n0 = !a.leader ? 0 : (v.lo < v.L ? v.lo : v.L);
+    v.n0 = ROWS == kOwn ? 0 : (v.lo < v.L ? v.lo : v.L);
   } else {
     v.n0 = a.n_init < v.L ? (int)a.n_init : v.L;
     v.lo = a.n_recent < v.L ? v.L - (int)a.n_recent : 0;
   }
   v.s0 = (int)(((uint32_t)v.n0 + 15) >> 4);
-  v.sw = v.lo >> 4 > v.s0 || SHARED ? v.lo >> 4 : v.s0;
+  v.sw = v.lo >> 4 > v.s0 || ROWS == kBoth ? v.lo >> 4 : v.s0;
   const int se = (int)(((uint32_t)v.L + 15) >> 4);
   v.n = v.s0 + (v.lo < v.L && se > v.sw ? se - v.sw : 0);
   return v;
@@ -182,14 +186,14 @@ __device__ __forceinline__ float* slot_of(const DecodeArgs& a, int share, int wh
   return a.partial + (size_t)(2 * share + which) * kDecodeSlot;
 }
 
-template <bool SHARED>
+template <int ROWS>
 __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, int lane, float4 o,
                                         float m, float l) {
-  if (SHARED && a.group && a.group[b] == kNoGroups) l = nanf("");
+  if (ROWS == kBoth && a.group[b] == kNoGroups) l = nanf("");
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
   const int64_t at = (int64_t)b * a.Hq + head;
   o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (SHARED && a.out16)
+  if (ROWS == kBoth && a.out16)
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * kD + 4 * lane) =
         make_uint2(pack2<kFmtBf16>(o.x, o.y), pack2<kFmtBf16>(o.z, o.w));
   else
@@ -213,7 +217,7 @@ __device__ __forceinline__ void put_row(const DecodeArgs& a, int b, int head, in
 __host__ __device__ constexpr int slabs_of(int fmt) { return fmt == kFmtE4m3 ? 2 : 1; }
 __host__ __device__ constexpr int ctas_of(int fmt) { return fmt == kFmtInt8 ? 4 : 3; }
 
-template <int FMT, bool SHARED>
+template <int FMT, int ROWS>
 __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kernel(DecodeArgs a) {
   constexpr bool B16 = FMT == kFmtBf16;
   constexpr int NS = slabs_of(FMT);      // slabs a warp works on at once
@@ -242,14 +246,14 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     const int b = b0 + me;
     int64_t n = 0;
     if (b < a.B) {
-      const Visible v = visible<SHARED>(a, b);
+      const Visible v = visible<ROWS>(a, b);
       n = (int64_t)v.n * Hkv;
       if (blockIdx.x == 0 && v.L != a.lens[b]) atomicOr(a.status, kStatusBadLength);
       if (n == 0 && b % gridDim.x == blockIdx.x)  // nothing visible
         for (int h = 0; h < a.Hq; ++h) {
-          const float none = SHARED && a.group && a.group[b] == kNoGroups ? nanf("") : 0.f;
+          const float none = ROWS == kBoth && a.group[b] == kNoGroups ? nanf("") : 0.f;
           float* o = a.out + ((int64_t)b * a.Hq + h) * kD;
-          if (SHARED && a.out16) {
+          if (ROWS == kBoth && a.out16) {
             uint16_t* o16 = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)b * a.Hq + h) * kD;
             for (int j = 0; j < kD; ++j) o16[j] = none == 0.f ? 0 : 0x7fff;
           } else {
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   bool first = true;
   while (at < end) {
     while (prefix[b + 1] <= at) ++b;
-    const Visible vis = visible<SHARED>(a, b);
+    const Visible vis = visible<ROWS>(a, b);
     const int g = (int)quotient(at - prefix[b], vis.n);
     // the unit in the list, and the slabs of it that are this share's
     const int64_t u0 = prefix[b] + (int64_t)g * vis.n, u1 = u0 + vis.n;
@@ -359,9 +363,9 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
     const int32_t* pages = a.c.page_table ? a.c.page_table + (int64_t)b * a.c.max_pages : nullptr;
     const uint32_t unit_row = (uint32_t)(((int64_t)b * Hkv + g) * a.c.l_cap);
     // (the shared rows': in another sequence's cache)
-    const int lead = SHARED && a.leader ? a.leader[b] : b;
+    const int lead = ROWS == kBoth ? a.leader[b] : b;
     const int32_t* pages0 =
-        SHARED && a.c.page_table ? a.c.page_table + (int64_t)lead * a.c.max_pages : nullptr;
+        ROWS == kBoth && a.c.page_table ? a.c.page_table + (int64_t)lead * a.c.max_pages : nullptr;
     const uint32_t unit_row0 = (uint32_t)(((int64_t)lead * Hkv + g) * a.c.l_cap);
     const uint8_t* k_lane = a.c.k + gr * ROW + 16 * tq;
     const uint8_t* v_lane = a.c.v + 2 * tq * ROW + 16 * VW * gr;
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
 #pragma unroll
       for (int s = 0; s < NS; ++s)
         if (pages && k + s < k1)
-          page[s] = (SHARED && k + s < vis.s0 ? pages0 : pages)[first_row(k + s) >> a.c.page_shift];
+          page[s] = (ROWS == kBoth && k + s < vis.s0 ? pages0 : pages)[first_row(k + s) >> a.c.page_shift];
     };
     auto find_rows = [&](int k) {
 #pragma unroll
@@ -389,12 +393,12 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
           seen[s] = 0u;
           if (k + s < k1)
             for (int j = 0; j < 16; ++j) {
-              const bool sees = SHARED ? (k + s < vis.s0 ? j < vis.n0 - i : j >= vis.lo - i)
+              const bool sees = ROWS == kBoth ? (k + s < vis.s0 ? j < vis.n0 - i : j >= vis.lo - i)
                                        : j < vis.n0 - i || j >= vis.lo - i;
               if (sees && j < vis.L - i) seen[s] |= 1u << j;
             }
         }
-        row[s] = (SHARED && k + s < vis.s0 ? unit_row0 : unit_row) + (uint32_t)i;
+        row[s] = (ROWS == kBoth && k + s < vis.s0 ? unit_row0 : unit_row) + (uint32_t)i;
         if (pages) {
           row[s] = (((uint32_t)page[s] * (uint32_t)Hkv + (uint32_t)g) << a.c.page_shift) +
                    ((uint32_t)i & ((1u << a.c.page_shift) - 1u));
@@ -656,7 +660,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
         o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
       }
       if (all) {
-        put_row<SHARED>(a, b, g * G + h, lane, o, m, l);
+        put_row<ROWS>(a, b, g * G + h, lane, o, m, l);
       } else {
         if (lane == 0) {
           slot[h] = m;
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
             }
           }
           l = warp_sum(l);
-          put_row<SHARED>(a, b, g * G + h, lane, o, m, l);
+          put_row<ROWS>(a, b, g * G + h, lane, o, m, l);
         }
         if (tid == 0) *ctr = 0u;  // ready for the next call
       }
@@ -713,6 +717,13 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   }
 }
 
+template <int ROWS>
+auto kernel_of(int fmt) {
+  return fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8, ROWS>
+         : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3, ROWS>
+                           : attn_decode_kernel<kFmtBf16, ROWS>;
+}
+
 }  // namespace
 
 int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
@@ -720,12 +731,10 @@ int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st) {
   const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
   const dim3 g(grid), th(kDecodeThreads);
-  const auto kernel = a.start ? (fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8, true>
-                                 : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3, true>
-                                                   : attn_decode_kernel<kFmtBf16, true>)
-                              : (fmt == kFmtInt8   ? attn_decode_kernel<kFmtInt8, false>
-                                 : fmt == kFmtE4m3 ? attn_decode_kernel<kFmtE4m3, false>
-                                                   : attn_decode_kernel<kFmtBf16, false>);
+  const int rows = !a.start ? kWindow : (a.leader ? kBoth : kOwn);
+  const auto kernel = rows == kWindow ? kernel_of<kWindow>(fmt)
+                      : rows == kOwn  ? kernel_of<kOwn>(fmt)
+                                      : kernel_of<kBoth>(fmt);
   if (smem > 24 * 1024) {  // with the static arrays: past the default limit
     const cudaError_t e = cudaFuncSetAttribute(
         (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
