@@ -39,7 +39,7 @@ __device__ int64_t block_prefix(int64_t x, int64_t* scratch, int64_t& total) {
 // The segments of a share, in order: costs [at, end) of the list.
 __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share) {
   const int Hkv = a.c.Hkv;
-  int count = 0;
+  int count = 0, first = 0;
   if (share < t.shares && t.cost > 0) {
     int64_t at = share_start(t, share);
     const int64_t end = share_start(t, share + 1);
@@ -55,10 +55,10 @@ __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share)
       SharedUnit u;
       if (s.rows > 0) {
         const int last = (s.rows - 1) / kUnitRows;  // all columns but this one are full
-        int64_t k = (at - s.cost0) / column;
+        int64_t k = over(at - s.cost0, column);
         if (k > last) k = last;
         const int w = s.rows - (int)k * kUnitRows > 128 ? kCostBoth : kCostAlone;
-        g = (at - s.cost0 - k * column) / (tiles * w);
+        g = over(at - s.cost0 - k * column, tiles * w);
         if (g < Hkv) u = unit_of(s, Hkv, (int)k, (int)g);
       }
       if (g >= Hkv) {
@@ -67,8 +67,8 @@ __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share)
         continue;
       }
       SharedSegment x;
-      x.j0 = (int)((at - u.cost0 + u.w - 1) / u.w);
-      const int64_t j1 = (end - u.cost0 + u.w - 1) / u.w;
+      x.j0 = (int)over(at - u.cost0 + u.w - 1, u.w);
+      const int64_t j1 = over(end - u.cost0 + u.w - 1, u.w);
       x.j1 = j1 < u.tiles ? (int)j1 : u.tiles;
       at = u.cost0 + (int64_t)u.tiles * u.w;
       if (x.j0 >= x.j1) continue;  // (begins behind the last tile's start)
@@ -84,14 +84,14 @@ __device__ void list_share(const SharedArgs& a, const SharedTotal& t, int share)
       x.copies = u.both() ? 1 : tile_copies(u.rows);
       x.part = segment_part(u, share, x.j0 == 0);
       const int number = share + s.unit0 + u.t * Hkv + u.g;
-      if (count == 0) a.total->first[share] = number;
+      if (count == 0) first = number;
       if (x.j0 == 0) a.spans[number - share].x = share;
       if (x.j1 == u.tiles) a.spans[number - share].y = share;
       a.segments[number] = x;
       ++count;
     }
   }
-  a.total->count[share] = count;
+  a.total->segments[share] = make_int2(first, count);
 }
 
 // The groups' work in a list, and who shares what with whom (the first CTA); the decode
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
   }
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kMostParts = 2 * kSharedShares;
 
 // A (sequence, KV head) a CTA.  First a warp a query head: the maxima and sums of the row's
@@ -287,11 +287,10 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(SharedArgs a)
 #pragma unroll 8
     for (int e = way; e < count; e += ways) {
       const float w = weight_s[h][e];
-      if (w > 0.f) {
-        const float4 x = __ldcg(parts + place_s[h][e] + (int64_t)c * rs);
-        o.x = fmaf(x.x, w, o.x); o.y = fmaf(x.y, w, o.y);
-        o.z = fmaf(x.z, w, o.z); o.w = fmaf(x.w, w, o.w);
-      }
+      float4 x = __ldcg(parts + place_s[h][e] + (int64_t)c * rs);
+      if (!(w > 0.f)) x = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever lies there)
+      o.x = fmaf(x.x, w, o.x); o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z); o.w = fmaf(x.w, w, o.w);
     }
     if (way == 0 && own_s[h] > 0.f) {
       const float w = own_s[h];

@@ -24,8 +24,7 @@ struct SharedGroup {
 struct SharedTotal {
   int64_t cost;
   int32_t shares;  // of the list that take part
-  // each share's segments: the number of the first, how many
-  int32_t first[kSharedShares], count[kSharedShares];
+  int2 segments[kSharedShares];  // each share's: the number of the first, how many
 };
 // What a share has of a unit.
 struct __align__(16) SharedSegment {
@@ -86,8 +85,14 @@ __host__ __device__ inline int64_t group_rows(int rows, int Hkv) {
 }
 
 #ifdef __CUDACC__
+// a / b of numbers that are not negative: in 32 bits where they fit (64-bit division takes
+// hundreds of cycles).
+__device__ __forceinline__ int64_t over(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (int64_t)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ int64_t share_start(const SharedTotal& t, int share) {
-  return (t.cost * share + t.shares - 1) / t.shares;
+  return over(t.cost * share + t.shares - 1, t.shares);
 }
 
 // A unit: queries [256 t, ...) of KV head g of a group.

@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     }
     fence_mbar_init();
     abort_s = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
   }
   if (tid < 8) bad_s[tid] = 0;
   if (warp == 0) {
@@ -167,8 +169,9 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
   auto wait = [&](uint64_t* x, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_long(x, parity, &abort_s)) != 0;
   };
-  const int n_seg = a.total->count[blockIdx.x];
-  const SharedSegment* segments = a.segments + (n_seg > 0 ? a.total->first[blockIdx.x] : 0);
+  const int2 list = a.total->segments[blockIdx.x];
+  const int n_seg = list.y;
+  const SharedSegment* segments = a.segments + list.x;
 
   if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
