@@ -39,9 +39,25 @@ constexpr int kRopeBatch = 5;   // rows of eight lanes in flight
 template <int TOKENS, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   constexpr int WAYS = kRopeThreads / 8 / TOKENS;
+  // Several axes: neighbouring pairs may turn by different positions, so a thread finds one
+  // pair's angle of the CTA's tokens, and the lanes take theirs from here, in the order of
+  // the table's rows.
+  __shared__ float4 angle_s[AXES ? TOKENS : 1][kD / 4];
   pdl_wait();
   const int slot = threadIdx.x >> 3;
   const int64_t t = (int64_t)blockIdx.x * TOKENS + slot / WAYS;
+  if (AXES) {
+    for (int i = threadIdx.x; i < TOKENS * a.rope.pairs; i += kRopeThreads) {
+      const int token = i / a.rope.pairs, pair = i - token * a.rope.pairs;
+      const int64_t at = (int64_t)blockIdx.x * TOKENS + token;
+      if (at < a.T) {
+        const uint32_t axis = a.axes.of[pair >> 3] >> (2 * (pair & 7)) & 3u;
+        reinterpret_cast<float2*>(angle_s[token])[rope_place(pair, kD / 2)] =
+            rope_angle(a.rope, a.positions[at + axis * a.axes.stride], pair);
+      }
+    }
+    __syncthreads();
+  }
   if (t >= a.T) return;
   const int H = a.Hq + a.Hkv;
   const RopeLane ln = rope_lane(a.rope, threadIdx.x & 7);
@@ -52,11 +68,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
   const int second = 8 * (ln.b - ln.a);
   float2 cs[8];
   if (ln.pair >= 0) {
-    if (AXES)
-      rope_angles_axes(a.rope, a.positions + t, a.axes.stride, a.axes.of[threadIdx.x & 7],
-                       threadIdx.x & 7, cs);
-    else
+    if (AXES) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 x = angle_s[slot / WAYS][8 * e + (threadIdx.x & 7)];
+        cs[2 * e] = make_float2(x.x, x.y);
+        cs[2 * e + 1] = make_float2(x.z, x.w);
+      }
+    } else {
       rope_angles(a.rope, a.positions[t], threadIdx.x & 7, cs);
+    }
     if (a.inverse)
 #pragma unroll
       for (int e = 0; e < 8; ++e) cs[e].y = -cs[e].y;

@@ -37,28 +37,29 @@ __device__ __forceinline__ void rope_angles(const RopeView& r, int64_t t, int l,
   for (int e = 0; e < 4; ++e) rope_sum(lo[n8 * e], hi[n8 * e], cs[2 * e], cs[2 * e + 1]);
 }
 
-// The same with a position for each axis of the eight pairs (`of`: their axes, two bits
-// each).  Pieces of 8 bytes, since neighbours may turn by different positions; false: a
-// position is out of range (its pairs are NaN).
+// cos and sin of position t for pair i; NaN where the position is out of range.
+__device__ __forceinline__ float2 rope_angle(const RopeView& r, int32_t t, int i) {
+  if ((uint32_t)t >= (uint64_t)r.max_pos) return make_float2(nanf(""), nanf(""));
+  const int place = rope_place(i, r.pairs);
+  const float2 a = r.lo[(int64_t)(t & (kRopeLow - 1)) * r.pairs + place];
+  const float2 b = r.hi[(int64_t)(t >> kRopeLowBits) * r.pairs + place];
+  return make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+}
+
+// rope_angles with a position for each axis of the eight pairs (`of`: their axes, two bits
+// each), piece by piece, since neighbours may turn by different positions; false: a
+// position is out of range.
 __device__ __forceinline__ bool rope_angles_axes(const RopeView& r, const int32_t* positions,
                                                  int64_t stride, uint32_t of, int l,
                                                  float2 (&cs)[8]) {
-  const int n8 = r.pairs >> 3;
-  bool good = true;
   int32_t t[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) t[e] = positions[((of >> (2 * e)) & 3u) * stride];
+  bool good = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    if ((uint32_t)t[e] >= (uint64_t)r.max_pos) {
-      cs[e] = make_float2(nanf(""), nanf(""));
-      good = false;
-      continue;
-    }
-    const int place = 2 * (n8 * (e >> 1) + l) + (e & 1);
-    const float2 a = r.lo[(int64_t)(t[e] & (kRopeLow - 1)) * r.pairs + place];
-    const float2 b = r.hi[(int64_t)(t[e] >> kRopeLowBits) * r.pairs + place];
-    cs[e] = make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+    cs[e] = rope_angle(r, t[e], 8 * l + e);
+    good &= (uint32_t)t[e] < (uint64_t)r.max_pos;
   }
   return good;
 }
