@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(append_threads(BLK), (KIND ? 512 : 768) / appe
 #pragma unroll
           for (int e = 0; e < 4; ++e) rope_sum(lo[i][e], hi[e], cs[2 * e], cs[2 * e + 1]);
         } else if (is_axes(KIND)) {
-          if (!rope_angles_axes(a.rope, a.positions + tok0 + r, a.axes.stride, a.axes.of[l], l,
-                                cs) && a.status)
+          if (!rope_angles_axes(a.rope, a.positions + tok0 + r, a.axes.stride, a.axes.n,
+                                a.axes.of[l], l, cs) && a.status)
             atomicOr(a.status, kStatusBadLength);
         } else {
           const int64_t at = a.positions ? (int64_t)a.positions[tok0 + r] : p0 + r;

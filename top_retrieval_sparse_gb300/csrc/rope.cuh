@@ -46,20 +46,33 @@ __device__ __forceinline__ float2 rope_angle(const RopeView& r, int32_t t, int i
   return make_float2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
 }
 
-// rope_angles with a position for each axis of the eight pairs (`of`: their axes, two bits
-// each), piece by piece, since neighbours may turn by different positions; false: a
-// position is out of range.
+// rope_angles with n positions, one on each axis of the eight pairs (`of`: their axes, two
+// bits each); false: a position is out of range.  Two neighbours on one axis take a piece of
+// 16 bytes of each row, others half of one each.
 __device__ __forceinline__ bool rope_angles_axes(const RopeView& r, const int32_t* positions,
-                                                 int64_t stride, uint32_t of, int l,
+                                                 int64_t stride, int n, uint32_t of, int l,
                                                  float2 (&cs)[8]) {
-  int32_t t[8];
+  int32_t t[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t[e] = positions[((of >> (2 * e)) & 3u) * stride];
+  for (int x = 0; x < 4; ++x) t[x] = x < n ? positions[x * stride] : 0;
+  auto at = [&](int e) {
+    const uint32_t x = of >> (2 * e) & 3u;
+    return x & 2u ? (x & 1u ? t[3] : t[2]) : (x & 1u ? t[1] : t[0]);
+  };
+  const int n8 = r.pairs >> 3;
   bool good = true;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = rope_angle(r, t[e], 8 * l + e);
-    good &= (uint32_t)t[e] < (uint64_t)r.max_pos;
+  for (int e = 0; e < 4; ++e) {
+    const int32_t a = at(2 * e), b = at(2 * e + 1);
+    if (a == b && (uint32_t)a < (uint64_t)r.max_pos) {
+      const float4* lo = reinterpret_cast<const float4*>(r.lo + (a & (kRopeLow - 1)) * (int64_t)r.pairs);
+      const float4* hi = reinterpret_cast<const float4*>(r.hi + (a >> kRopeLowBits) * (int64_t)r.pairs);
+      rope_sum(lo[n8 * e + l], hi[n8 * e + l], cs[2 * e], cs[2 * e + 1]);
+    } else {
+      cs[2 * e] = rope_angle(r, a, 8 * l + 2 * e);
+      cs[2 * e + 1] = rope_angle(r, b, 8 * l + 2 * e + 1);
+      good &= (uint32_t)a < (uint64_t)r.max_pos && (uint32_t)b < (uint64_t)r.max_pos;
+    }
   }
   return good;
 }
