@@ -242,6 +242,12 @@ def read_trace(buf: torch.Tensor):
     return out
 
 
+def _page_bufs(*pools: torch.Tensor) -> bytes:
+    """The tsa_page_buf of every pool of pages, [n_pages][...] (as their bytes)."""
+    return b"".join(struct.pack("=qq", p.data_ptr(), p.nbytes // max(1, p.shape[0]))
+                    for p in pools)
+
+
 class KV:
     """A layer's KV cache as the library sees it (keeps the tensors alive)."""
 
@@ -254,6 +260,7 @@ class KV:
             if t is not None and t.device != k.device:
                 raise ValueError(f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.page_table = k, v, page_table
+        self._bufs = _page_bufs(k, v)
         if page_table is None:
             if k.dim() != 4:
                 raise ValueError("contiguous k must be [B][Hkv][l_cap][d]")
@@ -819,6 +826,8 @@ class KV8:
                            (page_table, "page_table"), (status, "status"))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table, self.status, self.fmt = page_table, status, fmt
+        self._bufs = _page_bufs(k, v, k_scale, v_scale)
+        self._status = _ptr(status)
         self.block = rows // k_scale.shape[2]
         if page_table is None:
             self.B, self.l_cap, ps, mp, n_pages = n, rows, 0, 0, 0
@@ -1100,6 +1109,7 @@ class Pages:
         self.n_pages = refs.numel()
         n = int(lib().tsa_pages_workspace_size(self.B, self.max_pages, self.n_pages))
         self.workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+        self._ws, self._ws_bytes = self.workspace.data_ptr(), self.workspace.nbytes
         self.struct = _PagesStruct(table.data_ptr(), refs.data_ptr(), self.B, self.max_pages,
                                    self.n_pages, self.page_size)
         self._ref = C.byref(self.struct)
@@ -1112,28 +1122,35 @@ class Pages:
                    torch.zeros(n_pages, dtype=torch.int32, device=device), page_size)
 
     def _run(self, fn, stream, *args):
-        _run_on(self.device, stream, fn, self._ref, *args, self.workspace.data_ptr(),
-                self.workspace.nbytes)
+        _run_on(self.device, stream, fn, self._ref, *args, self._ws, self._ws_bytes)
 
-    def _range(self, lo, hi):
-        for t, name in ((lo, "lo"), (hi, "hi")):
-            _want(t, torch.int32, name)
-            if t.shape != (self.B,):
-                raise ValueError(f"{name} must be int32 [{self.B}], got {tuple(t.shape)}")
-        _gpu((self.table, "pages"), (lo, "lo"), (hi, "hi"))
-        return lo.data_ptr(), hi.data_ptr()
+    def _ints(self, n: int, **named):
+        """The int32 [n] tensors given (or None) on the pages' device, as pointers."""
+        out = []
+        for name, t in named.items():
+            if t is None:
+                out.append(None)
+                continue
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+            if t.shape != (n,) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 [{n}], got {tuple(t.shape)}")
+            if t.device != self.device:
+                _gpu((self.table, "pages"), (t, name))
+            out.append(t.data_ptr())
+        return out
 
 
 def pages_alloc(pages: Pages, lo: torch.Tensor, hi: torch.Tensor, stream=None) -> Pages:
     """Gives sequence b a free page (the lowest ones) for every entry that holds a
     position of [lo[b], hi[b]) and has none."""
-    pages._run(lib().pages_alloc, stream, *pages._range(lo, hi))
+    pages._run(lib().pages_alloc, stream, *pages._ints(pages.B, lo=lo, hi=hi))
     return pages
 
 
 def pages_free(pages: Pages, lo: torch.Tensor, hi: torch.Tensor, stream=None) -> Pages:
     """Takes from sequence b the pages that lie in positions [lo[b], hi[b]) altogether."""
-    pages._run(lib().pages_free, stream, *pages._range(lo, hi))
+    pages._run(lib().pages_free, stream, *pages._ints(pages.B, lo=lo, hi=hi))
     return pages
 
 
@@ -1144,18 +1161,11 @@ def pages_fork(pages: Pages, parents: torch.Tensor, children: torch.Tensor, lens
     pages are shared, a partial last one gets a page of its own.  Returns (src, dst),
     int32 [n], the pages that pages_copy has to copy (-1: none)."""
     n = parents.numel()
-    for t, name in ((parents, "parents"), (children, "children"), (lens, "lens"), (src, "src"),
-                    (dst, "dst")):
-        if t is not None:
-            _want(t, torch.int32, name)
-            if t.shape != (n,):
-                raise ValueError(f"{name} must be int32 [{n}], got {tuple(t.shape)}")
-    dev = _gpu((pages.table, "pages"), (parents, "parents"), (children, "children"),
-               (lens, "lens"), (src, "src"), (dst, "dst"))
-    src = _new(stream, dev, (n,), torch.int32) if src is None else src
-    dst = _new(stream, dev, (n,), torch.int32) if dst is None else dst
-    pages._run(lib().pages_fork, stream, _ptr(parents), _ptr(children), _ptr(lens), n, _ptr(src),
-               _ptr(dst))
+    if src is None or dst is None:
+        new = _new(stream, pages.device, (2, n), torch.int32).unbind(0)
+        src, dst = new[0] if src is None else src, new[1] if dst is None else dst
+    p = pages._ints(n, parents=parents, children=children, lens=lens, src=src, dst=dst)
+    pages._run(lib().pages_fork, stream, p[0], p[1], p[2], n, p[3], p[4])
     return src, dst
 
 
@@ -1166,16 +1176,13 @@ def pages_compact(pages: Pages, src: Optional[torch.Tensor] = None,
     moved by pages_copy).  Returns (src, dst, count): int32 [n_pages // 2] twice, padded
     with -1, and int32 [1]."""
     n = pages.n_pages // 2
-    for t, name, size in ((src, "src", n), (dst, "dst", n), (count, "count", 1)):
-        if t is not None:
-            _want(t, torch.int32, name)
-            if t.shape != (size,):
-                raise ValueError(f"{name} must be int32 [{size}], got {tuple(t.shape)}")
-    dev = _gpu((pages.table, "pages"), (src, "src"), (dst, "dst"), (count, "count"))
-    src = _new(stream, dev, (n,), torch.int32) if src is None else src
-    dst = _new(stream, dev, (n,), torch.int32) if dst is None else dst
-    count = _new(stream, dev, (1,), torch.int32) if count is None else count
-    pages._run(lib().pages_compact, stream, _ptr(src), _ptr(dst), _ptr(count))
+    if src is None or dst is None:
+        new = _new(stream, pages.device, (2, n), torch.int32).unbind(0)
+        src, dst = new[0] if src is None else src, new[1] if dst is None else dst
+    if count is None:
+        count = _new(stream, pages.device, (1,), torch.int32)
+    pages._run(lib().pages_compact, stream, *pages._ints(n, src=src, dst=dst),
+               *pages._ints(1, count=count))
     return src, dst, count
 
 
@@ -1184,27 +1191,29 @@ def pages_copy(caches, src: torch.Tensor, dst: torch.Tensor,
     """Copies page src[i] over page dst[i] (int32 [n], -1: none) in every cache given (a
     paged KV or KV8, or a list of them, of one pool size); count: int32 [1], how many
     pairs count."""
-    caches = list(caches) if isinstance(caches, (list, tuple)) else [caches]
+    if not isinstance(caches, (list, tuple)):
+        caches = (caches,)
     n = src.numel()
-    for t, name, shape in ((src, "src", (n,)), (dst, "dst", (n,)), (count, "count", (1,))):
+    for t, name, size in ((src, "src", n), (dst, "dst", n), (count, "count", 1)):
         if t is not None:
             _want(t, torch.int32, name)
-            if t.shape != shape:
-                raise ValueError(f"{name} must be int32 {list(shape)}, got {tuple(t.shape)}")
+            if t.shape != (size,):
+                raise ValueError(f"{name} must be int32 [{size}], got {tuple(t.shape)}")
     if not caches:
         return
-    bufs = []
+    n_pages, dev, status = caches[0].k.shape[0], src.device, None
     for c in caches:
         if c.page_table is None:
             raise ValueError("pages_copy needs paged caches")
-        if c.k.shape[0] != caches[0].k.shape[0]:
+        if c.k.shape[0] != n_pages:
             raise ValueError("the caches' pools must have the same number of pages")
-        bufs += [c.k, c.v] + ([c.k_scale, c.v_scale] if isinstance(c, KV8) else [])
-    dev = _gpu((src, "src"), (dst, "dst"), (count, "count"), *((b, "a cache") for b in bufs))
-    n_pages = bufs[0].shape[0]
+        if c.k.device != dev:
+            _gpu((src, "src"), (c.k, "a cache"))
+        status = status or getattr(c, "_status", None)
+    if dst.device != dev or dev.type != "cuda" or count is not None and count.device != dev:
+        _gpu((src, "src"), (dst, "dst"), (count, "count"))
     if n_pages == 0:
         return
-    arr = (_PageBuf * len(bufs))(*[(b.data_ptr(), b.nbytes // n_pages) for b in bufs])
-    status = next((c.status for c in caches if getattr(c, "status", None) is not None), None)
-    _run_on(dev, stream, lib().pages_copy, arr, len(bufs), n_pages, _ptr(src), _ptr(dst),
-            _ptr(count), n, _ptr(status))
+    bufs = b"".join([c._bufs for c in caches])
+    _run_on(dev, stream, lib().pages_copy, bufs, len(bufs) // 16, n_pages, src.data_ptr(),
+            dst.data_ptr(), _ptr(count), n, status)
