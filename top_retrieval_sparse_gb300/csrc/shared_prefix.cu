@@ -62,7 +62,7 @@ constexpr int kFoldEvery = PARTS == 2 ? 32 : 128;
 
 template <int FMT>
 struct SharedBars {
-  uint64_t q[2], s[2], p[2][2], o[2], full[kSlots<FMT>], empty[kSlots<FMT>], clean[kSlots<FMT>],
+  uint64_t q[2], s[2], p[2][4], o[2], full[kSlots<FMT>], empty[kSlots<FMT>], clean[kSlots<FMT>],
       drain[2], turn[2], raw_full[kRawSlots], raw_empty[kRawSlots], scale[kRawSlots];
 };
 
@@ -131,8 +131,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q[i], kTile);
       mbar_init(&bar.s[i], 1);
-      mbar_init(&bar.p[i][0], kTile);
-      mbar_init(&bar.p[i][1], kTile);
+      for (int c = 0; c < 4; ++c) mbar_init(&bar.p[i][c], kTile);
       mbar_init(&bar.o[i], 1);
       mbar_init(&bar.drain[i], 1);
       mbar_init(&bar.turn[i], 1);
@@ -304,8 +303,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             if (Q8) ok = wait(&bar.scale[raw_slot(seg_tile + tile)], raw_lap(seg_tile + tile));
             if (__builtin_expect(!ok, 0)) break;
             if (!warp_live) {  // nobody reads these rows' weights
-              mbar_arrive(&bar.p[x][0]);
-              mbar_arrive(&bar.p[x][1]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mbar_arrive(&bar.p[x][c]);
               continue;
             }
             fence_after();
@@ -330,56 +329,53 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) columns(c);
             }
-            // Weights of half a tile (64 keys) under the maximum `top`; their sum.
-            auto weights = [&](int half, float top) {
+            // Weights of a quarter of a tile (32 keys) under the maximum `top`; their sum.
+            auto weights = [&](int c, float top) {
               const float off = top == -INFINITY ? 0.f : (Q8 ? -top : -top * sc);
               float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               float sum = 0.f;
-#pragma unroll (Q8 ? 1 : 2)
-              for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                if (MANY && !mine_is(c)) {  // another copy's
-                  const uint32_t none[16] = {};
-                  store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, none);
-                  if (PARTS == 2) store_cols(s_at + 32 * c + 16, none);
-                  continue;
-                }
-                if (Q8) columns(c);
-                const float* y = s + (Q8 ? 0 : 32 * c);
-                uint32_t w[16], w2[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float f = sc, o = off;
-                  if constexpr (Q8) {
-                    const float4 k = blocks[2 * c + i / 8];
-                    f = fmaxf(row_sc * k.x, kLeastFactor);
-                    o = off + k.y;
-                    if (i % 8 == 0) add[0] = add[1] = make_float2(0.f, 0.f);
-                  }
-                  float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), make_float2(f, f),
-                                  make_float2(o, o));
-                  e.x = ex2(e.x);
-                  e.y = ex2(e.y);
-                  add[i & 1] = add2(add[i & 1], e);
-                  if constexpr (Q8) {
-                    if (i % 8 == 7)
-                      sum = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y),
-                                 blocks[2 * c + i / 8].z, sum);
-                  }
-                  w[i] = pack2<FMT>(e.x, e.y);
-                  if (PARTS == 2) {
-                    const float2 d = fma2(unpack2<FMT>(w[i]), make_float2(-1.f, -1.f), e);
-                    w2[i] = pack2<FMT>(d.x, d.y);
-                  }
-                }
-                store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, w);
-                if (PARTS == 2) store_cols(s_at + 32 * c + 16, w2);
+              if (MANY && !mine_is(c)) {  // another copy's
+                const uint32_t none[16] = {};
+                store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, none);
+                if (PARTS == 2) store_cols(s_at + 32 * c + 16, none);
+                return 0.f;
               }
+              if (Q8) columns(c);
+              const float* y = s + (Q8 ? 0 : 32 * c);
+              uint32_t w[16], w2[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float f = sc, o = off;
+                if constexpr (Q8) {
+                  const float4 k = blocks[2 * c + i / 8];
+                  f = fmaxf(row_sc * k.x, kLeastFactor);
+                  o = off + k.y;
+                  if (i % 8 == 0) add[0] = add[1] = make_float2(0.f, 0.f);
+                }
+                float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), make_float2(f, f),
+                                make_float2(o, o));
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                add[i & 1] = add2(add[i & 1], e);
+                if constexpr (Q8) {
+                  if (i % 8 == 7)
+                    sum = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y),
+                               blocks[2 * c + i / 8].z, sum);
+                }
+                w[i] = pack2<FMT>(e.x, e.y);
+                if (PARTS == 2) {
+                  const float2 d = fma2(unpack2<FMT>(w[i]), make_float2(-1.f, -1.f), e);
+                  w2[i] = pack2<FMT>(d.x, d.y);
+                }
+              }
+              store_cols(s_at + (PARTS == 2 ? 32 : 16) * c, w);
+              if (PARTS == 2) store_cols(s_at + 32 * c + 16, w2);
               return Q8 ? sum : (add[0].x + add[0].y) + (add[1].x + add[1].y);
             };
-            auto publish = [&](int half) {  // their products may begin
+            auto publish = [&](int c) {  // their products may begin
               wait_stores();
               fence_before();
-              mbar_arrive(&bar.p[x][half]);
+              mbar_arrive(&bar.p[x][c]);
             };
             float l0 = 0.f;
             if constexpr (Q8) {
@@ -416,18 +412,17 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
                   }
                 }
               }
-              l0 = weights(0, m);
             } else {
               // The maximum is off the path from S to the weights.  They are taken under the
-              // maximum so far as long as they stay below 2^kRescale: the first half's sum
-              // tells for itself, the second half's logits are looked at.  Where they do not
+              // maximum so far as long as they stay below 2^kRescale: the first quarter's sum
+              // tells for itself, the others' logits are looked at.  Where they do not
               // (first tiles, rarely later) the maximum is found, O and the sum are rescaled
               // and the weights taken again.
               bool good = m != -INFINITY || !live;
               if (__builtin_expect(__all_sync(0xffffffffu, good), 1)) {
-                float tops[4] = {s[64], s[65], s[66], s[67]};
+                float tops[4] = {s[32], s[33], s[34], s[35]};
 #pragma unroll
-                for (int i = 68; i < 124; i += 8)
+                for (int i = 36; i < 124; i += 8)
 #pragma unroll
                   for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[i + e], s[i + 4 + e]);
                 const float t = max3(fmaxf(tops[0], s[124]), fmaxf(tops[1], s[125]),
@@ -458,9 +453,14 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
                 l0 = weights(0, m);
               }
             }
-            publish(0);
-            l += l0 + weights(1, m);
-            publish(1);
+            if (!Q8) publish(0);
+            l += l0;
+            // (8-bit: one piece of code for all quarters, for the instruction cache's sake)
+#pragma unroll (Q8 ? 1 : 3)
+            for (int c = Q8 ? 0 : 1; c < 4; ++c) {
+              l += weights(c, m);
+              publish(c);
+            }
           }
         }
         };
@@ -585,17 +585,17 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           const bool more = j % kFoldEvery<PARTS> > 0;
           const uint32_t parity = (tiles + j) & 1;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && wait_long(&bar.p[x][half], parity, &abort_s);
-            if (half == 0 && both)
+          for (int c = 0; c < 4; ++c) {
+            ok = ok && wait_long(&bar.p[x][c], parity, &abort_s);
+            if (c == 0 && both)
               ok = ok && wait_long(&bar.turn[x], (turns + j + x) & 1, &abort_s);
             if (ok) {
               fence_after();
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k) {
+              for (int k = 2 * c; k < 2 * c + 2; ++k) {
                 const uint64_t vk = vx + ((k * 16 * 128) >> 4);
                 if (PARTS == 2) {
-                  const uint32_t w = s_at + 32 * (k >> 1) + 8 * (k & 1);
+                  const uint32_t w = s_at + 32 * c + 8 * (k & 1);
                   mma_ts(o_at, w, vk, kPv, more || k > 0);
                   mma_ts(o_at, w + 16, vk, kPv, true);
                 } else {
