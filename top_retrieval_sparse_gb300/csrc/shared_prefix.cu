@@ -771,45 +771,43 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         for (int w = 0; w < 2 && ok; ++w) {
           const uint32_t i = 2 * tile + w;
           ok = wait(&bar.raw_full[raw_slot(i)], raw_lap(i));
-          if (ok && i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
           if (!ok) break;
+          // The codes wait in registers for the operand's slot, and theirs is free again.
           const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
-          // (all loads before the first store; rows 8 apart have the same swizzle)
-#pragma unroll 1
-          for (int n0 = 0; n0 < 8; n0 += 4) {
-            uint4 c[4];
+          uint4 c[8];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int piece = ch ^ ((n0 + n) & 1) << 2;
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
-                           : "r"(from + (row0 + (n0 + n) / 2 * 32) * kD + piece * 16)
-                           : "memory");
-            }
+          for (int n = 0; n < 8; ++n) {
+            const int piece = ch ^ (n & 1) << 2;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(c[n].x), "=r"(c[n].y), "=r"(c[n].z), "=r"(c[n].w)
+                         : "r"(from + (row0 + n / 2 * 32) * kD + piece * 16)
+                         : "memory");
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.raw_empty[raw_slot(i)]);
+          if (i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
+          if (!ok) break;
+          // (rows 8 apart have the same swizzle)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int row = row0 + (n0 + n) / 2 * 32, piece = ch ^ ((n0 + n) & 1) << 2;
-              uint4 y, z;
-              widen<FMT>(c[n].x, y.x, y.y);
-              widen<FMT>(c[n].y, y.z, y.w);
-              widen<FMT>(c[n].z, z.x, z.y);
-              widen<FMT>(c[n].w, z.z, z.w);
-              if (left < kTile && row >= left) y = z = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t half = to + (piece >> 2) * kHalf + row * 128;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + at0),
-                           "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                           : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + (at0 ^ 16)),
-                           "r"(z.x), "r"(z.y), "r"(z.z), "r"(z.w)
-                           : "memory");
-            }
+          for (int n = 0; n < 8; ++n) {
+            const int row = row0 + n / 2 * 32, piece = ch ^ (n & 1) << 2;
+            uint4 y, z;
+            widen<FMT>(c[n].x, y.x, y.y);
+            widen<FMT>(c[n].y, y.z, y.w);
+            widen<FMT>(c[n].z, z.x, z.y);
+            widen<FMT>(c[n].w, z.z, z.w);
+            if (left < kTile && row >= left) y = z = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t half = to + (piece >> 2) * kHalf + row * 128;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + at0), "r"(y.x),
+                         "r"(y.y), "r"(y.z), "r"(y.w)
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(half + (at0 ^ 16)),
+                         "r"(z.x), "r"(z.y), "r"(z.z), "r"(z.w)
+                         : "memory");
           }
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar.full[slot_of<FMT>(i)]);
-            mbar_arrive(&bar.raw_empty[raw_slot(i)]);
-          }
+          if (lane == 0) mbar_arrive(&bar.full[slot_of<FMT>(i)]);
         }
       }
     }
