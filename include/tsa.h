@@ -8,9 +8,10 @@
  * log-sum-exp rescale.  A second entry point runs ReTopK's reuse path, which
  * recalls candidate keys from a per-head cache of past queries instead of
  * scanning every key on most steps.  Beside them stand the operators that a
- * program needs around the cache: rotary positions, an 8-bit cache (written with
- * rotated keys, read back, attended), and attention with a sliding window and
- * sinks for one token or many.
+ * program needs around the cache: rotary positions (one or several axes), an 8-bit
+ * cache (written with rotated keys, read back, attended), attention with a sliding
+ * window and sinks for one token or many, the pages of a cache (taken, given back,
+ * forked, compacted, copied), and attention of a batch that shares its first rows.
  *
  * Sources (page title, section / equation):
  *   [RA]  "RetrievalAttention: Accelerating Long-Context LLM Inference via
@@ -676,13 +677,20 @@ TSA_API int window_attn_decode(const void* q, const tsa_kv* kv, const int32_t* l
  *   q: bf16 [B][Hq][128]; lens: int32 [B] (device), 0: an empty place, its out 0, lse -inf;
  *   out: [B][Hq][128] = softmax(scale q.k) . v over both, fp32, or bf16 with out_bf16 != 0;
  *   lse_out: fp32 [B][Hq] or NULL.
- *   Visible rows must be finite; limits as kv8_attn_decode, and N <= 4096.
+ *   Visible rows must be finite; limits as kv8_attn_decode, N <= 4096, and less than 2^31
+ *   rows of all KV heads in the cache.
+ *   Sums are 32-bit.  The weights of the shared rows enter the second product in parts that add
+ *   up to 16 bits (fp32 out, bf16 caches; a 2^-18 of a weight is left out), 22 bits (fp32 out,
+ *   8-bit caches), or 8 and 11 bits (bf16 out); the own rows' as in the calls above, and the
+ *   shared rows' too where the whole cache (B * Hkv * l_cap rows) has at most 64 MiB of keys
+ *   and values: it is then read by every sequence for itself.
  *   workspace: tsa_shared_attn_workspace_size() bytes, 256-byte aligned, zero-filled before
  *   its first use; calls of either entry point and of whatever sizes may share one.
  * Device-detected errors (on the workspace): a lens[b] or shared[n] outside [0, l_cap] is
  * clamped and flagged; 0 < lens[b] < shared[n] is flagged and gives NaN; offsets that do not
  * rise are flagged and give NaN everywhere; pages as kv8_attn_decode (a bad page of the
- * shared rows: NaN for all of the group). */
+ * shared rows: NaN for all of the group).  Waits between the kernel's warps are bounded by
+ * about a second, after which what depended on them is NaN and TSA_ERR_TIMEOUT reported. */
 TSA_API size_t tsa_shared_attn_workspace_size(int B, int N, int Hq, int Hkv, int d);
 TSA_API int shared_attn_decode(const void* q, const tsa_kv* kv, const int32_t* lens, int B,
                                const int32_t* cu_group, const int32_t* shared, int N, int Hq,

@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kDecodeThreads, ctas_of(FMT)) attn_decode_kern
   __shared__ int64_t scan_s[kWarps];
   __shared__ int last_s;
   pdl_wait();
-  pdl_trigger();
+  // (bf16 outputs may be queries of a key scan, which reads them before its dependency wait)
+  if (ROWS != kBoth || !a.out16) pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gr = lane >> 2, tq = lane & 3;
   const int Hkv = a.c.Hkv, G = a.Hq / Hkv;

@@ -17,14 +17,37 @@
 // odd tiles for the same queries, so that a tile's chain of copy, product, softmax, product
 // is hidden by the other's all the same.
 //
+// Up to 64 queries lie two or four times in their tile, and each copy takes a part of every
+// tile's columns: the exponentials are then all warps' work, and the copies are joined at
+// the segment's end.
+//
 // Warps.  0 and 3: the matrix instructions of A and of B, 1: the copies, 2: the rows of V
 // behind P (zeroed, for whatever they hold 0 * NaN would reach the output), 4-7: softmax of
 // A (thread = row = tensor-memory lane), 8-11: of B.  K and V tiles go through a ring of
 // five 32 KB slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a page where
 // pages are smaller than a tile), which runs on across segments.  A slot is filled again
 // when its three readers have given it back: both matrix threads, or one and the zeroing
-// warp for the other, and the zeroing warp.  It passes every slot in order, so nobody falls
-// behind by two laps and a barrier's parity is never taken for another lap's.
+// warp for the other, and the zeroing warp.  It passes every slot in order.  Weights are
+// handed to the second product by quarters of a tile (by halves 22 us more of 409, 256
+// queries' worth of samples under 131071 rows).
+//
+// 8-bit caches.  Codes come by TMA into a ring of four 16 KB slots; warps 12-15 widen them to
+// fp16 (exact) into three operand slots, zeroing V's rows behind P, and find the blocks'
+// scales.  The queries are in fp16 too, each row's exponents shifted.  The keys' scale is a
+// factor of the logits, the values' belongs to the weights and is taken out of their sum.
+//
+// Numbers.  The weights enter the second product in two parts where the output is fp32
+// (2^-18 of a weight left out in bf16, 2^-22 in fp16), in one where it is bf16.  (A third
+// bf16 part has no room in tensor memory beside the logits.)
+//
+// What bounds it (one call, the kernel alone).  64 sequences x 4 heads under 32767 rows of 8
+// KV heads, fp32: 46 us for 20 us of bytes and 27 us of matrix instructions (three products
+// of a tile); 12 us pass before the first product.  256 x 7 heads under 131071 rows of 4,
+// bf16: 310 us, 1550 TFLOP/s; the path from the logits to the first weights is a little
+// longer than the other stream's products.  8 groups of 8 x 4 heads under 115K rows of 8, e4m3: 590 us,
+// 3.1 TB/s of codes: a tile's chain of barriers, and the widening, 700 cycles a tile of K or
+// V.  Waits that read the global timer took 17 % more there, loops unrolled past the
+// instruction cache 27 %.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -565,9 +588,16 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
         const int j0 = segments[seg].j0, P = segments[seg].P;
         const int all = segments[seg].j1 - j0, n = both ? all : (all - x + 1) / 2;
         auto number = [&](int j) { return passed + (both ? j : 2 * j + x); };
+        // Before the slots of a tile are waited for, what was in them has to have landed, or
+        // their barriers' parity would stand for the lap before that; a stream that has not
+        // used those tiles itself learns it from the zeroing warp, which passes all in order.
+        auto landed_before = [&](uint32_t tile) {
+          return tile < 2 ||
+                 wait_long(&bar.clean[slot_of<FMT>(tile - 2)], lap_of<FMT>(tile - 2), &abort_s);
+        };
         if (n > 0) {
           const uint32_t i = 2 * number(0);
-          ok = wait_long(&bar.q[x], segs & 1, &abort_s) &&
+          ok = wait_long(&bar.q[x], segs & 1, &abort_s) && landed_before(number(0)) &&
                wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (both && x == 1) ok = ok && wait_long(&bar.turn[1], turns & 1, &abort_s);
           if (ok) {
@@ -608,7 +638,8 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           commit_mma(&bar.empty[slot_of<FMT>(i)]);
           if (j + 1 < n) {
             const uint32_t k = 2 * number(j + 1);
-            ok = wait_long(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
+            ok = landed_before(number(j + 1)) &&
+                 wait_long(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
             if (!ok) break;
             qk(slot_of<FMT>(k));
           } else {
@@ -722,7 +753,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           __syncwarp();
         }
         if (lane == 0) {
-          if (!Q8) mbar_arrive(&bar.clean[slot_of<FMT>(tile)]);
+          mbar_arrive(&bar.clean[slot_of<FMT>(tile)]);
           give(i + 1);
         }
       }
