@@ -353,6 +353,85 @@ def test_streams_graphs_and_calls_of_all_sizes_share_a_workspace(tsa, cap):
     assert tsa.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3"])
+def test_random_batches_match_every_sequence_by_itself(tsa, fmt):
+    """Groups of all sizes and lengths in one call, against the decode step of every sequence
+    over tables that all name the shared pages; every kind of unit after every other."""
+    g = gen(20)
+    rng = __import__("random").Random(5)
+    for turn in range(24):
+        Hq, Hkv = rng.choice([(32, 8), (32, 4), (28, 4), (12, 4), (6, 2), (5, 5), (8, 1)])
+        ps = rng.choice([16, 32, 64, 128, 256])
+        N = rng.choice([1, 2, 5, 12])
+        sizes = [rng.choice([0, 1, 2, 3, 7, 16, 30, 70]) for _ in range(N)]
+        P = [rng.choice([0, 1, 127, 128, 129, rng.randint(1, 3000)]) for _ in range(N)]
+        P = [x if s else 1 for x, s in zip(P, sizes)]     # (within the cache)
+        cu = [rng.choice([0, 0, 2])]
+        for s in sizes:
+            cu.append(cu[-1] + s)
+        B = cu[-1] + rng.choice([0, 1])
+        if B == 0:
+            continue
+        start = [0] * B
+        for n in range(N):
+            start[cu[n]:cu[n + 1]] = [P[n]] * sizes[n]
+        lens = [s + rng.choice([0, 1, 5, 200]) for s in start]
+        per = max(-(-max(lens) // ps), (96 << 20) // (B * Hkv * 256 * ps) + 1)  # a large cache
+        pages = tsa.Pages.empty(B, per, sum(-(-x // ps) for x in lens) + 5, ps)
+        lead = [cu[n] for n in range(N) if sizes[n]]
+        first = [lens[b] if b in lead or start[b] == 0 else 0 for b in range(B)]
+        tsa.pages_alloc(pages, i32([0] * B), i32(first))
+        kids = [b for b in range(B) if start[b] and b not in lead]
+        if kids:
+            par = [max(x for x in lead if x <= b) for b in kids]
+            tsa.pages_fork(pages, i32(par), i32(kids), i32([start[b] // ps * ps for b in kids]))
+            # (the partly shared page: a page of its own, its rows up to start not read)
+            tsa.pages_alloc(pages, i32([start[b] // ps * ps if b in kids else 0 for b in range(B)]),
+                            i32([lens[b] if b in kids else 0 for b in range(B)]))
+        assert tsa.workspace_status(pages.workspace) == 0
+        n_pages = pages.n_pages
+        q = randn(g, B, Hq, D).bfloat16()
+        k, v = (randn(g, n_pages, Hkv, ps, D).bfloat16() for _ in range(2))
+        if fmt == "bf16":
+            cache = tsa.kv_paged(k, v, pages.table)
+        else:
+            blk = min(ps, rng.choice([16, 32, 64, 128]))
+            cache = tsa.KV8.paged(n_pages, Hkv, ps, pages.table, blk, fmt)
+            for i in range(0, n_pages, 4096):              # every page a sequence of its own
+                j = min(n_pages, i + 4096)
+                ids = torch.arange(i, j, device=DEV).int().view(-1, 1)
+                one = tsa.KV8(cache.k, cache.v, cache.k_scale, cache.v_scale, fmt, ids)
+                flat = [x[i:j].transpose(1, 2).reshape(-1, Hkv, D) for x in (k, v)]
+                tsa.kv8_append(one, *flat, i32([ps] * (j - i)))
+            # (one scale, so that a child's block of shared and own rows has the leader's too)
+            cache.k_scale.fill_(cache.k_scale.max())
+            cache.v_scale.fill_(cache.v_scale.max())
+        # rows before start in a child's own page are the leader's
+        for b in kids:
+            a, z = start[b] // ps * ps, start[b]
+            if a < z:
+                src, dst = (int(pages.table[x, a // ps]) for x in (max(x for x in lead if x <= b), b))
+                for x in (cache.k, cache.v):
+                    x[dst, :, : z - a] = x[src, :, : z - a]
+        for dtype in (torch.float32, torch.bfloat16):
+            out = torch.empty((B, Hq, D), dtype=dtype, device=DEV)
+            lse, lse1 = (torch.empty((B, Hq), device=DEV) for _ in range(2))
+            ws = tsa.shared_attn_decode_workspace(B, N, Hq, Hkv)
+            tsa.shared_attn_decode(q, cache, i32(lens), i32(cu), i32(P), out=out, lse_out=lse,
+                                   workspace=ws)
+            assert tsa.workspace_status(ws) == 0
+            step = tsa.window_attn_decode if fmt == "bf16" else tsa.kv8_attn_decode
+            want, _ = step(q, cache, i32(lens), 0, None, lse_out=lse1)
+            empty = lse1.isinf()
+            assert torch.equal(lse.isinf(), empty) and (out[empty] == 0).all()
+            assert ((lse - lse1).abs()[~empty] <= 1e-4).all()
+            # fp32: both within decode_close of 64 bits (logits' terms add up to about 10, 4.4e-5
+            # of values of at most 6 each); bf16: half a step of the weights and of the result
+            vmax = 6.0 if fmt == "bf16" else float(max(6.0, 448 * cache.v_scale.max()))
+            tol = 1e-4 * vmax if dtype == torch.float32 else 2 * HALF * vmax
+            assert ((out.float() - want).abs() <= tol).all(), (turn, dtype)
+
+
 def test_a_run_of_forked_sequences(tsa):
     """A prompt with an image is written into pages, forked for samples, and the samples go
     on: pages taken, keys rotated by axes and written, attended with the prompt's rows read

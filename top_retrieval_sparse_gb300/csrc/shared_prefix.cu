@@ -81,7 +81,7 @@ constexpr float kRescale = 16.f, kMost = 65536.f;
 // one sign for every row and part of a weight): after so many of a stream's tiles O is added,
 // with rounding, to the sum in the workspace and begins again.
 template <int PARTS>
-constexpr int kFoldEvery = PARTS == 2 ? 32 : 128;
+constexpr int kFoldEvery = PARTS == 2 ? 16 : 128;
 
 template <int FMT>
 struct SharedBars {
