@@ -43,8 +43,8 @@
 // What bounds it (one call, the kernel alone).  64 sequences x 4 heads under 32767 rows of 8
 // KV heads, fp32: 46 us for 20 us of bytes and 27 us of matrix instructions (three products
 // of a tile); 12 us pass before the first product.  256 x 7 heads under 131071 rows of 4,
-// bf16: 310 us, 1550 TFLOP/s; the path from the logits to the first weights is a little
-// longer than the other stream's products.  8 groups of 8 x 4 heads under 115K rows of 8, e4m3: 590 us,
+// bf16: 306 us, 1570 TFLOP/s; the path from the logits to the first weights is a little
+// longer than the other stream's products.  8 groups of 8 x 4 heads under 115K rows of 8, e4m3: 595 us,
 // 3.1 TB/s of codes: a tile's chain of barriers, and the widening, 700 cycles a tile of K or
 // V.  Waits that read the global timer took 17 % more there, loops unrolled past the
 // instruction cache 27 %.
@@ -284,31 +284,33 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
 
         bool more = false;                   // a sum is in the workspace, under `under`
         float under = 0.f;
-        // 32 columns of O, and the sum in the workspace.
-        auto whole = [&](int c, float f, float (&o)[32]) {
-          load_cols(o_at + 32 * c, o);
-          if (more && live) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 u = __ldcg(sums + (8 * c + i) * rs);
-              o[4 * i] = fmaf(u.x, f, o[4 * i]);
-              o[4 * i + 1] = fmaf(u.y, f, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(u.z, f, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(u.w, f, o[4 * i + 3]);
-            }
-          }
-        };
+        // O to the sum in the workspace.  While the maximum is the one that the sum is under,
+        // it is added there, without a wait for what is there.
         auto put = [&]() {
           const float f = !more || under == m ? 1.f : ex2(Q8 ? under - m : (under - m) * sc);
+          const bool scaled = __any_sync(0xffffffffu, f != 1.f && live);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float o[32];
-            whole(c, f, o);
-            if (live)
+            __syncwarp();
+            load_cols(o_at + 32 * c, o);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                __stcg(sums + (8 * c + i) * rs,
-                       make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+            for (int i = 0; i < 8 && live; ++i) {
+              float4* at = sums + (8 * c + i) * rs;
+              float4 y = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              if (more && !scaled) {
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(y.x),
+                             "f"(y.y), "f"(y.z), "f"(y.w)
+                             : "memory");
+              } else {
+                if (more) {
+                  const float4 u = __ldcg(at);
+                  y = make_float4(fmaf(u.x, f, y.x), fmaf(u.y, f, y.y), fmaf(u.z, f, y.z),
+                                  fmaf(u.w, f, y.w));
+                }
+                __stcg(at, y);
+              }
+            }
           }
           more = true;
           under = m;
@@ -512,6 +514,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 float o[32] = {};
+                __syncwarp();
                 if (ok) load_cols(o_at + 32 * c, o);
                 if (live) {
 #pragma unroll
