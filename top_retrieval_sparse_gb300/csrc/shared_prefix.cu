@@ -87,9 +87,19 @@ constexpr int kFoldEvery = PARTS == 2 ? 24 : 128;
 
 template <int FMT>
 struct SharedBars {
-  uint64_t q[2], s[2], p[2][4], o[2], full[kSlots<FMT>], empty[kSlots<FMT>], clean[kSlots<FMT>],
-      drain[2], turn[2], raw_full[kRawSlots], raw_empty[kRawSlots], scale[kRawSlots];
+  uint64_t q[2], s[2], p[2][4], o[2], full[kSlots<FMT>], empty[kSlots<FMT>], drain[2], turn[2],
+      raw_full[kRawSlots], raw_empty[kRawSlots], scale[kRawSlots];
 };
+
+// A barrier tells its last two phases apart and no more, so a wait for a slot is right only once
+// the slot's item of the lap before is known to have landed.  A stream that passes by the other's
+// tiles (a unit of one key tile is stream A's alone) may be any number of laps ahead of the ring.
+// It therefore waits for the slots of a tile only when the zeroing warp, which passes all
+// tiles in order, has counted all but kLag of those before it.  With five slots a tile's two
+// items lie in those of the two tiles before the last one.  With three its V takes the slot of
+// the last tile's K, which has landed when its own K has, since operands of codes land in
+// order.
+constexpr uint32_t kLag = 1;
 
 // Slot i of the rings' endless rows, and the parity of its barriers there.
 template <int FMT>
@@ -147,6 +157,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
   __shared__ float4 scale_s[Q8 ? kRawSlots : 1][8];
   __shared__ float2 run_s[2][64];            // maxima and sums while copies are joined
   __shared__ uint32_t tmem_s;
+  __shared__ uint32_t passed_s;              // tiles that the zeroing warp has passed
   __shared__ volatile int abort_s;
   __shared__ volatile int bad_s[8];          // number of a segment that met a bad page
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -164,7 +175,6 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&bar.full[i], Q8 ? 4 : 1);
       mbar_init(&bar.empty[i], 3);
-      mbar_init(&bar.clean[i], 1);
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&bar.raw_full[i], 1);
@@ -172,6 +182,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
       mbar_init(&bar.scale[i], 1);
     }
     fence_mbar_init();
+    passed_s = 0u;
     abort_s = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
@@ -587,22 +598,19 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
       };
       // so far: tiles and segments of this stream, turns, tiles of the segments
       uint32_t tiles = 0, segs = 0, turns = 0, passed = 0;
+      uint32_t seen = 0;                     // of the zeroing warp's count
       bool ok = true;
       for (int seg = 0; ok && seg < n_seg; ++seg) {
         const bool both = segments[seg].both;
         const int j0 = segments[seg].j0, P = segments[seg].P;
         const int all = segments[seg].j1 - j0, n = both ? all : (all - x + 1) / 2;
         auto number = [&](int j) { return passed + (both ? j : 2 * j + x); };
-        // Before the slots of a tile are waited for, what was in them has to have landed, or
-        // their barriers' parity would stand for the lap before that; a stream that has not
-        // used those tiles itself learns it from the zeroing warp, which passes all in order.
-        auto landed_before = [&](uint32_t tile) {
-          return tile < 2 ||
-                 wait_long(&bar.clean[slot_of<FMT>(tile - 2)], lap_of<FMT>(tile - 2), &abort_s);
+        auto in_reach = [&](uint32_t tile) {  // its slots may be waited for
+          return tile <= kLag || wait_count(&passed_s, tile - kLag, seen, &abort_s);
         };
         if (n > 0) {
           const uint32_t i = 2 * number(0);
-          ok = wait_long(&bar.q[x], segs & 1, &abort_s) && landed_before(number(0)) &&
+          ok = wait_long(&bar.q[x], segs & 1, &abort_s) && in_reach(number(0)) &&
                wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (both && x == 1) ok = ok && wait_long(&bar.turn[1], turns & 1, &abort_s);
           if (ok) {
@@ -615,7 +623,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           const uint32_t tile = number(j), i = 2 * tile + 1;  // V's slot
           ok = wait_long(&bar.full[slot_of<FMT>(i)], lap_of<FMT>(i), &abort_s);
           if (!Q8 && ok && (j0 + (int)(tile - passed) + 1) * kTile > P)
-            ok = wait_long(&bar.clean[slot_of<FMT>(tile)], lap_of<FMT>(tile), &abort_s);
+            ok = wait_count(&passed_s, tile + 1, seen, &abort_s);
           const uint64_t vx = vd + slot_of<FMT>(i) * (kSlotBytes >> 4);
           const bool more = j % kFoldEvery<PARTS> > 0;
           const uint32_t parity = (tiles + j) & 1;
@@ -643,7 +651,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           commit_mma(&bar.empty[slot_of<FMT>(i)]);
           if (j + 1 < n) {
             const uint32_t k = 2 * number(j + 1);
-            ok = landed_before(number(j + 1)) &&
+            ok = in_reach(number(j + 1)) &&
                  wait_long(&bar.full[slot_of<FMT>(k)], lap_of<FMT>(k), &abort_s);
             if (!ok) break;
             qk(slot_of<FMT>(k));
@@ -758,7 +766,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           __syncwarp();
         }
         if (lane == 0) {
-          mbar_arrive(&bar.clean[slot_of<FMT>(tile)]);
+          raise_count(&passed_s, tile + 1);
           give(i + 1);
         }
       }

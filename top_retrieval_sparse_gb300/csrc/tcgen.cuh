@@ -224,4 +224,28 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
+// A count in shared memory that one thread raises: what it did before is seen by a thread that
+// has found the count.  The wait is bounded as wait_long's are; `seen` is what the thread knows
+// of the count.
+__device__ __forceinline__ void raise_count(uint32_t* count, uint32_t to) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(to)
+               : "memory");
+}
+__device__ __forceinline__ bool wait_count(const uint32_t* count, uint32_t least, uint32_t& seen,
+                                           volatile int* abort) {
+  if (seen >= least) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  do {
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];"
+                 : "=r"(seen)
+                 : "r"(smem_u32(count))
+                 : "memory");
+    if (seen >= least) return true;
+    __nanosleep(40);
+  } while (!*abort && clock64() - t0 < 1ll << 31);
+  *abort = 1;
+  return false;
+}
+
 }  // namespace tsa
