@@ -313,3 +313,19 @@ def test_pages_on_streams_and_in_graphs(tsa):
         assert int(moves[2]) == len(m.compact())
         assert m.same(pages)
     assert tsa.workspace_status(pages.workspace) == 0
+
+
+@pytest.mark.parametrize("entry", [1, 5, 6, 9], ids=["free below", "free above", "outside", "far outside"])
+def test_compaction_flags_every_wrong_entry(tsa, entry):
+    """One entry that names no page in use, the only wrong one: left as it is and flagged.  (A free
+    page below those in use is a hole that another page moves into.)"""
+    def run(last):
+        pages = tsa.Pages(i32([[0, 2, 4, -1], [last, -1, -1, -1]]), i32([1, 0, 1, 0, 1, 0]), 16)
+        src, dst, count = tsa.pages_compact(pages)
+        assert src.tolist() == [4, -1, -1] and dst.tolist() == [1, -1, -1] and int(count) == 1
+        assert pages.table.tolist() == [[0, 2, 1, -1], [last, -1, -1, -1]]
+        assert pages.refs.tolist() == [1, 1, 1, 0, 0, 0]
+        return int(tsa.lib().tsa_workspace_status(pages.workspace.data_ptr(), 1, None))
+
+    assert run(-1) == 0 and run(-7) == 0
+    assert run(entry) != 0

@@ -376,10 +376,12 @@ __global__ void __launch_bounds__(kThreads) pages_follow_kernel(PagesArgs a) {
 #pragma unroll 4
   for (int64_t e = at; e < (int64_t)a.B * a.max_pages; e += step) {
     const int page = a.table[e];
-    if (page < live) continue;
+    if (page < 0) continue;
+    // (a page outside the pool, or one that counts as free: below `live` a hole that another
+    // page moves into)
     if (page >= a.n_pages || (a.free_bits[page / 32] >> (page % 32)) & 1u)
-      bad = true;  // a page outside the pool, or one that counts as free
-    else
+      bad = true;
+    else if (page >= live)
       a.table[e] = a.dst[a.rank[page]];
   }
   if (bad) atomicOr(a.status, kStatusBadLength);
