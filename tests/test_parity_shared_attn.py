@@ -486,3 +486,31 @@ def test_a_run_of_forked_sequences(tsa):
             assert int(pages.table.max()) == used - 1
     assert int(pages.refs.sum()) == int((pages.table >= 0).sum())
     assert tsa.workspace_status(pages.workspace) == 0 and tsa.workspace_status(cache.status) == 0
+
+
+@pytest.mark.parametrize("cap", [256, 20480], ids=["small", "large"])
+def test_shared_rows_past_the_cache_are_clamped(tsa, cap):
+    """shared[n] and lens[b] beyond the capacity stand for the capacity, and are flagged; a
+    sequence shorter than that is still shorter than its shared rows."""
+    g = gen(21)
+    Hq, Hkv, page = 4, 2, 16
+    kv, _ = bf16_cache(tsa, g, 5, Hkv, cap, page)
+    q = randn(g, 5, Hq, D).bfloat16()
+    ws = tsa.shared_attn_decode_workspace(5, 2, Hq, Hkv)
+
+    def run(lens, shared):
+        lse = torch.empty((5, Hq), device=DEV)
+        out, _ = tsa.shared_attn_decode(q, kv, i32(lens), i32([0, 3, 5]), i32(shared), lse_out=lse,
+                                        workspace=ws)
+        return out, lse, int(tsa.lib().tsa_workspace_status(ws.data_ptr(), 1, None))
+
+    want, lse, s = run([cap, cap, cap, 90, 100], [cap, 80])
+    assert s == 0 and not want.isnan().any()
+    for lens, shared in (([cap] * 3, cap + 1), ([cap] * 3, 2 ** 31 - 1), ([cap + 5, cap, cap + 1], cap),
+                         ([cap + 5] * 3, cap + 9)):
+        out, l, s = run(lens + [90, 100], [shared, 80])
+        assert s != 0 and torch.equal(out, want) and torch.equal(l, lse)
+    out, l, s = run([cap, cap - 1, 0, 90, 100], [cap + 1, 80])
+    assert s != 0 and out[1].isnan().all() and l[1].isnan().all() and (out[2] == 0).all()
+    # (other own rows cut the work elsewhere: as in test_bad_input_is_flagged)
+    assert torch.allclose(out[[0, 3, 4]], want[[0, 3, 4]], rtol=0, atol=1e-4)

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(SharedArgs a)
       const int P = a.shared[n], L = a.lens[b];
       start = P < 0 ? 0 : (P > a.c.l_cap ? (int)a.c.l_cap : P);
       if (a.leader) a.leader[b] = cu_s[n];
-      if (L > 0 && L < P) {
+      if (L > 0 && L < start) {
         atomicOr(a.status, kStatusBadLength);
         n = kNoGroups;
       }
