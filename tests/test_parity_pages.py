@@ -1,5 +1,6 @@
 """The page operators against a model of lists on the host: pages taken, given back,
 shared, moved and copied.  Whole numbers throughout, so everything is equal."""
+import ctypes
 import random
 
 import pytest
@@ -329,3 +330,41 @@ def test_compaction_flags_every_wrong_entry(tsa, entry):
 
     assert run(-1) == 0 and run(-7) == 0
     assert run(entry) != 0
+
+
+def test_large_calls_of_several_host_threads(tsa):
+    """Pools and batches of different sizes, whose kernels ask for different amounts of shared
+    memory, from two host threads at once: no launch is refused."""
+    import threading
+    L, codes = tsa.lib(), []
+
+    def pools(n):
+        pages = tsa.Pages.empty(2, 64, n, 16)
+        lo, hi, st = i32([0, 0]), i32([16, 32]), torch.cuda.Stream()
+        args = (pages._ref, lo.data_ptr(), hi.data_ptr(), pages._ws, pages._ws_bytes,
+                st.cuda_stream)
+        return L.pages_alloc, args, (pages, lo, hi, st)
+
+    def steps(B):
+        pt = torch.arange(B, dtype=torch.int32, device=DEV).view(B, 1)
+        k = torch.zeros((B, 1, 16, 128), dtype=torch.bfloat16, device=DEV)
+        q, lens = torch.zeros((B, 1, 128), dtype=torch.bfloat16, device=DEV), i32([3] * B)
+        out, ws = torch.empty((B, 1, 128), device=DEV), tsa.attn_decode_workspace(B, 1, 1)
+        kv, st = tsa.kv_paged(k, k, pt), torch.cuda.Stream()
+        args = (q.data_ptr(), ctypes.byref(kv.struct), lens.data_ptr(), B, 1, 1, 128, 0, 1 << 30,
+                0.1, out.data_ptr(), None, ws.data_ptr(), ws.nbytes, st.cuda_stream)
+        return L.window_attn_decode, args, (pt, k, q, lens, out, ws, kv, st)
+
+    def loop(fn, args):
+        codes.append({fn(*args) for _ in range(4000)})
+
+    for make, sizes in ((pools, (1 << 22, 1 << 23)), (steps, (4096, 3500))):
+        calls = [make(n) for n in sizes]
+        torch.cuda.synchronize()
+        threads = [threading.Thread(target=loop, args=c[:2]) for c in calls]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+    assert codes == [{0}] * 4

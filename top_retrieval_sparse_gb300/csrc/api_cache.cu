@@ -114,7 +114,8 @@ int check_tokens(int64_t T, int max_n, const int32_t* cu, int B, const char* wha
 
 int check_batch(int B, int Hkv, int d) {
   if (d != kD) return fail(TSA_ERR_INVALID_ARG, "d = %d: only d = 128 is compiled", d);
-  if (B < 0 || B > 4096) return fail(TSA_ERR_INVALID_ARG, "B = %d: must be in [0, 4096]", B);
+  if (B < 0 || B > kMostSequences)
+    return fail(TSA_ERR_INVALID_ARG, "B = %d: must be in [0, %d]", B, kMostSequences);
   if (Hkv <= 0 || Hkv > 1024)
     return fail(TSA_ERR_INVALID_ARG, "Hkv = %d: must be in [1, 1024]", Hkv);
   return TSA_OK;

@@ -8,10 +8,6 @@ using namespace tsa;
 
 namespace {
 
-// More pages than this (134 million positions in pages of 16) would not fit the
-// snapshot's prefix in shared memory.
-constexpr int kMostPages = 1 << 23;
-
 bool pages_sizes(int B, int max_pages, int n_pages) {
   return B >= 0 && B <= 4096 && max_pages > 0 && n_pages > 0 && n_pages <= kMostPages &&
          (int64_t)B * max_pages < (int64_t)1 << 31;

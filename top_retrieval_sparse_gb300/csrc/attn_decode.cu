@@ -730,15 +730,19 @@ auto kernel_of(int fmt) {
 int attn_decode_ctas(int fmt) { return ctas_of(fmt); }
 
 cudaError_t launch_attn_decode(const DecodeArgs& a, int fmt, int grid, cudaStream_t st) {
-  const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
+  const auto list_bytes = [](int B) { return (size_t)(B + 1) * sizeof(int64_t); };
+  const size_t smem = list_bytes(a.B);
   const dim3 g(grid), th(kDecodeThreads);
   const int rows = !a.start ? kWindow : (a.leader ? kBoth : kOwn);
   const auto kernel = rows == kWindow ? kernel_of<kWindow>(fmt)
                       : rows == kOwn  ? kernel_of<kOwn>(fmt)
                                       : kernel_of<kBoth>(fmt);
   if (smem > 24 * 1024) {  // with the static arrays: past the default limit
-    const cudaError_t e = cudaFuncSetAttribute(
-        (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the most that any call asks for: the limit belongs to the kernel, and another host
+    // thread's smaller one would refuse this launch)
+    const cudaError_t e =
+        cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)list_bytes(kMostSequences));
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kernel, g, th, smem, st, a);

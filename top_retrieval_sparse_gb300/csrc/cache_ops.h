@@ -127,6 +127,8 @@ struct ReadArgs {
 };
 cudaError_t launch_kv8_read(const ReadArgs& a, cudaStream_t st);
 
+constexpr int kMostSequences = 4096;  // of a batch
+
 // One decode step (attn_decode.cu).
 constexpr int kNoGroups = -2;
 constexpr int kDecodeThreads = 128;

@@ -441,8 +441,11 @@ template <typename K>
 cudaError_t with_prefix(K kernel, dim3 grid, const PagesArgs& a, cudaStream_t st) {
   const size_t smem = prefix_bytes(a.n_pages);
   if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        (const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the most that any call asks for: the limit belongs to the kernel, and another host
+    // thread's smaller one would refuse this launch)
+    const cudaError_t e =
+        cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)prefix_bytes(kMostPages));
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kernel, grid, dim3(kThreads), smem, st, a);

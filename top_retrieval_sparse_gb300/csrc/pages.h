@@ -7,6 +7,9 @@
 namespace tsa {
 
 constexpr int kPagesChunk = 256;  // pages of a count in the snapshot
+// More pages than this (134 million positions in pages of 16) would not fit the
+// snapshot's prefix in shared memory.
+constexpr int kMostPages = 1 << 23;
 enum PagesKind : int { kPagesTake = 0, kPagesFork = 1, kPagesCompact = 2 };
 
 struct PagesArgs {
