@@ -617,7 +617,8 @@ TSA_API int pages_compact(const tsa_pages* pages, int32_t* src, int32_t* dst, in
  * 0: nothing.  No dst may be named twice or be a src as well.  bufs: host array; a buffer
  * is [n_pages][bytes] (the K, V or scales of a layer: Hkv * page_size rows or blocks).
  * data 4-byte aligned, bytes a multiple of 4 (16 for both is faster).  Pages outside
- * [0, n_pages) are skipped, and flagged in status (NULL, or as tsa_kv8's). */
+ * [0, n_pages) are skipped, and flagged in status (NULL, or as tsa_kv8's; the workspace of
+ * the other calls begins with such a word). */
 typedef struct tsa_page_buf {
   void* data;
   int64_t bytes;

@@ -368,3 +368,22 @@ def test_large_calls_of_several_host_threads(tsa):
             t.join()
         torch.cuda.synchronize()
     assert codes == [{0}] * 4
+
+
+def test_copies_of_bf16_pages_report_to_the_pages(tsa):
+    """A bf16 cache has no status word: pages outside the pool are flagged in the workspace of
+    the Pages given."""
+    k = torch.randn((7, 2, 16, 128), device=DEV).bfloat16()
+    pages = tsa.Pages.empty(2, 4, 7, 16)
+    kv = tsa.kv_paged(k, k.clone(), pages.table)
+    want = k.clone()
+    want[1] = want[0]
+    tsa.pages_copy(kv, i32([0]), i32([1]), pages=pages)
+    assert torch.equal(kv.k, want) and tsa.workspace_status(pages.workspace) == 0
+    tsa.pages_copy([kv, kv], i32([7, 0, -1]), i32([2, 7, 9]), pages=pages)
+    assert torch.equal(kv.k, want)
+    assert int(tsa.lib().tsa_workspace_status(pages.workspace.data_ptr(), 1, None)) != 0
+    cache = tsa.KV8.paged(7, 2, 16, pages.table, 16, "int8")
+    tsa.pages_copy([kv, cache], i32([7]), i32([2]), pages=pages)   # a cache's own word first
+    assert tsa.workspace_status(pages.workspace) == 0
+    assert int(tsa.lib().tsa_workspace_status(cache.status.data_ptr(), 1, None)) != 0

@@ -1187,10 +1187,12 @@ def pages_compact(pages: Pages, src: Optional[torch.Tensor] = None,
 
 
 def pages_copy(caches, src: torch.Tensor, dst: torch.Tensor,
-               count: Optional[torch.Tensor] = None, stream=None) -> None:
+               count: Optional[torch.Tensor] = None, stream=None,
+               pages: Optional[Pages] = None) -> None:
     """Copies page src[i] over page dst[i] (int32 [n], -1: none) in every cache given (a
     paged KV or KV8, or a list of them, of one pool size); count: int32 [1], how many
-    pairs count."""
+    pairs count.  Pages outside the pool are skipped, and flagged in the first status word
+    among the caches, or, where none has one (bf16 caches), in the workspace of `pages`."""
     if not isinstance(caches, (list, tuple)):
         caches = (caches,)
     n = src.numel()
@@ -1210,6 +1212,10 @@ def pages_copy(caches, src: torch.Tensor, dst: torch.Tensor,
         if c.k.device != dev:
             _gpu((src, "src"), (c.k, "a cache"))
         status = status or getattr(c, "_status", None)
+    if pages is not None:
+        if pages.device != dev:
+            _gpu((src, "src"), (pages.table, "pages"))
+        status = status or pages._ws
     if dst.device != dev or dev.type != "cuda" or count is not None and count.device != dev:
         _gpu((src, "src"), (dst, "dst"), (count, "count"))
     if n_pages == 0:
