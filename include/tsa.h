@@ -597,8 +597,9 @@ TSA_API int pages_free(const tsa_pages* pages, const int32_t* lo, const int32_t*
  * -1; the pages that it held count one entry less (and are not given out by this call).
  * Entries that the parent has not are -1 in the child too.  One parent may have many
  * children.  If a child is named twice or is a parent of the same call, an index or a
- * length is out of range, a parent's entry is outside the pool, or the free pages do not
- * suffice, nothing changes, src and dst are -1, and that is flagged. */
+ * length is out of range, a parent's entry names a page outside the pool or one that counts
+ * as free, or the free pages do not suffice, nothing changes, src and dst are -1, and that is
+ * flagged; so are such entries of a child, which are replaced all the same. */
 TSA_API int pages_fork(const tsa_pages* pages, const int32_t* parents, const int32_t* children,
                        const int32_t* lens, int n, int32_t* src, int32_t* dst, void* workspace,
                        size_t ws_bytes, void* stream);

@@ -387,3 +387,32 @@ def test_copies_of_bf16_pages_report_to_the_pages(tsa):
     tsa.pages_copy([kv, cache], i32([7]), i32([2]), pages=pages)   # a cache's own word first
     assert tsa.workspace_status(pages.workspace) == 0
     assert int(tsa.lib().tsa_workspace_status(cache.status.data_ptr(), 1, None)) != 0
+
+
+def test_a_fork_onto_entries_that_name_free_pages(tsa):
+    """A child's old entries may name pages that count as free (a state that no call leaves), the
+    very page that the fork gives out among them: flagged, and the page counts once."""
+    for row in ([-1, 2, -1, -1], [2, -1, -1, -1], [-1, -1, 2, -1], [-1, -1, 3, 9]):
+        for _ in range(20):
+            pages = tsa.Pages(i32([[0, 1, -1, -1], row]), i32([1, 1, 0, 0, 0, 0]), 16)
+            src, dst = tsa.pages_fork(pages, i32([0]), i32([1]), i32([24]))
+            assert (int(src), int(dst)) == (1, 2)
+            assert pages.table.tolist() == [[0, 1, -1, -1], [0, 2, -1, -1]]
+            assert pages.refs.tolist() == [2, 1, 1, 0, 0, 0]
+            assert int(tsa.lib().tsa_workspace_status(pages.workspace.data_ptr(), 1, None)) != 0
+
+
+def test_a_fork_of_entries_that_name_free_pages(tsa):
+    """A parent's entry that names a page that counts as free: nothing changes, and it is
+    flagged; behind the forked positions it does not matter."""
+    for take, good in ((40, False), (48, False), (16, False), (33, False), (0, True)):
+        pages = tsa.Pages(i32([[3, 1, 0, -1], [-1] * 4]), i32([1, 1, 0, 0, 0, 0]), 16)
+        t, r = pages.table.clone(), pages.refs.clone()
+        src, dst = tsa.pages_fork(pages, i32([0]), i32([1]), i32([take]))
+        status = int(tsa.lib().tsa_workspace_status(pages.workspace.data_ptr(), 1, None))
+        assert (status == 0) == good and int(src) == int(dst) == -1
+        assert torch.equal(pages.table, t) and torch.equal(pages.refs, r)
+    pages = tsa.Pages(i32([[0, 1, 3, -1], [-1] * 4]), i32([1, 1, 0, 0, 0, 0]), 16)
+    src, dst = tsa.pages_fork(pages, i32([0]), i32([1]), i32([24]))
+    assert (int(src), int(dst)) == (1, 2) and pages.refs.tolist() == [2, 1, 1, 0, 0, 0]
+    assert tsa.workspace_status(pages.workspace) == 0

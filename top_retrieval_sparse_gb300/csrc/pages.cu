@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(kThreads) pages_snapshot_kernel(PagesArgs a) {
         bad |= a.parents[k] == f.child || (k != i && a.children[k] == f.child);
       const int32_t* row = a.table + (int64_t)f.parent * a.max_pages;
 #pragma unroll 4
-      for (int j = threadIdx.x; j < f.full + f.part; j += kThreads) bad |= row[j] >= a.n_pages;
+      for (int j = threadIdx.x; j < f.full + f.part; j += kThreads) {
+        const int page = row[j];
+        bad |= page >= a.n_pages || (page >= 0 && a.refs[page] == 0);
+      }
       bad = block_sum(bad, scratch);
     }
     if (threadIdx.x == 0) {
@@ -164,6 +167,10 @@ __global__ void __launch_bounds__(kThreads) pages_snapshot_kernel(PagesArgs a) {
   }
 }
 
+// Whether a page of the pool was free in the snapshot.
+__device__ __forceinline__ bool is_free(const PagesArgs& a, int page) {
+  return (a.free_bits[page / 32] >> (page % 32)) & 1u;
+}
 // Counts before every chunk into shared memory; returns how many pages are free.
 __device__ int chunk_prefix(const PagesArgs& a, int* before, int* scratch) {
   const int chunks = (a.n_pages + kPagesChunk - 1) / kPagesChunk;
@@ -316,9 +323,11 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(PagesArgs a) {
   for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.max_pages; j += gridDim.x * kThreads) {
     const int was = to[j];
     const int now = j < f.full ? from[j] : (j == f.full ? fresh : -1);
-    if (was == now) continue;
+    // (an entry of a page that counted as free: it may be the one given out here)
+    const bool stale = was >= 0 && was < a.n_pages && is_free(a, was);
+    if (was == now && !stale) continue;
     if (now >= 0) atomicAdd(a.refs + now, 1);
-    if (was >= 0) wrong |= !let_go(a, was);
+    if (was >= 0) wrong |= stale || !let_go(a, was);
     to[j] = now < 0 ? -1 : now;
   }
   if (wrong) atomicOr(a.status, kStatusBadLength);
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) pages_moves_kernel(PagesArgs a) {
        k += gridDim.x * kThreads)
     a.src[k] = a.dst[k] = -1;
   for (int p = blockIdx.x * kThreads + threadIdx.x; p < a.n_pages; p += gridDim.x * kThreads) {
-    const bool free = (a.free_bits[p / 32] >> (p % 32)) & 1u;
+    const bool free = is_free(a, p);
     if (p < live) {
       if (free) a.dst[free_below(a, before, p)] = p;
     } else if (!free) {
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) pages_follow_kernel(PagesArgs a) {
     if (page < 0) continue;
     // (a page outside the pool, or one that counts as free: below `live` a hole that another
     // page moves into)
-    if (page >= a.n_pages || (a.free_bits[page / 32] >> (page % 32)) & 1u)
+    if (page >= a.n_pages || is_free(a, page))
       bad = true;
     else if (page >= live)
       a.table[e] = a.dst[a.rank[page]];
