@@ -134,3 +134,48 @@ def test_many_short_units_and_a_long_one_in_random_order(tsa, fmt):
         # up to 20, relative to values of at most 22 and sums of weights: 4e-4
         assert ((lse - lse1).abs() <= 8e-4).all(), turn
         assert ((out - want).abs() <= 8e-4 * 22).all(), turn
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_many_calls_over_codes_in_the_second_level_cache(tsa, fmt):
+    """Codes that are copied as fast as their slots are given back: hundreds of calls give what
+    the first gave, and that is right."""
+    rng = __import__("random").Random(8)
+    g = gen(31)
+    for G, Hkv in ((5, 2), (7, 4), (8, 8)):
+        shared = [rng.choice([rng.randint(1, 128), rng.randint(129, 3000), rng.randint(300, 9000)])
+                  for _ in range(40)]
+        sizes = [rng.choice([1, 2, 5, 16]) for _ in shared]
+        cu = [sum(sizes[:i]) for i in range(len(sizes) + 1)]
+        lens = [shared[n] + b % 4 for n, s in enumerate(sizes) for b in range(s)]
+        B, Hq = len(lens), G * Hkv
+        table, k, v = pool_of(g, cu, shared, lens, Hkv, 256)
+        cache = tsa.KV8.paged(k.shape[0], Hkv, PS, table, 64, fmt)
+        for x, scale, codes in ((k, cache.k_scale, cache.k), (v, cache.v_scale, cache.v)):
+            scale.fill_(2.0 ** -2)
+            codes.copy_((x.float() * 4).round().clamp(-127, 127) + 128 if fmt == "int8" else
+                        (x.float() * 4).to(torch.float8_e4m3fn).view(torch.uint8))
+        pool = values(cache)
+
+        def rows(b, h):
+            used = table[b, : -(-lens[b] // PS)].long().clamp(min=0)
+            return tuple(x[used, h].reshape(-1, D) for x in pool)
+
+        def steps(b, h):
+            return torch.full((-(-lens[b] // PS) * PS,), 0.25, dtype=torch.float64, device=DEV)
+
+        q = randn(g, B, Hq, D).bfloat16()
+        lse = torch.empty((B, Hq), device=DEV)
+        ws = tsa.shared_attn_decode_workspace(B, len(shared), Hq, Hkv)
+        args = (q, cache, i32(lens), i32(cu), i32(shared))
+        for dtype in (torch.bfloat16, torch.float32):
+            out, again = (torch.empty((B, Hq, D), dtype=dtype, device=DEV) for _ in range(2))
+            tsa.shared_attn_decode(*args, out=out, lse_out=lse, workspace=ws)
+            check(q, rows, lens, cu, shared, Hkv, out, lse, steps=steps,
+                  only=[b for b in range(B) if b % 5 == 0])
+            wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+            for _ in range(250):
+                tsa.shared_attn_decode(*args, out=again, workspace=ws)
+                wrong += (again != out).any()
+            assert int(wrong) == 0
+        assert tsa.workspace_status(ws) == 0

@@ -104,10 +104,11 @@ class Barrier:
 class Ring:
     """The segments of a share, [(key tiles, both streams, V's last rows zeroed)].  `lag`: tiles
     that a stream may wait ahead of the zeroing warp's count; None: a wait by parity in its
-    place (what the count is there for)."""
+    place (what the count is there for).  `returned`: codes are given back when their loads have
+    returned; else a load may find what its slot holds later."""
 
-    def __init__(self, segs, q8, lag):
-        self.segs, self.q8, self.lag = segs, q8, lag
+    def __init__(self, segs, q8, lag, returned=True):
+        self.segs, self.q8, self.lag, self.returned = segs, q8, lag, returned
         self.S, self.raw = slots(q8), number("shared_prefix.cu", r"kRawSlots = (\d)")
         self.tiles = []                     # of every tile: (both, stream, zeroed)
         for n, both, tail in segs:
@@ -185,12 +186,16 @@ class Ring:
                 self.scale_holds[tile % self.raw] = tile
                 self.scale[tile % self.raw].arrive()
             yield lambda: self.raw_full[r].passed(it // self.raw & 1)
-            if self.raw_holds[r] != it:
-                raise Wrong("codes of another tile are widened")
-            self.taken[it] = self.taken.get(it, 0) + 1
-            self.raw_empty[r].arrive()
             if it >= self.S:
                 yield lambda: self.empty[it % self.S].passed(it // self.S & 1 ^ 1)
+            self.taken[it] = self.taken.get(it, 0) + 1
+            if not self.returned:
+                self.raw_empty[r].arrive()
+                yield lambda: True
+            if self.raw_holds[r] != it:
+                raise Wrong("codes of another tile are widened")
+            if self.returned:
+                self.raw_empty[r].arrive()
             self.free(it)
             self.holds[it % self.S][w] = it
             self.full[it % self.S].arrive()
@@ -325,15 +330,23 @@ def lag():
     return number("shared_prefix.cu", r"constexpr uint32_t kLag = (\d+);")
 
 
+def loads_returned():
+    """Whether who gives a slot of codes back depends on all that was loaded from it."""
+    return re.search(r"any \|= c\[e\]\.x \| c\[e\]\.y \| c\[e\]\.z \| c\[e\]\.w;\s+"
+                     r"const int by = __any_sync\(0xffffffffu, any != 0u\) \? 0 : 1;\s+"
+                     r"__syncwarp\(\);\s+if \(lane == by\) mbar_arrive\(&bar\.raw_empty",
+                     source("shared_prefix.cu")) is not None
+
+
 HELD = [None, "copy", "zero", "land", "matrix0", "matrix1", "softmax0", "softmax1", "tensor0",
         "tensor1", "widen0", "widen3"]
 
 
-def schedules(lists, q8, ahead, runs):
+def schedules(lists, q8, ahead, runs, returned=None):
     for seed in range(runs):
         rng = random.Random(seed)
-        Ring(lists(rng), q8, ahead).run(rng, rng.choice(HELD[: None if q8 else 10]),
-                                        rng.choice([1, 10, 10 ** 9]))
+        ring = Ring(lists(rng), q8, ahead, loads_returned() if returned is None else returned)
+        ring.run(rng, rng.choice(HELD[: None if q8 else 10]), rng.choice([1, 10, 10 ** 9]))
 
 
 def short_before_long(rng):
@@ -365,6 +378,11 @@ def test_no_schedule_breaks_the_ring(q8, lists):
 def test_the_model_sees_a_stream_that_takes_another_lap(q8, lists, ahead):
     with pytest.raises(Wrong):
         schedules(lists, q8, ahead and ahead(), 1500)
+
+
+def test_the_model_sees_codes_that_are_given_back_before_their_loads_return():
+    with pytest.raises(Wrong, match="codes of another tile"):
+        schedules(mixed, True, lag(), 1500, returned=False)
 
 
 # Batches (sequences of every group, their shared rows, query heads of a KV head, KV heads) in

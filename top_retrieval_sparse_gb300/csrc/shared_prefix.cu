@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
           const uint32_t i = 2 * tile + w;
           ok = wait(&bar.raw_full[raw_slot(i)], raw_lap(i));
           if (!ok) break;
-          // The codes wait in registers for the operand's slot, and theirs is free again.
+          // The codes wait in registers for the operand's slot.
           const uint32_t from = raw + raw_slot(i) * kRawBytes, to = ring + slot_of<FMT>(i) * kSlotBytes;
           uint4 c[8];
 #pragma unroll
@@ -827,13 +827,24 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
                          : "r"(from + (row0 + n / 2 * 32) * kD + piece * 16)
                          : "memory");
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.raw_empty[raw_slot(i)]);
           if (i >= SLOTS) ok = wait(&bar.empty[slot_of<FMT>(i)], lap_of<FMT>(i) ^ 1);
           if (!ok) break;
           // (rows 8 apart have the same swizzle)
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
+            if (n == 2) {
+              // The codes' slot is free, but not before all loads have returned: one that is
+              // still on its way (the products keep shared memory busy) would find the codes of
+              // the next lap, so which lane arrives depends on what they brought.  (Arriving
+              // without that: 654 us for the documents below, and tiles that were torn.  Before
+              // the first piece 703, before the third 684, before the seventh 693.)
+              uint32_t any = 0u;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) any |= c[e].x | c[e].y | c[e].z | c[e].w;
+              const int by = __any_sync(0xffffffffu, any != 0u) ? 0 : 1;
+              __syncwarp();
+              if (lane == by) mbar_arrive(&bar.raw_empty[raw_slot(i)]);
+            }
             const int row = row0 + n / 2 * 32, piece = ch ^ (n & 1) << 2;
             uint4 y, z;
             widen<FMT>(c[n].x, y.x, y.y);
