@@ -717,6 +717,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             ok = Q8 ? wait(&bar.raw_empty[sl], raw_lap(it) ^ 1)
                     : wait(&bar.empty[sl], lap_of<FMT>(it) ^ 1);
           if (!ok) break;
+          if (Q8) fence_proxy_async();  // (behind the widening warps' reads of the slot)
           if (lane == 0) mbar_expect_tx(landed, bytes);
           __syncwarp();
           if (row >= 0)
