@@ -416,3 +416,14 @@ def test_a_fork_of_entries_that_name_free_pages(tsa):
     src, dst = tsa.pages_fork(pages, i32([0]), i32([1]), i32([24]))
     assert (int(src), int(dst)) == (1, 2) and pages.refs.tolist() == [2, 1, 1, 0, 0, 0]
     assert tsa.workspace_status(pages.workspace) == 0
+
+
+def test_a_pool_without_sequences(tsa):
+    pages = tsa.Pages.empty(0, 4, 10, 16)
+    none = i32([])
+    tsa.pages_alloc(pages, none, none)
+    tsa.pages_free(pages, none, none)
+    assert tsa.pages_fork(pages, none, none, none)[0].numel() == 0
+    src, dst, count = tsa.pages_compact(pages)
+    assert int(count) == 0 and (src == -1).all() and (dst == -1).all()
+    assert (pages.refs == 0).all() and tsa.workspace_status(pages.workspace) == 0

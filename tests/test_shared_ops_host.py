@@ -216,3 +216,12 @@ def test_what_the_binding_refuses_about_pages_and_groups(tsa):
         tsa.shared_attn_decode(q[:1], kv, i(2), i(2), i(1))
     with pytest.raises(ValueError, match="CUDA"):
         tsa.shared_attn_decode(q, kv, i(2), i(2), i(1))
+
+
+def test_a_pool_without_sequences_needs_no_table(tsa):
+    for name in ALL[:2]:
+        assert _call(tsa, name, _pages(tsa, B=0, table=None), lo=None, hi=None) == 0
+    assert _call(tsa, "pages_fork", _pages(tsa, B=0, table=None), n=0) == 0
+    for name in ALL:
+        _refused(tsa, _call(tsa, name, _pages(tsa, B=1, table=None)))
+        _refused(tsa, _call(tsa, name, _pages(tsa, B=0, refs=None)))

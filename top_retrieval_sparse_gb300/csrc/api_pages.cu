@@ -41,7 +41,8 @@ int check_pages(const tsa_pages* p, void* ws, size_t bytes, PagesArgs& a) {
                 "max_pages < 2^31", p->B, p->n_pages, p->max_pages);
   if ((int64_t)p->max_pages * ps >= (int64_t)1 << 31)
     return fail(TSA_ERR_INVALID_ARG, "max_pages * page_size must be < 2^31");
-  if (!p->table || !p->refs) return fail(TSA_ERR_INVALID_ARG, "table and refs must be non-NULL");
+  if ((!p->table && p->B > 0) || !p->refs)
+    return fail(TSA_ERR_INVALID_ARG, "table and refs must be non-NULL");
   if (!aligned(p->table, 4) || !aligned(p->refs, 4))
     return fail(TSA_ERR_INVALID_ARG, "table and refs must be 4-byte aligned");
   const Layout l = layout_of(p->B, p->n_pages);
