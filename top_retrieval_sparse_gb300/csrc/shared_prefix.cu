@@ -27,9 +27,15 @@
 // five 32 KB slots by TMA (two 64-column boxes with the 128-byte swizzle; a box a page where
 // pages are smaller than a tile), which runs on across segments.  A slot is filled again
 // when its three readers have given it back: both matrix threads, or one and the zeroing
-// warp for the other, and the zeroing warp.  It passes every slot in order.  Weights are
-// handed to the second product by quarters of a tile (by halves 22 us more of 409, 256
+// warp for the other, and the zeroing warp.  It passes every slot in order and counts the
+// tiles; a stream that has passed by tiles of the other waits for that count (kLag).  Weights
+// are handed to the second product by quarters of a tile (by halves 22 us more of 409, 256
 // queries' worth of samples under 131071 rows).
+//
+// Registers.  The compiler spills 232 bytes of the form for bf16 caches with fp32 output, 92 of
+// that with bf16 output and 76 to 80 of those for 8-bit caches.  Loads and stores of spills are
+// 1.8, 0.7 and at most 0.07 % of the instructions that run (counters, the cases below): a
+// few a key tile in the first two, a few a segment in the others.
 //
 // 8-bit caches.  Codes come by TMA into a ring of four 16 KB slots; warps 12-15 widen them to
 // fp16 (exact) into three operand slots, zeroing V's rows behind P, and find the blocks'
@@ -37,17 +43,22 @@
 // factor of the logits, the values' belongs to the weights and is taken out of their sum.
 //
 // Numbers.  The weights enter the second product in two parts where the output is fp32
-// (2^-18 of a weight left out in bf16, 2^-22 in fp16), in one where it is bf16.  (A third
-// bf16 part has no room in tensor memory beside the logits.)
+// (2^-18 of a weight left out in bf16, 2^-22 in fp16; a third bf16 part has no room in tensor
+// memory beside the logits), in one where it is bf16, as in the prompt kernel.  There the
+// weights' errors are of the size of the output's own rounding and independent of each
+// other: 256 x 7 heads under 131071 rows are 2.4e-3 off 64 bits where rounding alone leaves
+// 1.66e-3, and take 396 us; with two parts 1.66e-3 and 558.  e4m3 (one fp16 part has 11 bits): 1.67e-3
+// for 1.66e-3, 683 us for 768.
 //
 // What bounds it (one call, the kernel alone).  64 sequences x 4 heads under 32767 rows of 8
 // KV heads, fp32: 46 us for 20 us of bytes and 27 us of matrix instructions (three products
 // of a tile); 12 us pass before the first product.  256 x 7 heads under 131071 rows of 4,
 // bf16: 306 us, 1570 TFLOP/s; the path from the logits to the first weights is a little
-// longer than the other stream's products.  8 groups of 8 x 4 heads under 115K rows of 8, e4m3: 595 us,
-// 3.1 TB/s of codes: a tile's chain of barriers, and the widening, 700 cycles a tile of K or
-// V.  Waits that read the global timer took 17 % more there, loops unrolled past the
-// instruction cache 27 %.
+// longer than the other stream's products.  8 groups of 8 x 4 heads under 115K rows of 8, e4m3: 623 us,
+// 2.96 TB/s of codes: a tile's chain of barriers, and shared memory (a tile moves 224 KB through
+// it: 32 copied in, 32 read and 64 written by the widening warps, 96 read by the products).
+// Waits that read the global timer took 17 % more there, loops unrolled past the instruction
+// cache 27 %.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             if (__builtin_expect(j == j0 && j > 0, 0)) put();
             // 8-bit: y = log2 of a weight with its row's value scale, block by block of 16; the
             // columns are read twice, 32 at a time, for want of registers.
-            const float4* blocks = scale_s[Q8 ? (seg_tile + tile) % kRawSlots : 0];
+            [[maybe_unused]] const float4* blocks = scale_s[Q8 ? (seg_tile + tile) % kRawSlots : 0];
             float s[Q8 ? 32 : 128];
             auto columns = [&](int c) {  // 32 c ..., masked
               float(&y)[32] = reinterpret_cast<float(&)[32]>(s[Q8 ? 0 : 32 * c]);
@@ -836,9 +847,9 @@ __global__ void __launch_bounds__(kSharedThreads<FMT>, 1)
             if (n == 2) {
               // The codes' slot is free, but not before all loads have returned: one that is
               // still on its way (the products keep shared memory busy) would find the codes of
-              // the next lap, so which lane arrives depends on what they brought.  (Arriving
-              // without that: 654 us for the documents below, and tiles that were torn.  Before
-              // the first piece 703, before the third 684, before the seventh 693.)
+              // the next lap, so which lane arrives depends on what they brought.  (The e4m3
+              // groups of the header, whole call: arriving right behind the loads took 654 us and
+              // tore tiles; here 683, before the first piece 703, before the seventh 693.)
               uint32_t any = 0u;
 #pragma unroll
               for (int e = 0; e < 8; ++e) any |= c[e].x | c[e].y | c[e].z | c[e].w;
